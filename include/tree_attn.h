@@ -310,6 +310,84 @@ tree_attn_status tree_attn_plan_describe_schedule(tree_attn_plan_t plan, char* b
 tree_attn_status tree_attn_plan_get_stats(tree_attn_plan_t plan,
                                           tree_attn_plan_stats* stats);
 
+/* ------------------------------------------------------------------------
+ * Operators of a decode loop whose lengths live on the GPU.
+ *
+ * A plan fixes lengths and pages when it is made.  The calls below take them
+ * from device memory instead, so that one captured CUDA graph serves every
+ * step of a batch: page tables grow on the GPU, new keys and values go to
+ * their slots, the batch attends to a shared prefix and its own tokens, and
+ * the next tokens are drawn.
+ *
+ *   - They hold no state: every buffer is the caller's, on the current
+ *     device, 16-byte aligned where it holds keys, values or queries, 4-byte
+ *     aligned otherwise.  All are asynchronous on `stream`, allocate nothing
+ *     and may be captured.
+ *   - Page pools as in tree_attn_run(), in bf16 or fp16 (tree_attn_dtype).
+ *     A slot is page * 16 + place; page ids are below 2^27.
+ *   - What is wrong with values in device memory cannot be returned by the
+ *     call: it is OR-ed into the caller's status word (int32, may be NULL),
+ *     which stays set until the caller clears it.  No value in device memory
+ *     makes a kernel read or write outside the buffers as described.
+ * ------------------------------------------------------------------------ */
+typedef enum { TA_BF16 = 0, TA_FP16 = 1, TA_FP32 = 2 } tree_attn_dtype;
+
+enum {
+  TREE_ATTN_BATCH_NO_PAGES = 1,   /* fewer free pages than needed            */
+  TREE_ATTN_BATCH_TABLE_FULL = 2, /* a request outgrows its table row, or the
+                                     new tokens the outputs' max_new         */
+  TREE_ATTN_BATCH_BAD_INPUT = 4,  /* a length, offset or count out of range  */
+  TREE_ATTN_BATCH_BAD_SLOT = 8    /* a page id or slot out of range          */
+};
+
+/* Most requests of a batch. */
+#define TREE_ATTN_MAX_REQUESTS 16384
+
+/* Extend (or cut back) every request of a batch, on the GPU: take pages from
+ * a stack of free ones, enter them in the requests' tables, and give each new
+ * token its slot and position.
+ *   lens[n_requests]       tokens held; advanced in place.
+ *   n_new[n_requests]      tokens to add; negative: to take back (at most all).
+ *   block_table            row b (table_stride ints apart, table_width used)
+ *                          lists request b's pages in order; entries past its
+ *                          pages are not read and may hold anything.
+ *   free_pages[free_capacity], n_free[1]
+ *                          the stack: pages are taken from its top (request
+ *                          by request), given-back pages are put on top, the
+ *                          last one lowest: an extension taken back leaves
+ *                          the stack as it was.  Both change in place.
+ *   slots, positions [max_new]  per new token, request by request: its slot,
+ *                          and position_base + its index in the request; -1
+ *                          past the last new token.
+ *   cu_new[n_requests+1]   new tokens before each request (may be NULL).
+ * All or nothing: where pages, table rows or max_new do not suffice, or a
+ * length is out of range, the state stays as it is, every slot and position
+ * is -1, cu_new is all 0, and the status word says why.  A page given back
+ * keeps its (now unused) entry in its table row.
+ * Errors: TA_ERR_INVALID_ARG, TA_ERR_ALIGNMENT, TA_ERR_UNSUPPORTED (more than
+ * TREE_ATTN_MAX_REQUESTS requests, or rows of 2^31 tokens), TA_ERR_CUDA. */
+tree_attn_status tree_attn_extend_tables(int32_t* lens, const int32_t* n_new, int32_t n_requests,
+                                         int32_t* block_table, int64_t table_stride,
+                                         int32_t table_width, int32_t* free_pages,
+                                         int32_t free_capacity, int32_t* n_free, int32_t max_new,
+                                         int32_t position_base, int32_t* slots,
+                                         int32_t* positions, int32_t* cu_new, int32_t* status,
+                                         void* stream);
+
+/* Write new keys and values to their slots, every kv head.
+ *   k_new, v_new   [n_tokens][n_kv_heads][head_dim] of 2-byte elements, tokens
+ *                  k_stride / v_stride elements apart (multiples of 8: a part
+ *                  of a joint projection needs no copy).
+ *   slots          per token; -1 is skipped, and so is a slot outside the
+ *                  pools (which also sets the status word).
+ * Two tokens with one slot leave either's values.  Errors:
+ * TA_ERR_INVALID_ARG, TA_ERR_ALIGNMENT, TA_ERR_UNSUPPORTED, TA_ERR_CUDA. */
+tree_attn_status tree_attn_append_slots(const void* k_new, const void* v_new, int64_t k_stride,
+                                        int64_t v_stride, const int32_t* slots, int32_t n_tokens,
+                                        int32_t n_kv_heads, int32_t head_dim, void* k_pages,
+                                        void* v_pages, int32_t num_pages, int32_t* status,
+                                        void* stream);
+
 /* Release a plan and its device memory (NULL is ignored).  The caller must
  * make sure no run() of the plan is still executing on the GPU. */
 void tree_attn_plan_destroy(tree_attn_plan_t plan);

@@ -19,6 +19,8 @@ from ._abi import (  # noqa: F401
     status_string,
 )
 from .api import Plan, plan, run  # noqa: F401
+from .batch import append_slots, extend_tables  # noqa: F401
 
-__all__ = ["Plan", "plan", "run", "Options", "PlanStats", "TreeAttnError",
+__all__ = ["Plan", "plan", "run", "extend_tables", "append_slots",
+           "Options", "PlanStats", "TreeAttnError",
            "load_library", "status_string", "LIB_PATH"]

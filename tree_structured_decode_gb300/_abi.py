@@ -20,8 +20,11 @@ EXPORTS = (
     "tree_attn_plan_describe", "tree_attn_plan_get_stats", "tree_attn_plan_destroy",
     "tree_attn_status_string", "tree_attn_last_error", "tree_attn_profile_enable",
     "tree_attn_profile_read", "tree_attn_run_static", "tree_attn_append_kv",
-    "tree_attn_plan_describe_schedule",
+    "tree_attn_plan_describe_schedule", "tree_attn_extend_tables", "tree_attn_append_slots",
 )
+MAX_REQUESTS = 16384
+# Bits of the status word of the operators whose lengths live on the GPU.
+BATCH_NO_PAGES, BATCH_TABLE_FULL, BATCH_BAD_INPUT, BATCH_BAD_SLOT = 1, 2, 4, 8
 STATIC_SCRATCH_BYTES = 32 << 20
 
 
@@ -80,12 +83,12 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     global _lib
     if _lib is not None and path is None:
         return _lib
-    p = path or os.environ.get("TREE_ATTN_LIB", LIB_PATH)
-    if not os.path.exists(p):
+    where = path or os.environ.get("TREE_ATTN_LIB", LIB_PATH)
+    if not os.path.exists(where):
         raise ImportError(
-            f"libtreeattn.so not found at {p}: build it with "
+            f"libtreeattn.so not found at {where}: build it with "
             "`python -m tree_structured_decode_gb300.build` (no CPU fallback exists)")
-    lib = ctypes.CDLL(p)
+    lib = ctypes.CDLL(where)
     lib.tree_attn_options_init.argtypes = [ctypes.POINTER(Options)]
     lib.tree_attn_options_init.restype = None
     lib.tree_attn_plan.argtypes = [
@@ -99,6 +102,11 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.tree_attn_run_static.restype = ctypes.c_int
     lib.tree_attn_append_kv.argtypes = [ctypes.c_void_p] * 6
     lib.tree_attn_append_kv.restype = ctypes.c_int
+    p, i, n = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+    lib.tree_attn_extend_tables.argtypes = [p, p, i, p, n, i, p, i, p, i, i, p, p, p, p, p]
+    lib.tree_attn_extend_tables.restype = ctypes.c_int
+    lib.tree_attn_append_slots.argtypes = [p, p, n, n, p, i, i, i, p, p, i, p, p]
+    lib.tree_attn_append_slots.restype = ctypes.c_int
     lib.tree_attn_device_status.argtypes = [ctypes.c_void_p, ctypes.c_void_p, _I32P]
     lib.tree_attn_device_status.restype = ctypes.c_int
     lib.tree_attn_profile_enable.argtypes = [ctypes.c_void_p, ctypes.c_int32]

@@ -1,0 +1,140 @@
+"""Python entry points of the operators whose lengths live on the GPU:
+page tables and slot maps, the append by slot, attention behind a shared
+prefix, and sampling.
+
+Argument marshalling only: each function checks its tensors, makes the outputs
+that were not given, and calls the C ABI (``include/tree_attn.h``).  The
+functions take no host synchronisation and may be captured in a CUDA graph.
+They run on the tensors' device: on ``stream`` if given, else on that device's
+current stream.
+"""
+from __future__ import annotations
+
+import contextlib
+
+from ._abi import check, load_library
+
+_DTYPE = None
+
+
+def _dtype(t):
+    global _DTYPE
+    if _DTYPE is None:
+        import torch
+
+        _DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    return _DTYPE.get(t.dtype, -1)
+
+
+def _launch_on(device, stream):
+    """(a context that makes `device` and `stream` current, the stream's handle)."""
+    import torch
+
+    index = device.index
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+        if index == torch.cuda.current_device():
+            return contextlib.nullcontext(), handle
+        return torch.cuda.device(index), handle
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(stream), stream.cuda_stream
+
+
+def _ints(name, t, shape, device):
+    import torch
+
+    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor on {device}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} shape {tuple(t.shape)} != {shape}")
+    return t.data_ptr()
+
+
+def _status(t, device):
+    return None if t is None else _ints("status", t, (1,), device)
+
+
+def _table(t, rows, device):
+    import torch
+
+    if t.dtype != torch.int32 or t.device != device or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"block_table must be a 2-d int32 tensor on {device} with contiguous rows")
+    if t.shape[0] != rows:
+        raise ValueError(f"block_table has {t.shape[0]} rows for {rows} requests")
+    stride = t.stride(0) if rows > 1 else t.shape[1]
+    return t.data_ptr(), max(stride, t.shape[1]) if rows <= 1 else stride, t.shape[1]
+
+
+def _cuda(name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _pools(k_pages, v_pages, device):
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if _dtype(t) not in (0, 1) or t.device != device or not t.is_contiguous() or t.dim() != 4:
+            raise ValueError(f"{name} must be a contiguous bf16 or fp16 tensor [pages, kv heads, 16, d] on {device}")
+    if k_pages.dtype != v_pages.dtype or k_pages.shape != v_pages.shape or k_pages.shape[2] != 16:
+        raise ValueError("k_pages and v_pages must have one type and one shape [pages, kv heads, 16, d]")
+
+
+def _rows(name, t, pools):
+    """Token stride of a [tokens, heads, d] tensor whose tokens are whole rows."""
+    if t.dtype != pools.dtype or t.device != pools.device or t.dim() != 3:
+        raise ValueError(f"{name} must be a [tokens, heads, d] tensor of the pools' type and device")
+    n, h, d = t.shape
+    if d != pools.shape[3] or t.stride(2) != 1 or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: each token's [heads, d={pools.shape[3]}] must be contiguous")
+    return t.stride(0) if n > 1 else h * d
+
+
+def extend_tables(lens, n_new, block_table, free_pages, n_free, max_new, position_base=0, status=None, stream=None):
+    """``tree_attn_extend_tables``: add ``n_new`` tokens to every request (negative: take back), in place.
+
+    ``lens``, ``n_new`` int32 ``[requests]``; ``block_table`` int32 ``[requests, width]``; ``free_pages`` int32
+    ``[capacity]`` with ``n_free`` int32 ``[1]`` (a stack); ``max_new`` the number of tokens that the outputs have room
+    for.  Returns ``(slots, positions, cu_new)``, int32 ``[max_new]`` twice and ``[requests + 1]``.  All or nothing: see
+    ``status`` (int32 ``[1]``, OR-ed) and ``include/tree_attn.h``."""
+    import torch
+
+    device = _cuda("lens", lens)
+    b = lens.shape[0]
+    table, stride, width = _table(block_table, b, device)
+    args = (_ints("lens", lens, (b,), device), _ints("n_new", n_new, (b,), device), b, table, stride, width,
+            _ints("free_pages", free_pages, (free_pages.numel(),), device), free_pages.numel(),
+            _ints("n_free", n_free, (1,), device))
+    max_new = int(max_new)
+    if max_new < 0:
+        raise ValueError("max_new is negative")
+    context, handle = _launch_on(device, stream)
+    with context:
+        # one allocation: slots, positions, cu_new
+        out = torch.empty(2 * max_new + b + 1, dtype=torch.int32, device=device)
+        slots, positions, cu = out.split_with_sizes((max_new, max_new, b + 1))
+        at = out.data_ptr()
+        check(load_library().tree_attn_extend_tables(*args, max_new, int(position_base), at, at + 4 * max_new,
+                                                     at + 8 * max_new, _status(status, device), handle),
+              "tree_attn_extend_tables")
+    return slots, positions, cu
+
+
+def append_slots(k_new, v_new, slots, k_pages, v_pages, status=None, stream=None):
+    """``tree_attn_append_slots``: write ``k_new``, ``v_new`` (``[tokens, kv heads, d]``, each token's row contiguous) to
+    ``slots`` (int32 ``[tokens]``, -1: none) of the page pools, in place."""
+    device = _cuda("k_pages", k_pages)
+    _pools(k_pages, v_pages, device)
+    ks, vs = _rows("k_new", k_new, k_pages), _rows("v_new", v_new, k_pages)
+    t, h, d = k_new.shape
+    if k_new.shape != v_new.shape or h != k_pages.shape[1]:
+        raise ValueError(f"k_new {tuple(k_new.shape)} and v_new {tuple(v_new.shape)} must be "
+                         f"[tokens, {k_pages.shape[1]}, {d}]")
+    slots_at = _ints("slots", slots, (t,), device)
+    context, handle = _launch_on(device, stream)
+    with context:
+        check(load_library().tree_attn_append_slots(k_new.data_ptr(), v_new.data_ptr(), ks, vs, slots_at, t, h, d,
+                                                    k_pages.data_ptr(), v_pages.data_ptr(), k_pages.shape[0],
+                                                    _status(status, device), handle), "tree_attn_append_slots")

@@ -1,0 +1,44 @@
+// Parameter blocks and launchers of the operators whose lengths live on the
+// GPU: page tables, append by slot, shared-prefix attention, sampling.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace ta {
+
+// Element types of the C ABI (tree_attn_dtype).
+enum { kBf16 = 0, kFp16 = 1, kFp32 = 2 };
+
+constexpr int kPage = 16;           // tokens per page
+constexpr unsigned kMaxPages = 1u << 27;  // a slot number (page * 16 + place) stays below 2^31
+constexpr int kMaxRequests = 16384; // three scans of a batch stay in shared memory
+
+// Bits of the status word (TREE_ATTN_BATCH_* of the C ABI).
+enum { kBatchNoPages = 1, kBatchTableFull = 2, kBatchBadInput = 4, kBatchBadSlot = 8 };
+
+struct ExtendParams {
+  int32_t* lens;
+  const int32_t* n_new;
+  int32_t* table;
+  long long table_stride;
+  int32_t* free_pages;
+  int32_t* n_free;
+  int32_t *slots, *positions, *cu_new, *status;
+  int n_req, width, free_cap, max_new, position_base;
+};
+cudaError_t launch_extend_tables(const ExtendParams& p, cudaStream_t s);
+
+struct AppendSlotsParams {
+  const uint16_t *k_new, *v_new;
+  long long k_stride, v_stride;  // elements from one token to the next
+  const int32_t* slots;
+  uint16_t *k_pages, *v_pages;
+  int32_t* status;
+  long long n_slots;             // num_pages * 16
+  int n_tokens, hkv, d;
+};
+cudaError_t launch_append_slots(const AppendSlotsParams& p, cudaStream_t s);
+
+}  // namespace ta

@@ -1,0 +1,124 @@
+// C ABI of the operators whose lengths live on the GPU: argument checks and
+// launches.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <string>
+
+#include "../../include/tree_attn.h"
+#include "batch.h"
+#include "plan_state.h"
+
+namespace {
+
+tree_attn_status fail(tree_attn_status s, const std::string& msg) {
+  ta::set_last_error(msg);
+  return s;
+}
+tree_attn_status launched(cudaError_t e, const char* what) {
+  if (e == cudaSuccess) return TA_OK;
+  return fail(TA_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+}
+bool off(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+// Nothing is thrown across the ABI.
+template <class F>
+tree_attn_status guarded(F&& f) {
+  try {
+    ta::set_last_error("");
+    return f();
+  } catch (...) {
+    return TA_ERR_OOM;
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+tree_attn_status tree_attn_extend_tables(int32_t* lens, const int32_t* n_new, int32_t n_requests,
+                                         int32_t* block_table, int64_t table_stride,
+                                         int32_t table_width, int32_t* free_pages,
+                                         int32_t free_capacity, int32_t* n_free, int32_t max_new,
+                                         int32_t position_base, int32_t* slots,
+                                         int32_t* positions, int32_t* cu_new, int32_t* status,
+                                         void* stream) {
+  return guarded([&]() -> tree_attn_status {
+    if (n_requests < 0 || table_width < 0 || free_capacity < 0 || max_new < 0 || position_base < 0)
+      return fail(TA_ERR_INVALID_ARG, "a count, size or the position base is negative");
+    if (!n_free || (n_requests > 0 && (!lens || !n_new)) ||
+        (n_requests > 0 && table_width > 0 && !block_table) || (free_capacity > 0 && !free_pages) ||
+        (max_new > 0 && (!slots || !positions)))
+      return fail(TA_ERR_INVALID_ARG, "a buffer of the tables is NULL");
+    if (table_stride < table_width)
+      return fail(TA_ERR_INVALID_ARG, "table_stride is below table_width");
+    if (n_requests > TREE_ATTN_MAX_REQUESTS)
+      return fail(TA_ERR_UNSUPPORTED, "more than " + std::to_string(TREE_ATTN_MAX_REQUESTS) + " requests");
+    if ((int64_t)table_width * ta::kPage + position_base > INT32_MAX)
+      return fail(TA_ERR_UNSUPPORTED, "table_width * 16 + position_base passes 2^31");
+    if (off(lens, 4) || off(n_new, 4) || off(block_table, 4) || off(free_pages, 4) ||
+        off(n_free, 4) || off(slots, 4) || off(positions, 4) || off(cu_new, 4) || off(status, 4))
+      return fail(TA_ERR_ALIGNMENT, "int32 buffers must be 4-byte aligned");
+    ta::ExtendParams p{};
+    p.lens = lens;
+    p.n_new = n_new;
+    p.table = block_table;
+    p.table_stride = table_stride;
+    p.free_pages = free_pages;
+    p.n_free = n_free;
+    p.slots = slots;
+    p.positions = positions;
+    p.cu_new = cu_new;
+    p.status = status;
+    p.n_req = n_requests;
+    p.width = table_width;
+    p.free_cap = free_capacity;
+    p.max_new = max_new;
+    p.position_base = position_base;
+    return launched(ta::launch_extend_tables(p, static_cast<cudaStream_t>(stream)),
+                    "table extension launch");
+  });
+}
+
+tree_attn_status tree_attn_append_slots(const void* k_new, const void* v_new, int64_t k_stride,
+                                        int64_t v_stride, const int32_t* slots, int32_t n_tokens,
+                                        int32_t n_kv_heads, int32_t head_dim, void* k_pages,
+                                        void* v_pages, int32_t num_pages, int32_t* status,
+                                        void* stream) {
+  return guarded([&]() -> tree_attn_status {
+    if (n_tokens < 0 || n_kv_heads <= 0 || num_pages < 0)
+      return fail(TA_ERR_INVALID_ARG, "n_tokens, n_kv_heads or num_pages out of range");
+    if (head_dim != 64 && head_dim != 128)
+      return fail(TA_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+    if (n_kv_heads > 4096 || (uint32_t)num_pages > ta::kMaxPages)
+      return fail(TA_ERR_UNSUPPORTED, "more than 4096 kv heads or 2^27 pages");
+    if (n_tokens == 0) return TA_OK;
+    if (!k_new || !v_new || !slots || (num_pages > 0 && (!k_pages || !v_pages)))
+      return fail(TA_ERR_INVALID_ARG, "k_new, v_new, slots, k_pages and v_pages must be non-NULL");
+    const int64_t row = (int64_t)n_kv_heads * head_dim;
+    if (n_tokens > 1 && (k_stride < row || v_stride < row))
+      return fail(TA_ERR_INVALID_ARG, "k_stride and v_stride must be at least n_kv_heads * head_dim");
+    if (off(k_new, 16) || off(v_new, 16) || off(k_pages, 16) || off(v_pages, 16) || k_stride % 8 ||
+        v_stride % 8)
+      return fail(TA_ERR_ALIGNMENT,
+                  "k_new, v_new, k_pages and v_pages must be 16-byte aligned, strides multiples of 8 elements");
+    if (off(slots, 4) || off(status, 4))
+      return fail(TA_ERR_ALIGNMENT, "int32 buffers must be 4-byte aligned");
+    ta::AppendSlotsParams p{};
+    p.k_new = static_cast<const uint16_t*>(k_new);
+    p.v_new = static_cast<const uint16_t*>(v_new);
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.slots = slots;
+    p.k_pages = static_cast<uint16_t*>(k_pages);
+    p.v_pages = static_cast<uint16_t*>(v_pages);
+    p.status = status;
+    p.n_slots = (long long)num_pages * ta::kPage;
+    p.n_tokens = n_tokens;
+    p.hkv = n_kv_heads;
+    p.d = head_dim;
+    return launched(ta::launch_append_slots(p, static_cast<cudaStream_t>(stream)), "append launch");
+  });
+}
+
+}  // extern "C"
