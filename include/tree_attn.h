@@ -337,7 +337,9 @@ enum {
   TREE_ATTN_BATCH_TABLE_FULL = 2, /* a request outgrows its table row, or the
                                      new tokens the outputs' max_new         */
   TREE_ATTN_BATCH_BAD_INPUT = 4,  /* a length, offset or count out of range  */
-  TREE_ATTN_BATCH_BAD_SLOT = 8    /* a page id or slot out of range          */
+  TREE_ATTN_BATCH_BAD_SLOT = 8,   /* a page id or slot out of range          */
+  TREE_ATTN_BATCH_TIMEOUT = 16    /* an in-kernel wait ran out (results
+                                     undefined); should never be seen        */
 };
 
 /* Most requests of a batch. */
@@ -387,6 +389,49 @@ tree_attn_status tree_attn_append_slots(const void* k_new, const void* v_new, in
                                         int32_t n_kv_heads, int32_t head_dim, void* k_pages,
                                         void* v_pages, int32_t num_pages, int32_t* status,
                                         void* stream);
+
+/* Attention of a batch whose requests share a prefix, which is computed once
+ * for all of them.
+ *   q              [n_tokens][n_q_heads][head_dim], tokens q_stride elements
+ *                  apart (a multiple of 8); type dtype (bf16 or fp16), as the
+ *                  pools'.
+ *   block_table, lens   the requests' own tokens (behind the prefix), as
+ *                  tree_attn_extend_tables() keeps them; lens counts this
+ *                  step's tokens.
+ *   cu_new[n_requests+1]   request b's queries are tokens [cu_new[b],
+ *                  cu_new[b+1]); NULL: one query each, n_tokens ==
+ *                  n_requests.  The j-th of n queries sees the prefix and the
+ *                  request's first lens[b] - n + j + 1 tokens.
+ *   prefix_pages, prefix_len   pages of the shared prefix (device) and its
+ *                  tokens; 0 for none.
+ *   softmax_scale  <= 0 selects 1/sqrt(head_dim).
+ *   out            [n_tokens][n_q_heads][head_dim], q's type, contiguous.
+ *   lse            fp32 [n_tokens][n_q_heads] (natural log), may be NULL.
+ *   workspace      device memory of tree_attn_prefix_workspace() bytes,
+ *                  256-byte aligned; two runs that may overlap on the GPU need
+ *                  two.
+ * A row that sees no key, and every token at or past cu_new[n_requests], gets
+ * out = 0 and lse = -inf.  Slots past a request's end may hold anything; those
+ * of its tokens that a query does not see (later drafts) must be finite.  A
+ * page id out of range reads as zeros and sets the status word.
+ * Errors: TA_ERR_INVALID_ARG, TA_ERR_ALIGNMENT, TA_ERR_UNSUPPORTED,
+ * TA_ERR_BUFFER_TOO_SMALL (workspace), TA_ERR_CUDA. */
+tree_attn_status tree_attn_prefix_run(const void* q, int64_t q_stride, const void* k_pages,
+                                      const void* v_pages, int32_t num_pages,
+                                      const int32_t* block_table, int64_t table_stride,
+                                      int32_t table_width, const int32_t* lens,
+                                      const int32_t* cu_new, int32_t n_requests, int32_t n_tokens,
+                                      const int32_t* prefix_pages, int32_t prefix_len,
+                                      int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                      int32_t dtype, float softmax_scale, void* out, float* lse,
+                                      int32_t* status, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+
+/* Bytes of workspace that tree_attn_prefix_run() needs for these sizes on the
+ * current device.  Errors: TA_ERR_INVALID_ARG, TA_ERR_UNSUPPORTED. */
+tree_attn_status tree_attn_prefix_workspace(int32_t n_requests, int32_t n_tokens,
+                                            int32_t prefix_len, int32_t n_q_heads,
+                                            int32_t n_kv_heads, int32_t head_dim, size_t* bytes);
 
 /* Release a plan and its device memory (NULL is ignored).  The caller must
  * make sure no run() of the plan is still executing on the GPU. */

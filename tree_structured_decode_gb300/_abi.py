@@ -21,10 +21,11 @@ EXPORTS = (
     "tree_attn_status_string", "tree_attn_last_error", "tree_attn_profile_enable",
     "tree_attn_profile_read", "tree_attn_run_static", "tree_attn_append_kv",
     "tree_attn_plan_describe_schedule", "tree_attn_extend_tables", "tree_attn_append_slots",
+    "tree_attn_prefix_run", "tree_attn_prefix_workspace",
 )
 MAX_REQUESTS = 16384
 # Bits of the status word of the operators whose lengths live on the GPU.
-BATCH_NO_PAGES, BATCH_TABLE_FULL, BATCH_BAD_INPUT, BATCH_BAD_SLOT = 1, 2, 4, 8
+BATCH_NO_PAGES, BATCH_TABLE_FULL, BATCH_BAD_INPUT, BATCH_BAD_SLOT, BATCH_TIMEOUT = 1, 2, 4, 8, 16
 STATIC_SCRATCH_BYTES = 32 << 20
 
 
@@ -107,6 +108,11 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.tree_attn_extend_tables.restype = ctypes.c_int
     lib.tree_attn_append_slots.argtypes = [p, p, n, n, p, i, i, i, p, p, i, p, p]
     lib.tree_attn_append_slots.restype = ctypes.c_int
+    lib.tree_attn_prefix_run.argtypes = [p, n, p, p, i, p, n, i, p, p, i, i, p, i, i, i, i, i, ctypes.c_float,
+                                         p, p, p, p, ctypes.c_size_t, p]
+    lib.tree_attn_prefix_run.restype = ctypes.c_int
+    lib.tree_attn_prefix_workspace.argtypes = [i, i, i, i, i, i, ctypes.POINTER(ctypes.c_size_t)]
+    lib.tree_attn_prefix_workspace.restype = ctypes.c_int
     lib.tree_attn_device_status.argtypes = [ctypes.c_void_p, ctypes.c_void_p, _I32P]
     lib.tree_attn_device_status.restype = ctypes.c_int
     lib.tree_attn_profile_enable.argtypes = [ctypes.c_void_p, ctypes.c_int32]

@@ -11,6 +11,7 @@ current stream.
 from __future__ import annotations
 
 import contextlib
+import ctypes
 
 from ._abi import check, load_library
 
@@ -138,3 +139,49 @@ def append_slots(k_new, v_new, slots, k_pages, v_pages, status=None, stream=None
         check(load_library().tree_attn_append_slots(k_new.data_ptr(), v_new.data_ptr(), ks, vs, slots_at, t, h, d,
                                                     k_pages.data_ptr(), v_pages.data_ptr(), k_pages.shape[0],
                                                     _status(status, device), handle), "tree_attn_append_slots")
+
+
+def prefix_attention(q, k_pages, v_pages, block_table, lens, cu_new=None, prefix_pages=None, prefix_len=0,
+                     softmax_scale=0.0, out=None, lse=None, want_lse=True, status=None, stream=None):
+    """``tree_attn_prefix_run``: every query attends to the shared prefix and to its own request's tokens.
+
+    ``q`` ``[tokens, q heads, d]`` (each token's heads contiguous); ``block_table`` int32 ``[requests, width]`` and
+    ``lens`` int32 ``[requests]`` as ``extend_tables`` keeps them; ``cu_new`` int32 ``[requests + 1]`` (None: one query a
+    request); ``prefix_pages`` int32 with ``prefix_len`` tokens.  Returns ``(out, lse)``: ``out`` of q's type, ``lse``
+    fp32 ``[tokens, q heads]`` (None without ``want_lse``)."""
+    import torch
+
+    device = _cuda("q", q)
+    _pools(k_pages, v_pages, device)
+    q_stride = _rows("q", q, k_pages)
+    t, hq, d = q.shape
+    b = lens.shape[0]
+    table, stride, width = _table(block_table, b, device)
+    lens_at = _ints("lens", lens, (b,), device)
+    cu_at = None if cu_new is None else _ints("cu_new", cu_new, (b + 1,), device)
+    prefix_len, prefix_at = int(prefix_len), None
+    if prefix_pages is not None:
+        prefix_at = _ints("prefix_pages", prefix_pages, (prefix_pages.numel(),), device)
+    if prefix_len > 0 and (prefix_pages is None or prefix_pages.numel() * 16 < prefix_len):
+        raise ValueError(f"prefix_pages holds fewer than prefix_len = {prefix_len} tokens")
+    for name, x, shape, dtype in (("out", out, (t, hq, d), q.dtype), ("lse", lse, (t, hq), torch.float32)):
+        if x is not None and (x.dtype != dtype or x.device != device or not x.is_contiguous() or tuple(x.shape) != shape):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on {device}")
+    lib = load_library()
+    context, handle = _launch_on(device, stream)
+    with context:
+        need = ctypes.c_size_t(0)
+        check(lib.tree_attn_prefix_workspace(b, t, prefix_len, hq, k_pages.shape[1], d, ctypes.byref(need)),
+              "tree_attn_prefix_workspace")
+        # from torch's allocator, call by call: runs on other streams or in other graphs have their own
+        work = torch.empty(need.value, dtype=torch.uint8, device=device)
+        if out is None:
+            out = torch.empty((t, hq, d), dtype=q.dtype, device=device)
+        if lse is None and want_lse:
+            lse = torch.empty((t, hq), dtype=torch.float32, device=device)
+        check(lib.tree_attn_prefix_run(q.data_ptr(), q_stride, k_pages.data_ptr(), v_pages.data_ptr(), k_pages.shape[0],
+                                       table, stride, width, lens_at, cu_at, b, t, prefix_at, prefix_len, hq,
+                                       k_pages.shape[1], d, _dtype(q), float(softmax_scale), out.data_ptr(),
+                                       None if lse is None else lse.data_ptr(), _status(status, device), work.data_ptr(),
+                                       need.value, handle), "tree_attn_prefix_run")
+    return out, lse

@@ -16,7 +16,8 @@ constexpr unsigned kMaxPages = 1u << 27;  // a slot number (page * 16 + place) s
 constexpr int kMaxRequests = 16384; // three scans of a batch stay in shared memory
 
 // Bits of the status word (TREE_ATTN_BATCH_* of the C ABI).
-enum { kBatchNoPages = 1, kBatchTableFull = 2, kBatchBadInput = 4, kBatchBadSlot = 8 };
+enum { kBatchNoPages = 1, kBatchTableFull = 2, kBatchBadInput = 4, kBatchBadSlot = 8,
+       kBatchTimeout = 16 };
 
 struct ExtendParams {
   int32_t* lens;
@@ -40,5 +41,24 @@ struct AppendSlotsParams {
   int n_tokens, hkv, d;
 };
 cudaError_t launch_append_slots(const AppendSlotsParams& p, cudaStream_t s);
+
+struct PrefixParams {
+  const uint16_t* q;
+  long long q_stride;            // elements from one token to the next
+  const uint16_t *k_pages, *v_pages;
+  const int32_t* table;
+  long long table_stride;
+  const int32_t* lens;
+  const int32_t* cu;             // tokens before each request; null: one each
+  const int32_t* prefix_pages;
+  uint16_t* out;                 // [tokens][hq][d], q's type
+  float* lse;                    // [tokens][hq] natural log, or null
+  int32_t* status;
+  int width, prefix_len, n_tokens, n_req, hq, hkv, gqa, d, num_pages, dtype, num_sms;
+  float scale_log2;              // softmax scale * log2(e)
+};
+// Workspace of a run; 0 where there is nothing to do.
+size_t prefix_workspace(const PrefixParams& p);
+cudaError_t launch_prefix_attention(const PrefixParams& p, void* workspace, cudaStream_t s);
 
 }  // namespace ta

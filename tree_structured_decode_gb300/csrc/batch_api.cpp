@@ -2,6 +2,7 @@
 // launches.
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 #include <string>
 
@@ -30,6 +31,39 @@ tree_attn_status guarded(F&& f) {
   } catch (...) {
     return TA_ERR_OOM;
   }
+}
+
+// SMs of the current device (152 where there is none).
+int device_sms() {
+  int device = 0, sms = 0;
+  if (cudaGetDevice(&device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || sms <= 0)
+    return 152;
+  return sms;
+}
+
+// The sizes that decide the workspace of a prefix run.
+tree_attn_status prefix_sizes(int32_t n_requests, int32_t n_tokens, int32_t prefix_len,
+                              int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                              ta::PrefixParams* p) {
+  if (n_requests < 0 || n_tokens < 0 || prefix_len < 0 || n_q_heads <= 0 || n_kv_heads <= 0)
+    return fail(TA_ERR_INVALID_ARG, "a count or length is out of range");
+  if (head_dim != 64 && head_dim != 128) return fail(TA_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (n_q_heads % n_kv_heads || n_q_heads / n_kv_heads > 128)
+    return fail(TA_ERR_UNSUPPORTED, "n_q_heads must be a multiple of n_kv_heads, at most 128 times it");
+  if (n_requests > TREE_ATTN_MAX_REQUESTS)
+    return fail(TA_ERR_UNSUPPORTED, "more than " + std::to_string(TREE_ATTN_MAX_REQUESTS) + " requests");
+  if ((int64_t)n_tokens * n_q_heads > INT32_MAX / 2)
+    return fail(TA_ERR_UNSUPPORTED, "2^30 query rows or more");
+  p->n_req = n_requests;
+  p->n_tokens = n_tokens;
+  p->prefix_len = prefix_len;
+  p->hq = n_q_heads;
+  p->hkv = n_kv_heads;
+  p->gqa = n_q_heads / n_kv_heads;
+  p->d = head_dim;
+  p->num_sms = device_sms();
+  return TA_OK;
 }
 
 }  // namespace
@@ -118,6 +152,83 @@ tree_attn_status tree_attn_append_slots(const void* k_new, const void* v_new, in
     p.hkv = n_kv_heads;
     p.d = head_dim;
     return launched(ta::launch_append_slots(p, static_cast<cudaStream_t>(stream)), "append launch");
+  });
+}
+
+tree_attn_status tree_attn_prefix_run(const void* q, int64_t q_stride, const void* k_pages,
+                                      const void* v_pages, int32_t num_pages,
+                                      const int32_t* block_table, int64_t table_stride,
+                                      int32_t table_width, const int32_t* lens,
+                                      const int32_t* cu_new, int32_t n_requests, int32_t n_tokens,
+                                      const int32_t* prefix_pages, int32_t prefix_len,
+                                      int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                      int32_t dtype, float softmax_scale, void* out, float* lse,
+                                      int32_t* status, void* workspace, size_t workspace_bytes,
+                                      void* stream) {
+  return guarded([&]() -> tree_attn_status {
+    ta::PrefixParams p{};
+    const tree_attn_status st =
+        prefix_sizes(n_requests, n_tokens, prefix_len, n_q_heads, n_kv_heads, head_dim, &p);
+    if (st != TA_OK) return st;
+    if (dtype != TA_BF16 && dtype != TA_FP16)
+      return fail(TA_ERR_UNSUPPORTED, "queries and pages must be bf16 or fp16");
+    if (table_width < 0 || (n_requests > 1 && table_stride < table_width))
+      return fail(TA_ERR_INVALID_ARG, "table_width is negative or table_stride below it");
+    if ((int64_t)table_width * ta::kPage > INT32_MAX || (uint32_t)num_pages > ta::kMaxPages)
+      return fail(TA_ERR_UNSUPPORTED, "rows of 2^31 tokens or more, or num_pages out of range");
+    if (!cu_new && n_tokens != n_requests)
+      return fail(TA_ERR_INVALID_ARG, "without cu_new there is one query a request: n_tokens must be n_requests");
+    if (n_tokens == 0) return TA_OK;
+    if (!q || !out || !k_pages || !v_pages || num_pages == 0 ||
+        (n_requests > 0 && (!lens || (table_width > 0 && !block_table))) ||
+        (prefix_len > 0 && !prefix_pages))
+      return fail(TA_ERR_INVALID_ARG, "q, out, the pools, lens, block_table and prefix_pages must be non-NULL");
+    if (n_tokens > 1 && q_stride < (int64_t)n_q_heads * head_dim)
+      return fail(TA_ERR_INVALID_ARG, "q_stride must be at least n_q_heads * head_dim");
+    if (off(q, 16) || off(k_pages, 16) || off(v_pages, 16) || off(out, 16) || q_stride % 8)
+      return fail(TA_ERR_ALIGNMENT,
+                  "q, out and the pools must be 16-byte aligned, q_stride a multiple of 8 elements");
+    if (off(block_table, 4) || off(lens, 4) || off(cu_new, 4) || off(prefix_pages, 4) ||
+        off(lse, 4) || off(status, 4))
+      return fail(TA_ERR_ALIGNMENT, "int32 and fp32 buffers must be 4-byte aligned");
+    const size_t need = ta::prefix_workspace(p);
+    if (workspace_bytes < need)
+      return fail(TA_ERR_BUFFER_TOO_SMALL, "the workspace needs " + std::to_string(need) + " bytes");
+    if (!workspace || off(workspace, 256))
+      return fail(workspace ? TA_ERR_ALIGNMENT : TA_ERR_INVALID_ARG,
+                  "the workspace must be non-NULL and 256-byte aligned");
+    p.q = static_cast<const uint16_t*>(q);
+    p.q_stride = q_stride;
+    p.k_pages = static_cast<const uint16_t*>(k_pages);
+    p.v_pages = static_cast<const uint16_t*>(v_pages);
+    p.num_pages = num_pages;
+    p.table = block_table;
+    p.table_stride = table_stride;
+    p.width = table_width;
+    p.lens = lens;
+    p.cu = cu_new;
+    p.prefix_pages = prefix_pages;
+    p.out = static_cast<uint16_t*>(out);
+    p.lse = lse;
+    p.status = status;
+    p.dtype = dtype;
+    p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.f / std::sqrt((float)head_dim)) * 1.4426950408889634f;
+    return launched(ta::launch_prefix_attention(p, workspace, static_cast<cudaStream_t>(stream)),
+                    "prefix attention launch");
+  });
+}
+
+tree_attn_status tree_attn_prefix_workspace(int32_t n_requests, int32_t n_tokens,
+                                            int32_t prefix_len, int32_t n_q_heads,
+                                            int32_t n_kv_heads, int32_t head_dim, size_t* bytes) {
+  return guarded([&]() -> tree_attn_status {
+    if (!bytes) return fail(TA_ERR_INVALID_ARG, "bytes is NULL");
+    ta::PrefixParams p{};
+    const tree_attn_status st =
+        prefix_sizes(n_requests, n_tokens, prefix_len, n_q_heads, n_kv_heads, head_dim, &p);
+    if (st != TA_OK) return st;
+    *bytes = ta::prefix_workspace(p);
+    return TA_OK;
   });
 }
 

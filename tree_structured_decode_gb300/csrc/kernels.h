@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "planner.h"
@@ -79,6 +80,9 @@ struct MergeParams {
 };
 constexpr int64_t kMergeEarlyRows = 16384;
 
+// Tensor map of a page pool (see its definition).
+cudaError_t make_page_map(CUtensorMap* m, const void* base, int d, int hkv, int num_pages,
+                          bool whole_page_head);
 // Launch the persistent grouped partial-attention kernel (TMA + tcgen05 /
 // CUDA cores), one CTA per schedule entry.  kv_evict: the plan's K/V mostly
 // streams once (HostPlan::kv_evict); its copies then carry L2 policies.

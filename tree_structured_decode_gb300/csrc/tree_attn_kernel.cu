@@ -1312,6 +1312,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+}  // namespace
+
 // Page pool [pages][hkv][16][d] bf16 as a 4-D tensor (d, slot, head, page)
 // whose box is one 64-column half of a page-head; or, for whole_page_head
 // with d = 128, a 5-D tensor (64 columns, slot, column half, head, page) whose
@@ -1342,6 +1344,8 @@ cudaError_t make_page_map(CUtensorMap* m, const void* base, int d, int hkv, int 
   }
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
+
+namespace {
 
 template <int D, bool kEvict>
 cudaError_t launch_d(const AttnParams& p, int grid, int num_pages, cudaStream_t s) {
