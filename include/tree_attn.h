@@ -433,6 +433,39 @@ tree_attn_status tree_attn_prefix_workspace(int32_t n_requests, int32_t n_tokens
                                             int32_t prefix_len, int32_t n_q_heads,
                                             int32_t n_kv_heads, int32_t head_dim, size_t* bytes);
 
+/* Draw tokens from rows of logits with given random numbers.
+ *   logits         [n_rows][vocab] bf16, fp16 or fp32 (dtype), rows `stride`
+ *                  elements apart.
+ *   u              fp32 [n_rows][draws] in [0, 1): each gives one token of its
+ *                  row, independently (several: branches of one node).
+ *   temperature, top_k, top_p, min_p   per row [n_rows] in device memory, or,
+ *                  where the pointer is NULL, the value ..._all for every row.
+ *   tokens         int32 [n_rows][draws].
+ *   logprobs       fp32 [n_rows][draws]: ln of the token's probability among
+ *                  the kept ones; may be NULL.
+ * With w_i = exp((l_i - max) / temperature) and the order of falling logits
+ * (equal ones by index), the kept tokens are the first top_k of the order;
+ * of those the shortest part from its start whose weight is at least top_p of
+ * theirs; of those the ones with w_i >= min_p.  At least one is kept.  The
+ * token is the first kept one, by index, at which the running sum of weights
+ * passes u times the total.
+ *   - temperature not above 0: the largest logit (the first of equal ones).
+ *     top_k <= 0 or >= vocab, top_p >= 1 (or NaN), min_p <= 0 (or NaN): off.
+ *   - Weights are whole multiples of 2^-42 of the largest, summed exactly:
+ *     results do not depend on the GPU's timing.
+ *   - -inf is never drawn; a row with a NaN, or with nothing above -inf, gives
+ *     token -1 and logprob NaN.  +inf shares the row among its like.
+ *   - u below 0 (or NaN) counts as 0, 1 and above as the last kept token.
+ * Errors: TA_ERR_INVALID_ARG, TA_ERR_ALIGNMENT, TA_ERR_UNSUPPORTED (vocab
+ * above TREE_ATTN_MAX_VOCAB), TA_ERR_CUDA. */
+#define TREE_ATTN_MAX_VOCAB 262144
+tree_attn_status tree_attn_sample(const void* logits, int64_t stride, int32_t dtype,
+                                  int32_t n_rows, int32_t vocab, const float* u, int32_t draws,
+                                  const float* temperature, float temperature_all,
+                                  const int32_t* top_k, int32_t top_k_all, const float* top_p,
+                                  float top_p_all, const float* min_p, float min_p_all,
+                                  int32_t* tokens, float* logprobs, void* stream);
+
 /* Release a plan and its device memory (NULL is ignored).  The caller must
  * make sure no run() of the plan is still executing on the GPU. */
 void tree_attn_plan_destroy(tree_attn_plan_t plan);

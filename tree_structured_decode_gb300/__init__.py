@@ -19,8 +19,8 @@ from ._abi import (  # noqa: F401
     status_string,
 )
 from .api import Plan, plan, run  # noqa: F401
-from .batch import append_slots, extend_tables, prefix_attention  # noqa: F401
+from .batch import append_slots, extend_tables, prefix_attention, sample  # noqa: F401
 
-__all__ = ["Plan", "plan", "run", "extend_tables", "append_slots", "prefix_attention",
+__all__ = ["Plan", "plan", "run", "extend_tables", "append_slots", "prefix_attention", "sample",
            "Options", "PlanStats", "TreeAttnError",
            "load_library", "status_string", "LIB_PATH"]

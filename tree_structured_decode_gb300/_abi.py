@@ -22,8 +22,10 @@ EXPORTS = (
     "tree_attn_profile_read", "tree_attn_run_static", "tree_attn_append_kv",
     "tree_attn_plan_describe_schedule", "tree_attn_extend_tables", "tree_attn_append_slots",
     "tree_attn_prefix_run", "tree_attn_prefix_workspace",
+    "tree_attn_sample",
 )
 MAX_REQUESTS = 16384
+MAX_VOCAB = 262144
 # Bits of the status word of the operators whose lengths live on the GPU.
 BATCH_NO_PAGES, BATCH_TABLE_FULL, BATCH_BAD_INPUT, BATCH_BAD_SLOT, BATCH_TIMEOUT = 1, 2, 4, 8, 16
 STATIC_SCRATCH_BYTES = 32 << 20
@@ -113,6 +115,9 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.tree_attn_prefix_run.restype = ctypes.c_int
     lib.tree_attn_prefix_workspace.argtypes = [i, i, i, i, i, i, ctypes.POINTER(ctypes.c_size_t)]
     lib.tree_attn_prefix_workspace.restype = ctypes.c_int
+    f = ctypes.c_float
+    lib.tree_attn_sample.argtypes = [p, n, i, i, i, p, i, p, f, p, i, p, f, p, f, p, p, p]
+    lib.tree_attn_sample.restype = ctypes.c_int
     lib.tree_attn_device_status.argtypes = [ctypes.c_void_p, ctypes.c_void_p, _I32P]
     lib.tree_attn_device_status.restype = ctypes.c_int
     lib.tree_attn_profile_enable.argtypes = [ctypes.c_void_p, ctypes.c_int32]

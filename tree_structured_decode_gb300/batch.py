@@ -185,3 +185,40 @@ def prefix_attention(q, k_pages, v_pages, block_table, lens, cu_new=None, prefix
                                        None if lse is None else lse.data_ptr(), _status(status, device), work.data_ptr(),
                                        need.value, handle), "tree_attn_prefix_run")
     return out, lse
+
+
+def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=None):
+    """``tree_attn_sample``: draw tokens from rows of logits with given random numbers.
+
+    ``logits`` ``[rows, vocab]`` bf16, fp16 or fp32 (rows may lie apart); ``u`` fp32 in [0, 1), ``[rows]`` or ``[rows,
+    draws]``: each number gives one token of its row.  ``temperature``, ``top_k``, ``top_p``, ``min_p``: one number for all
+    rows, or a tensor ``[rows]`` (fp32; int32 for ``top_k``); None switches a filter off.  Returns ``(tokens, logprobs)``,
+    int32 and fp32, shaped as ``u``; see ``include/tree_attn.h`` for the order of the filters and for rows that hold
+    nothing to draw."""
+    import torch
+
+    device = _cuda("logits", logits)
+    code = _dtype(logits)
+    if code < 0 or logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be a bf16, fp16 or fp32 tensor [rows, vocab] with contiguous rows")
+    rows, vocab = logits.shape
+    if u.dtype != torch.float32 or u.device != device or not u.is_contiguous() or u.dim() not in (1, 2) or u.shape[0] != rows:
+        raise ValueError(f"u must be a contiguous fp32 tensor [{rows}] or [{rows}, draws] on {device}")
+    draws = u.shape[1] if u.dim() == 2 else 1
+    args = []
+    for name, x, off, kind in (("temperature", temperature, 1.0, torch.float32), ("top_k", top_k, 0, torch.int32),
+                               ("top_p", top_p, 1.0, torch.float32), ("min_p", min_p, 0.0, torch.float32)):
+        if isinstance(x, torch.Tensor):
+            if x.dtype != kind or x.device != device or not x.is_contiguous() or x.dim() != 1 or x.shape[0] != rows:
+                raise ValueError(f"{name} must be a number or a contiguous {kind} tensor [{rows}] on {device}")
+            args += [x.data_ptr(), off]
+        else:
+            args += [None, off if x is None else type(off)(x)]
+    context, handle = _launch_on(device, stream)
+    with context:
+        tokens = torch.empty(u.shape, dtype=torch.int32, device=device)
+        logprobs = torch.empty(u.shape, dtype=torch.float32, device=device)
+        check(load_library().tree_attn_sample(logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, code, rows, vocab,
+                                              u.data_ptr(), draws, *args, tokens.data_ptr(), logprobs.data_ptr(), handle),
+              "tree_attn_sample")
+    return tokens, logprobs

@@ -61,4 +61,22 @@ struct PrefixParams {
 size_t prefix_workspace(const PrefixParams& p);
 cudaError_t launch_prefix_attention(const PrefixParams& p, void* workspace, cudaStream_t s);
 
+constexpr int kMaxVocab = 262144;  // eight CTAs' shared memory
+struct SampleParams {
+  const void* logits;            // [rows][vocab], rows `stride` elements apart
+  long long stride;
+  int dtype, rows, vocab, draws;
+  const float* u;                // [rows][draws]
+  // per row, or one value for all where the pointer is null
+  const float *temperature, *top_p, *min_p;
+  const int32_t* top_k;
+  float temperature_all, top_p_all, min_p_all;
+  int top_k_all;
+  int32_t* tokens;               // [rows][draws]
+  float* logprobs;               // [rows][draws] or null
+  int num_sms;
+  int slice;                     // logits of a CTA (set by the launch)
+};
+cudaError_t launch_sample(const SampleParams& p, cudaStream_t s);
+
 }  // namespace ta

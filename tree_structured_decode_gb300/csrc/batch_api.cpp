@@ -232,4 +232,48 @@ tree_attn_status tree_attn_prefix_workspace(int32_t n_requests, int32_t n_tokens
   });
 }
 
+tree_attn_status tree_attn_sample(const void* logits, int64_t stride, int32_t dtype,
+                                  int32_t n_rows, int32_t vocab, const float* u, int32_t draws,
+                                  const float* temperature, float temperature_all,
+                                  const int32_t* top_k, int32_t top_k_all, const float* top_p,
+                                  float top_p_all, const float* min_p, float min_p_all,
+                                  int32_t* tokens, float* logprobs, void* stream) {
+  return guarded([&]() -> tree_attn_status {
+    if (n_rows < 0 || draws < 0 || vocab <= 0)
+      return fail(TA_ERR_INVALID_ARG, "n_rows, draws or vocab out of range");
+    if (dtype != TA_BF16 && dtype != TA_FP16 && dtype != TA_FP32)
+      return fail(TA_ERR_UNSUPPORTED, "logits must be bf16, fp16 or fp32");
+    if (vocab > TREE_ATTN_MAX_VOCAB)
+      return fail(TA_ERR_UNSUPPORTED, "vocab is above " + std::to_string(TREE_ATTN_MAX_VOCAB));
+    if (n_rows > INT32_MAX / 8) return fail(TA_ERR_UNSUPPORTED, "2^28 rows or more");
+    if (n_rows == 0 || draws == 0) return TA_OK;
+    if (!logits || !u || !tokens)
+      return fail(TA_ERR_INVALID_ARG, "logits, u and tokens must be non-NULL");
+    if (n_rows > 1 && stride < vocab) return fail(TA_ERR_INVALID_ARG, "stride is below vocab");
+    if (off(logits, dtype == TA_FP32 ? 4 : 2) || off(u, 4) || off(temperature, 4) ||
+        off(top_k, 4) || off(top_p, 4) || off(min_p, 4) || off(tokens, 4) || off(logprobs, 4))
+      return fail(TA_ERR_ALIGNMENT, "a buffer is not aligned to its elements");
+    ta::SampleParams p{};
+    p.logits = logits;
+    p.stride = stride;
+    p.dtype = dtype;
+    p.rows = n_rows;
+    p.vocab = vocab;
+    p.draws = draws;
+    p.u = u;
+    p.temperature = temperature;
+    p.temperature_all = temperature_all;
+    p.top_k = top_k;
+    p.top_k_all = top_k_all;
+    p.top_p = top_p;
+    p.top_p_all = top_p_all;
+    p.min_p = min_p;
+    p.min_p_all = min_p_all;
+    p.tokens = tokens;
+    p.logprobs = logprobs;
+    p.num_sms = device_sms();
+    return launched(ta::launch_sample(p, static_cast<cudaStream_t>(stream)), "sampling launch");
+  });
+}
+
 }  // extern "C"
