@@ -16,11 +16,13 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <cstring>
 
 #include "batch.h"
 #include "kernels.h"
+#include "prefix_attn.h"
 #include "ptx.cuh"
 
 namespace ta {
@@ -32,34 +34,8 @@ constexpr int kMinPages = 4;    // shortest run of a warp
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr long long kWaitLimitNs = 2000000000ll;
 
-// What the kernels know of a request, checked: its first token and row count
-// lie in the batch, its pages in the table.
-struct Request {
-  long long p0;  // pages in the line before it
-  int len, n, tok0, np;
-};
-
-// One line of segments: the requests' own tokens, or the prefix as a request
-// of its own whose rows are all tokens'.
-struct Line {
-  Request* req;
-  long long* sizes;   // [0] pages in the line, [1] a warp's run
-  float* piece_o;     // [2 * warps][kRows][d]
-  float2* piece_ml;   // [2 * warps][kRows]: {m, l}
-  float* row_o;       // [tokens * hq][d]: segments in one run
-  float2* row_ml;
-  const int32_t* table;
-  long long table_stride;
-  int n_req, width, causal;
-};
-
-struct Args {
-  PrefixParams p;
-  Line line[2];  // own tokens, prefix
-};
-
-__device__ __forceinline__ int tiles_of(const Request& r, int gqa) {
-  return (r.n * gqa + kRows - 1) / kRows;
+__device__ __forceinline__ int tiles_of(const Request& r, int gqa, int tile_rows = kRows) {
+  return (r.n * gqa + tile_rows - 1) / tile_rows;
 }
 
 // Last i in [0, n) with key(i) <= x, 32 probes a step (key ascending, key(0) <= x).
@@ -134,16 +110,6 @@ __global__ void __launch_bounds__(1024) prefix_schedule_kernel(const Args a) {
     const long long total = s_warp[31];
     a.line[0].sizes[0] = total;
     a.line[0].sizes[1] = max((total + nw - 1) / nw, (long long)kMinPages);
-    Request r;
-    r.p0 = 0;
-    r.len = p.prefix_len;
-    r.n = p.n_tokens;
-    r.tok0 = 0;
-    r.np = (p.prefix_len + kPage - 1) / kPage;
-    a.line[1].req[0] = r;
-    const long long all = work(r);
-    a.line[1].sizes[0] = all;
-    a.line[1].sizes[1] = max((all + nw - 1) / nw, (long long)kMinPages);
   }
 }
 
@@ -217,7 +183,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   }
   __syncwarp();
 
-  const long long total = L.sizes[0], run = L.sizes[1];
+  const long long total = L.steps(), run = L.length();
   const int w = warp * gridDim.x + blockIdx.x;
   const long long x0 = min((long long)w * run, total);
   const int count = (int)(min(x0 + run, total) - x0);
@@ -236,12 +202,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       int lo = 0, hi = L.n_req;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (__ldcg(&L.req[mid].p0) <= x)
+        if (L.req[mid].p0 <= x)
           lo = mid;
         else
           hi = mid;
       }
-      const Request q = L.req[lo];
+      const Request q = L.request(lo);
       const long long in = x - q.p0;
       const long long seg = in / q.np;
       const int tiles = tiles_of(q, p.gqa);
@@ -295,7 +261,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       head = __shfl_sync(0xffffffffu, cur.head, at);
       tile = __shfl_sync(0xffffffffu, cur.tile, at);
       pg0 = pg;
-      const Request r = L.req[b];
+      const Request r = L.request(b);
       len = r.len;
       tok0 = r.tok0;
       rows = min(kRows, r.n * p.gqa - tile * kRows);
@@ -456,17 +422,17 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const Args a) {
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       const Line& L = a.line[which];
-      const Request r = which ? L.req[0] : own;
+      const Request r = which ? L.one : own;
       if (r.np == 0) continue;
       const int in = (tok - r.tok0) * p.gqa + h % p.gqa;
-      const long long seg = (long long)(h / p.gqa) * tiles_of(r, p.gqa) + in / kRows;
-      const long long first = r.p0 + seg * r.np, run = L.sizes[1];
+      const long long seg = (long long)(h / p.gqa) * tiles_of(r, p.gqa, L.tile_rows) + in / L.tile_rows;
+      const long long first = r.p0 + seg * r.np, run = L.length();
       const long long w0 = first / run, w1 = (first + r.np - 1) / run;
       if (w0 == w1) {
         fold(L.row_o + row * D, L.row_ml[row]);
       } else {
         for (long long w = w0; w <= w1; ++w) {
-          const long long at = (2 * w + (w == w0 ? 1 : 0)) * kRows + in % kRows;
+          const long long at = (2 * w + (w == w0 ? 1 : 0)) * L.tile_rows + in % L.tile_rows;
           fold(L.piece_o + at * D, L.piece_ml[at]);
         }
       }
@@ -481,6 +447,10 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const Args a) {
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
+// Query rows from which the prefix goes to the tensor-core tiles.
+constexpr int kTileMinRows = 17;
+bool by_tiles(const PrefixParams& p) { return (long long)p.n_tokens * p.gqa >= kTileMinRows; }
+
 // Lays the workspace out; returns its size.
 size_t lay_out(const PrefixParams& p, uint8_t* base, Args* a) {
   size_t at = 0;
@@ -489,21 +459,34 @@ size_t lay_out(const PrefixParams& p, uint8_t* base, Args* a) {
     at += up(bytes);
     return q;
   };
-  const size_t pieces = 2 * (size_t)p.num_sms * kWarps * kRows;
   const size_t rows = (size_t)p.n_tokens * p.hq;
   for (int i = 0; i < 2; ++i) {
     Line& L = a->line[i];
-    if (i == 1 && p.prefix_len == 0) {
-      L = Line{};
-    }
+    L = Line{};
     L.n_req = i ? 1 : p.n_req;
     L.width = i ? 0 : p.width;
     L.causal = i ? 0 : 1;
     L.table = i ? p.prefix_pages : p.table;
     L.table_stride = i ? 0 : p.table_stride;
-    L.req = reinterpret_cast<Request*>(take(sizeof(Request) * (size_t)(L.n_req + 1)));
-    L.sizes = reinterpret_cast<long long*>(take(16));
-    if (i == 1 && p.prefix_len == 0) continue;
+    L.tile_rows = kRows;
+    if (i == 1) {
+      if (p.prefix_len == 0) continue;
+      const bool tiles = by_tiles(p);
+      L.tile_rows = tiles ? kTileRows : kRows;
+      const int step = tiles ? kTileTokens : kPage;
+      L.one.len = p.prefix_len;
+      L.one.n = p.n_tokens;
+      L.one.np = (p.prefix_len + step - 1) / step;
+      const long long blocks = ((long long)p.n_tokens * p.gqa + L.tile_rows - 1) / L.tile_rows;
+      const long long runs = tiles ? p.num_sms : (long long)p.num_sms * kWarps;
+      L.total = blocks * p.hkv * L.one.np;
+      L.run = std::max((L.total + runs - 1) / runs, tiles ? 1ll : (long long)kMinPages);
+    } else {
+      L.req = reinterpret_cast<Request*>(take(sizeof(Request) * (size_t)(L.n_req + 1)));
+      L.sizes = reinterpret_cast<long long*>(take(16));
+    }
+    const size_t pieces =
+        2 * (size_t)p.num_sms * (L.tile_rows == kTileRows ? kTileRows : kWarps * kRows);
     L.piece_o = reinterpret_cast<float*>(take(pieces * p.d * 4));
     L.piece_ml = reinterpret_cast<float2*>(take(pieces * 8));
     L.row_o = reinterpret_cast<float*>(take(rows * p.d * 4));
@@ -523,9 +506,18 @@ cudaError_t run(const Args& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = make_page_map(&mv, p.v_pages, D, p.hkv, p.num_pages, true);
   if (e != cudaSuccess) return e;
+  if (p.prefix_len > 0) {
+    if (by_tiles(p)) {
+      CUtensorMap half;  // one 64-column half of a page-head
+      e = make_page_map(&half, p.k_pages, D, p.hkv, p.num_pages, false);
+      if (e != cudaSuccess) return e;
+      e = launch_prefix_tiles(a, half, mv, s);
+      if (e != cudaSuccess) return e;
+    } else {
+      prefix_line_kernel<D, kHalf><<<p.num_sms, kWarps * 32, Ring<D>::kSmem, s>>>(mk, mv, a, 1);
+    }
+  }
   prefix_schedule_kernel<<<1, 1024, 0, s>>>(a);
-  if (p.prefix_len > 0)
-    prefix_line_kernel<D, kHalf><<<p.num_sms, kWarps * 32, Ring<D>::kSmem, s>>>(mk, mv, a, 1);
   prefix_line_kernel<D, kHalf><<<p.num_sms, kWarps * 32, Ring<D>::kSmem, s>>>(mk, mv, a, 0);
   const long long rows = (long long)p.n_tokens * p.hq;
   prefix_merge_kernel<D, kHalf><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a);
