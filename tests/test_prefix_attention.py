@@ -177,7 +177,7 @@ def test_bad_values_on_the_device_are_said_and_stay_in_bounds():
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
         attend(c, status=status)
         assert status.item() == bit
-    for cu in ([0, 5, 2], [-1, 1, 2], [0, 1, 3], [2, 1, 0]):
+    for cu in ([0, 5, 2], [-1, 1, 2], [0, 1, 3], [2, 1, 0], [0, 2, 1], [0, 2, -9]):
         c = to_gpu(s)
         c["cu"] = torch.tensor(cu, dtype=torch.int32, device="cuda")
         status = torch.zeros(1, dtype=torch.int32, device="cuda")

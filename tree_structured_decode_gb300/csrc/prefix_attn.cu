@@ -28,15 +28,9 @@
 namespace ta {
 namespace {
 
-constexpr int kRows = 16;       // query rows of a tile (the M of mma.m16n8k16)
-constexpr int kWarps = 8;       // per CTA, each on its own
-constexpr int kMinPages = 4;    // shortest run of a warp
+constexpr float kGrowLog2 = 8.f;  // the running maximum is raised when a score passes it by 2^8
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr long long kWaitLimitNs = 2000000000ll;
-
-__device__ __forceinline__ int tiles_of(const Request& r, int gqa, int tile_rows = kRows) {
-  return (r.n * gqa + tile_rows - 1) / tile_rows;
-}
 
 // Last i in [0, n) with key(i) <= x, 32 probes a step (key ascending, key(0) <= x).
 template <class Key>
@@ -52,65 +46,12 @@ __device__ __forceinline__ int find_warp(int n, long long x, int lane, Key key) 
   return lo;
 }
 
-// ------------------------------------------------------------- schedule
-// One block: checks lengths and offsets, sums up the line of own pages.
+// Batches without a prefix kernel that does it on the side, or with many
+// requests.
 __global__ void __launch_bounds__(1024) prefix_schedule_kernel(const Args a) {
-  const PrefixParams& p = a.p;
   __shared__ long long s_warp[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.n_req + 1023) / 1024;
-  const int b0 = min(tid * per, p.n_req), b1 = min(b0 + per, p.n_req);
-  int bad = 0;
-  auto request = [&](int b) {
-    Request r;
-    int len = p.lens[b], first = b, last = b + 1;
-    if (p.cu) first = p.cu[b], last = p.cu[b + 1];
-    if (len < 0 || len > p.width * kPage || first < 0 || last < first || last > p.n_tokens)
-      bad |= kBatchBadInput;
-    r.len = min(max(len, 0), p.width * kPage);
-    r.tok0 = min(max(first, 0), p.n_tokens);
-    r.n = min(max(last, r.tok0), p.n_tokens) - r.tok0;
-    r.np = (r.len + kPage - 1) / kPage;
-    r.p0 = 0;
-    return r;
-  };
-  auto work = [&](const Request& r) {
-    return (long long)tiles_of(r, p.gqa) * r.np * p.hkv;
-  };
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += work(request(b));
-  long long v = mine;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, v, off);
-    if (lane >= off) v += o;
-  }
-  if (lane == 31) s_warp[warp] = v;
-  __syncthreads();
-  if (warp == 0) {
-    long long w = s_warp[lane];
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, w, off);
-      if (lane >= off) w += o;
-    }
-    s_warp[lane] = w;
-  }
-  __syncthreads();
-  long long at = v - mine + (warp > 0 ? s_warp[warp - 1] : 0);
-  for (int b = b0; b < b1; ++b) {
-    Request r = request(b);
-    r.p0 = at;
-    a.line[0].req[b] = r;
-    at += work(r);
-  }
-  if (bad && p.status) atomicOr(p.status, bad);
-  if (tid == 0) {
-    const long long nw = (long long)p.num_sms * kWarps;
-    const long long total = s_warp[31];
-    a.line[0].sizes[0] = total;
-    a.line[0].sizes[1] = max((total + nw - 1) / nw, (long long)kMinPages);
-  }
+  asm volatile("griddepcontrol.launch_dependents;");
+  schedule_own(a, threadIdx.x, 1024, 0, s_warp);
 }
 
 // ------------------------------------------------------------- attention
@@ -148,25 +89,47 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return ptx::pack_bf16(lo, hi);
 }
 
+// The transpose of an 8 x 8 matrix of 16-bit values held two a lane.
+__device__ __forceinline__ uint32_t turn(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
 // A page-head in shared memory: [64-column half][16 tokens][128 B], 128-byte swizzle.
 __device__ __forceinline__ uint32_t page_at(uint32_t base, int row, int chunk) {
   return base + (chunk >> 3) * 2048 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
 }
 
+constexpr int kMaxPlaces = 2048;  // requests whose places are searched in shared memory
+
+// 12 warps an SM hide one another's latencies; each has two pages (four at d =
+// 64) in flight or in use.
+constexpr int kLineWarps = 12;
 template <int D>
 struct Ring {
+  static constexpr int kWarps = kLineWarps;
   static constexpr int kHead = kPage * D * 2;           // bytes of a page-head
-  static constexpr int kStages = D == 128 ? 3 : 6;      // K and V of one page each
+  static constexpr int kStages = 2 * (128 / D);  // K and V of one page each
   static constexpr int kBytes = kWarps * kStages * 2 * kHead;
-  static constexpr int kSmem = kBytes + kWarps * kStages * 8;
+  // barriers, the schedule's sum, requests' places in the line
+  static constexpr int kSum = kBytes + kWarps * kStages * 8;
+  static constexpr int kPlaces = kSum + 16;
+  static constexpr int kSmem = kPlaces + kMaxPlaces * 8;
+  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 
+// NT: tiles of 8 query rows.
 // Each warp streams its run of pages through its own ring of shared-memory
-// stages (K and V of one page, by TMA) and never waits for another warp.
-// S = Q K^T and O += P V on mma.m16n8k16 with 16 tokens a page; the kernel is
-// bound by reading K and V once, where the query rows of a request are few.
-template <int D, bool kHalf>
-__global__ void __launch_bounds__(kWarps * 32, 1)
+// stages (K and V of one page, by TMA) and never waits for another warp.  Query
+// rows are the N of mma.m16n8k16, a page's 16 tokens its M and then its K:
+//   S^T = K Q^T (16 x 8 NT),  O^T += V^T P^T (d x 8 NT),
+// with P^T turned by movmatrix.  (Rows as M want 16 of them: twice the products
+// and accumulators for the eight or fewer rows of one query.)  The running
+// maximum grows only when a score passes it by 2^8, so most pages need no
+// reduction across lanes.  Bound by reading K and V once.
+template <int D, bool kHalf, int NT>
+__global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
     prefix_line_kernel(const __grid_constant__ CUtensorMap tmk,
                        const __grid_constant__ CUtensorMap tmv, const Args a, const int which) {
   using R = Ring<D>;
@@ -177,13 +140,33 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   const int g = lane >> 2, t = lane & 3;
   const uint32_t ring = ptx::smem_u32(smem_raw) + warp * R::kStages * 2 * R::kHead;
   const uint32_t bars = ptx::smem_u32(smem_raw) + R::kBytes + warp * R::kStages * 8;
+  if (ptx::smem_u32(smem_raw) & 1023) {  // the swizzled pages need it
+    if (threadIdx.x == 0 && p.status) atomicOr(p.status, kBatchTimeout);
+    return;
+  }
   if (lane == 0) {
     for (int s = 0; s < R::kStages; ++s) ptx::mbar_init(bars + 8 * s, 1);
     ptx::fence_mbar_init();
   }
   __syncwarp();
+  // the next kernel may set itself up while this one runs
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (which == 0) {
+    // the schedule and the prefix's pieces are the kernels' before this one
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+  } else if (a.side_schedule && blockIdx.x == gridDim.x - 1 && warp == R::kWarps - 1) {
+    schedule_own(a, lane, 32, 1, reinterpret_cast<long long*>(smem_raw + R::kSum));
+  }
 
-  const long long total = L.steps(), run = L.length();
+  long long* places = reinterpret_cast<long long*>(smem_raw + R::kPlaces);
+  const bool near = which == 0 && L.n_req <= kMaxPlaces;
+  if (near) {
+    for (int b = threadIdx.x; b < L.n_req; b += R::kWarps * 32) places[b] = L.req[b].p0;
+    __syncthreads();
+  }
+  const Cuts cuts = which ? prefix_cuts(a) : own_cuts(a);
+  const long long total = cuts.total, run = cuts.run;
+  auto request = [&](int b) { return which ? cuts.one : L.req[b]; };
   const int w = warp * gridDim.x + blockIdx.x;
   const long long x0 = min((long long)w * run, total);
   const int count = (int)(min(x0 + run, total) - x0);
@@ -202,18 +185,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       int lo = 0, hi = L.n_req;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (L.req[mid].p0 <= x)
+        if ((near ? places[mid] : L.req[mid].p0) <= x)
           lo = mid;
         else
           hi = mid;
       }
-      const Request q = L.request(lo);
+      const Request q = request(lo);
       const long long in = x - q.p0;
-      const long long seg = in / q.np;
-      const int tiles = tiles_of(q, p.gqa);
+      const long long seg = quotient(in, q.np);
+      const int tiles = tiles_of(q, p.gqa, L.tile_rows);
       r.b = lo;
-      r.head = (int)(seg / tiles);
-      r.tile = (int)(seg % tiles);
+      r.head = (int)quotient(seg, tiles);
+      r.tile = (int)(seg - (long long)r.head * tiles);
       r.pg = (int)(in - seg * q.np);
       r.np = q.np;
       r.page = L.table[(long long)lo * L.table_stride + r.pg];
@@ -245,10 +228,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     if (i < count) copy(i, page, head);
   }
 
-  uint32_t qf[D / 16][4];
-  float o[D / 8][4];
-  float m[2], l[2];
-  int vis[2], len = 0, b = 0, head = 0, tile = 0, pg0 = 0, rows = 0, tok0 = 0;
+  uint32_t qf[D / 16][NT][2];
+  float o[D / 16][NT][4];
+  float m[NT][2], l[NT][2];  // rows 8 nt + 2 t + e
+  int vis[NT][2], len = 0, b = 0, head = 0, tile = 0, pg0 = 0, rows = 0, tok0 = 0;
   for (int i = 0; i < count; ++i) {
     const int at = i & 31;
     if (i > 0 && at == 0) {
@@ -261,29 +244,33 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       head = __shfl_sync(0xffffffffu, cur.head, at);
       tile = __shfl_sync(0xffffffffu, cur.tile, at);
       pg0 = pg;
-      const Request r = L.request(b);
+      const Request r = request(b);
       len = r.len;
       tok0 = r.tok0;
-      rows = min(kRows, r.n * p.gqa - tile * kRows);
+      rows = min(8 * NT, r.n * p.gqa - tile * 8 * NT);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = tile * kRows + g + 8 * e;
-        const bool there = g + 8 * e < rows;
-        const int j = row / p.gqa;
-        vis[e] = !there ? 0 : L.causal ? max(r.len - r.n + j + 1, 0) : r.len;
-        const uint16_t* src = p.q + (tok0 + j) * p.q_stride + (head * p.gqa + row % p.gqa) * D + 2 * t;
+      for (int n = 0; n < NT; ++n) {
+        const int row = tile * 8 * NT + 8 * n + g;
+        const bool there = 8 * n + g < rows;
+        const uint16_t* src =
+            p.q + (tok0 + row / p.gqa) * p.q_stride + (head * p.gqa + row % p.gqa) * D + 2 * t;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          qf[k][e] = there ? *reinterpret_cast<const uint32_t*>(src + 16 * k) : 0u;
-          qf[k][2 + e] = there ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 8) : 0u;
+          qf[k][n][0] = there ? *reinterpret_cast<const uint32_t*>(src + 16 * k) : 0u;
+          qf[k][n][1] = there ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 8) : 0u;
         }
-        m[e] = -INFINITY;
-        l[e] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r2 = 8 * n + 2 * t + e, j = (tile * 8 * NT + r2) / p.gqa;
+          vis[n][e] = r2 >= rows ? 0 : L.causal ? max(r.len - r.n + j + 1, 0) : r.len;
+          m[n][e] = -INFINITY;
+          l[n][e] = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[k][n][e] = 0.f;
       }
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
     }
     const int s = i % R::kStages;
     const uint32_t kb = ring + s * 2 * R::kHead, vb = kb + R::kHead;
@@ -306,60 +293,85 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         return;
       }
     }
-    float sc[2][4] = {};
+    float sc[NT][4] = {};  // tokens g, g + 8; rows 2 t, 2 t + 1
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       uint32_t kf[4];
-      ldsm4(kf, page_at(kb, (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
-      mma16816<kHalf>(sc[0], qf[k], kf[0], kf[1]);
-      mma16816<kHalf>(sc[1], qf[k], kf[2], kf[3]);
+      ldsm4(kf, page_at(kb, (lane & 7) + (((lane >> 3) & 1) << 3), 2 * k + (lane >> 4)));
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma16816<kHalf>(sc[n], kf, qf[k][n][0], qf[k][n][1]);
     }
     const int tk0 = pg * kPage;
-    if (tk0 + kPage > vis[0] || tk0 + kPage > vis[1]) {
+    bool grow = false;
+    float mx[NT][2];
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (tk0 + n * 8 + 2 * t + (e & 1) >= vis[e >> 1]) sc[n][e] = -INFINITY;
-    }
-    uint32_t pf[4];
-    float alpha[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float mx = fmaxf(fmaxf(sc[0][2 * e], sc[0][2 * e + 1]), fmaxf(sc[1][2 * e], sc[1][2 * e + 1]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float m_new = fmaxf(m[e], mx * p.scale_log2);
-      const float off = m_new == -INFINITY ? 0.f : m_new;  // nothing seen yet
-      alpha[e] = m[e] == m_new ? 1.f : ptx::ex2(m[e] - off);
-      m[e] = m_new;
-      float w4[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) w4[k] = ptx::ex2(fmaf(sc[k >> 1][2 * e + (k & 1)], p.scale_log2, -off));
-      l[e] = fmaf(l[e], alpha[e], (w4[0] + w4[1]) + (w4[2] + w4[3]));
-      pf[e] = pack2<kHalf>(w4[0], w4[1]);
-      pf[2 + e] = pack2<kHalf>(w4[2], w4[3]);
-    }
-    if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n) {
-        o[n][0] *= alpha[0];
-        o[n][1] *= alpha[0];
-        o[n][2] *= alpha[1];
-        o[n][3] *= alpha[1];
+      for (int e = 0; e < 2; ++e) {
+        if (tk0 + kPage > vis[n][e]) {
+          if (tk0 + g >= vis[n][e]) sc[n][e] = -INFINITY;
+          if (tk0 + g + 8 >= vis[n][e]) sc[n][2 + e] = -INFINITY;
+        }
+        mx[n][e] = fmaxf(sc[n][e], sc[n][2 + e]) * p.scale_log2;
+        grow |= mx[n][e] > m[n][e] + kGrowLog2;
       }
     }
-    // V rows past the request's end may hold anything: their weight is 0, but
-    // 0 * NaN is not 0
-    const int left = len - tk0;
-    const uint32_t keep0 = (2 * t < left ? 0xffffu : 0u) | (2 * t + 1 < left ? 0xffff0000u : 0u);
-    const uint32_t keep1 = (2 * t + 8 < left ? 0xffffu : 0u) | (2 * t + 9 < left ? 0xffff0000u : 0u);
+    if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-    for (int n = 0; n < D / 8; n += 2) {
-      uint32_t vf[4];
-      ldsm4t(vf, page_at(vb, (lane & 7) + (((lane >> 3) & 1) << 3), n + (lane >> 4)));
-      mma16816<kHalf>(o[n], pf, vf[0] & keep0, vf[1] & keep1);
-      mma16816<kHalf>(o[n + 1], pf, vf[2] & keep0, vf[3] & keep1);
+      for (int n = 0; n < NT; ++n) {
+        float alpha[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = mx[n][e];
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          x = fmaxf(x, m[n][e]);
+          alpha[e] = x == m[n][e] ? 1.f : ptx::ex2(m[n][e] - x);
+          m[n][e] = x;
+          l[n][e] *= alpha[e];
+        }
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[k][n][e] *= alpha[e & 1];
+      }
+    }
+    uint32_t pf[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float off = m[n][e] == -INFINITY ? 0.f : m[n][e];  // nothing seen yet
+        sc[n][e] = ptx::ex2(fmaf(sc[n][e], p.scale_log2, -off));
+        sc[n][2 + e] = ptx::ex2(fmaf(sc[n][2 + e], p.scale_log2, -off));
+        l[n][e] += sc[n][e] + sc[n][2 + e];
+      }
+      pf[n][0] = turn(pack2<kHalf>(sc[n][0], sc[n][1]));
+      pf[n][1] = turn(pack2<kHalf>(sc[n][2], sc[n][3]));
+    }
+    const int left = len - tk0;
+    if (left >= kPage) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t vf[4];
+        ldsm4t(vf, page_at(vb, (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma16816<kHalf>(o[k][n], vf, pf[n][0], pf[n][1]);
+      }
+    } else {
+      // V rows past the request's end may hold anything: their weight is 0, but
+      // 0 * NaN is not 0
+      const uint32_t keep0 = (2 * t < left ? 0xffffu : 0u) | (2 * t + 1 < left ? 0xffff0000u : 0u);
+      const uint32_t keep1 = (2 * t + 8 < left ? 0xffffu : 0u) | (2 * t + 9 < left ? 0xffff0000u : 0u);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t vf[4];
+        ldsm4t(vf, page_at(vb, (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)));
+        vf[0] &= keep0, vf[1] &= keep0, vf[2] &= keep1, vf[3] &= keep1;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma16816<kHalf>(o[k][n], vf, pf[n][0], pf[n][1]);
+      }
     }
     __syncwarp();  // the stage is read by every lane
     {
@@ -370,25 +382,39 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       if (j < count) copy(j, page, hd);
     }
     if (pg + 1 == np || i + 1 == count) {  // the segment, or this warp's part of it, ends
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-      }
       const bool whole = pg0 == 0 && pg + 1 == np;
-      const long long slot = (2ll * w + (pg0 == 0 ? 1 : 0)) * kRows;
+      const long long slot = (2ll * w + (pg0 == 0 ? 1 : 0)) * (8 * NT);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = g + 8 * e;
-        if (r < rows) {
-          const int row = tile * kRows + r;
-          const long long at_row =
-              (long long)(tok0 + row / p.gqa) * p.hq + head * p.gqa + row % p.gqa;
-          float* dst = whole ? L.row_o + at_row * D : L.piece_o + (slot + r) * D;
+      for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int n = 0; n < D / 8; ++n)
-            *reinterpret_cast<float2*>(dst + 8 * n + 2 * t) = make_float2(o[n][2 * e], o[n][2 * e + 1]);
-          if (t == 0) (whole ? L.row_ml[at_row] : L.piece_ml[slot + r]) = make_float2(m[e], l[e]);
+        for (int e = 0; e < 2; ++e) {
+          float den = l[n][e];
+          den += __shfl_xor_sync(0xffffffffu, den, 4);
+          den += __shfl_xor_sync(0xffffffffu, den, 8);
+          den += __shfl_xor_sync(0xffffffffu, den, 16);
+          const int r = 8 * n + 2 * t + e;
+          if (r >= rows) continue;
+          const int row = tile * 8 * NT + r;
+          const long long at_row = (long long)(tok0 + row / p.gqa) * p.hq + head * p.gqa + row % p.gqa;
+          if (whole && a.join) {  // there is no prefix: the row is done
+            const float inv = den > 0.f ? 1.f / den : den == 0.f ? 0.f : den;
+            uint16_t* dst = p.out + at_row * D + g;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t two = pack2<kHalf>(o[k][n][e] * inv, o[k][n][2 + e] * inv);
+              dst[16 * k] = (uint16_t)two;
+              dst[16 * k + 8] = (uint16_t)(two >> 16);
+            }
+            if (g == 0 && p.lse) p.lse[at_row] = den == 0.f ? -INFINITY : (m[n][e] + log2f(den)) * kLn2;
+          } else {
+            float* dst = (whole ? L.row_o + at_row * D : L.piece_o + (slot + r) * D) + g;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              dst[16 * k] = o[k][n][e];
+              dst[16 * k + 8] = o[k][n][2 + e];
+            }
+            if (g == 0) (whole ? L.row_ml[at_row] : L.piece_ml[slot + r]) = make_float2(m[n][e], den);
+          }
         }
       }
     }
@@ -396,53 +422,100 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 }
 
 // ------------------------------------------------------------- merge
-// A warp a row (token, q head): joins the pieces of both lines.
+// Half a warp a row (token, q head): joins the pieces of both lines, where the
+// line kernel has not.  The pieces' {m, l} are read by 16 lanes at once, their O
+// four at a time: a row of many pieces costs few dependent loads.  Bound by the
+// latency of that chain (request, {m, l}, O); the rows in flight hide it.
 template <int D, bool kHalf>
 __global__ void __launch_bounds__(256) prefix_merge_kernel(const Args a) {
   const PrefixParams& p = a.p;
-  const int lane = threadIdx.x & 31;
-  const long long row = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  if (row >= (long long)p.n_tokens * p.hq) return;
-  constexpr int E = D / 32;
-  const int tok = (int)(row / p.hq), h = (int)(row % p.hq);
-  float M = -INFINITY, den = 0.f, acc[E] = {};
-  auto fold = [&](const float* o, const float2 ml) {
-    if (ml.x == -INFINITY) return;
-    const float m_new = fmaxf(M, ml.x);
-    const float a0 = ptx::ex2(M - m_new), a1 = ptx::ex2(ml.x - m_new);
-    den = den * a0 + ml.y * a1;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * a0 + o[lane * E + e] * a1;
-    M = m_new;
-  };
-  const int b = find_warp(p.n_req, tok, lane, [&](int i) { return (long long)a.line[0].req[i].tok0; });
+  constexpr int E = D / 16;  // columns of a lane
+  const int lane = threadIdx.x & 31, in = lane & 15;
+  const long long pair = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const long long rows = (long long)p.n_tokens * p.hq;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (2 * pair >= rows) return;
+  const long long row = min(2 * pair + (lane >> 4), rows - 1);
+  const int tok = (int)((uint32_t)row / (uint32_t)p.hq), h = (int)((uint32_t)row % (uint32_t)p.hq);
+  int b = tok;
+  if (p.cu) {
+    auto first = [&](int i) { return (long long)a.line[0].req[i].tok0; };
+    b = find_warp(p.n_req, __shfl_sync(0xffffffffu, tok, 0), lane, first);
+    if (__any_sync(0xffffffffu, tok != __shfl_sync(0xffffffffu, tok, 0))) {
+      const int b2 = find_warp(p.n_req, __shfl_sync(0xffffffffu, tok, 31), lane, first);
+      if (lane >= 16) b = b2;
+    }
+  }
   const Request own = a.line[0].req[b];
   const bool there = p.n_req > 0 && tok >= own.tok0 && tok < own.tok0 + own.n;
+  Pieces po{}, pp{};
   if (there) {
+    if (p.prefix_len > 0) {
+      const Cuts cuts = prefix_cuts(a);
+      if (tok < cuts.one.n) pp = pieces_of(a.line[1], cuts.one, cuts.run, p, tok, h);  // else cu is broken
+    }
+    po = pieces_of(a.line[0], own, a.line[0].sizes[1], p, tok, h);
+  }
+  const int n = po.n + pp.n;
+  const bool done = a.join && po.n == 1;  // by the line kernel
+  int most = done ? 0 : n;
+  most = max(most, __shfl_xor_sync(0xffffffffu, most, 16));
+  float M = -INFINITY, den = 0.f, acc[E] = {};
+  for (int k0 = 0; k0 < most; k0 += 16) {
+    const int k = k0 + in;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    const float* src = a.line[0].row_o;  // anything that may be read
+    if (k < po.n)
+      ml = po.ml(k), src = po.o(k, D);
+    else if (k < n)
+      ml = pp.ml(k - po.n), src = pp.o(k - po.n, D);
+    float m_new = ml.x;
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      const Line& L = a.line[which];
-      const Request r = which ? L.one : own;
-      if (r.np == 0) continue;
-      const int in = (tok - r.tok0) * p.gqa + h % p.gqa;
-      const long long seg = (long long)(h / p.gqa) * tiles_of(r, p.gqa, L.tile_rows) + in / L.tile_rows;
-      const long long first = r.p0 + seg * r.np, run = L.length();
-      const long long w0 = first / run, w1 = (first + r.np - 1) / run;
-      if (w0 == w1) {
-        fold(L.row_o + row * D, L.row_ml[row]);
-      } else {
-        for (long long w = w0; w <= w1; ++w) {
-          const long long at = (2 * w + (w == w0 ? 1 : 0)) * L.tile_rows + in % L.tile_rows;
-          fold(L.piece_o + at * D, L.piece_ml[at]);
+    for (int off = 8; off; off >>= 1) m_new = fmaxf(m_new, __shfl_xor_sync(0xffffffffu, m_new, off));
+    m_new = fmaxf(M, m_new);
+    const float base = m_new == -INFINITY ? 0.f : m_new;
+    const float a0 = ptx::ex2(M - base), w = ptx::ex2(ml.x - base);
+    float sum = w * ml.y;
+#pragma unroll
+    for (int off = 8; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    den = den * a0 + sum;
+    M = m_new;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= a0;
+    const int cnt = min(16, n - k0), all = min(16, most - k0);
+    const unsigned long long at = reinterpret_cast<unsigned long long>(src);
+    for (int j = 0; j < all; j += 4) {
+      float4 v[4][E / 4];
+      float wj[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4* s = reinterpret_cast<const float4*>(__shfl_sync(0xffffffffu, at, (lane & 16) + min(j + i, 15)));
+        wj[i] = __shfl_sync(0xffffffffu, w, (lane & 16) + min(j + i, 15));
+#pragma unroll
+        for (int e = 0; e < E / 4; ++e)
+          v[i][e] = j + i < cnt ? __ldcg(s + 16 * e + in) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (j + i >= cnt) wj[i] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E / 4; ++e) {
+          acc[4 * e] = fmaf(v[i][e].x, wj[i], acc[4 * e]);
+          acc[4 * e + 1] = fmaf(v[i][e].y, wj[i], acc[4 * e + 1]);
+          acc[4 * e + 2] = fmaf(v[i][e].z, wj[i], acc[4 * e + 2]);
+          acc[4 * e + 3] = fmaf(v[i][e].w, wj[i], acc[4 * e + 3]);
         }
       }
     }
   }
-  const float inv = den > 0.f ? 1.f / den : 0.f;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + row * D + lane * E);
+  if (done || 2 * pair + (lane >> 4) >= rows) return;
+  const float inv = den > 0.f ? 1.f / den : den == 0.f ? 0.f : den;  // a NaN stays one
 #pragma unroll
-  for (int e = 0; e < E; e += 2) dst[e / 2] = pack2<kHalf>(acc[e] * inv, acc[e + 1] * inv);
-  if (lane == 0 && p.lse) p.lse[row] = den > 0.f ? (M + log2f(den)) * kLn2 : -INFINITY;
+  for (int e = 0; e < E / 4; ++e)
+    *reinterpret_cast<uint2*>(p.out + row * D + 64 * e + 4 * in) =
+        make_uint2(pack2<kHalf>(acc[4 * e] * inv, acc[4 * e + 1] * inv),
+                   pack2<kHalf>(acc[4 * e + 2] * inv, acc[4 * e + 3] * inv));
+  if (in == 0 && p.lse) p.lse[row] = den == 0.f ? -INFINITY : (M + log2f(den)) * kLn2;
 }
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
@@ -450,6 +523,8 @@ size_t up(size_t x) { return (x + 255) / 256 * 256; }
 // Query rows from which the prefix goes to the tensor-core tiles.
 constexpr int kTileMinRows = 17;
 bool by_tiles(const PrefixParams& p) { return (long long)p.n_tokens * p.gqa >= kTileMinRows; }
+
+constexpr int kMaxSideRequests = 2048;
 
 // Lays the workspace out; returns its size.
 size_t lay_out(const PrefixParams& p, uint8_t* base, Args* a) {
@@ -468,60 +543,97 @@ size_t lay_out(const PrefixParams& p, uint8_t* base, Args* a) {
     L.causal = i ? 0 : 1;
     L.table = i ? p.prefix_pages : p.table;
     L.table_stride = i ? 0 : p.table_stride;
-    L.tile_rows = kRows;
+    // query rows of a tile: 8, or 16 where a request has more on average (the
+    // prefix by lines has at most 16).  32 were slower, with the registers they
+    // take: 62 us against 37 at 128 requests of up to four drafts, 16 rows each.
+    const long long queries = i || p.n_req == 0 ? p.n_tokens : (p.n_tokens + p.n_req - 1) / p.n_req;
+    L.tile_rows = queries * p.gqa <= 8 ? 8 : 16;
+    L.step = kPage;
+    L.runs = p.num_sms * kLineWarps;
     if (i == 1) {
       if (p.prefix_len == 0) continue;
-      const bool tiles = by_tiles(p);
-      L.tile_rows = tiles ? kTileRows : kRows;
-      const int step = tiles ? kTileTokens : kPage;
-      L.one.len = p.prefix_len;
-      L.one.n = p.n_tokens;
-      L.one.np = (p.prefix_len + step - 1) / step;
-      const long long blocks = ((long long)p.n_tokens * p.gqa + L.tile_rows - 1) / L.tile_rows;
-      const long long runs = tiles ? p.num_sms : (long long)p.num_sms * kWarps;
-      L.total = blocks * p.hkv * L.one.np;
-      L.run = std::max((L.total + runs - 1) / runs, tiles ? 1ll : (long long)kMinPages);
+      if (by_tiles(p)) L.tile_rows = kTileRows, L.step = kTileTokens, L.runs = p.num_sms;
     } else {
       L.req = reinterpret_cast<Request*>(take(sizeof(Request) * (size_t)(L.n_req + 1)));
       L.sizes = reinterpret_cast<long long*>(take(16));
     }
-    const size_t pieces =
-        2 * (size_t)p.num_sms * (L.tile_rows == kTileRows ? kTileRows : kWarps * kRows);
+    const size_t pieces = 2 * (size_t)L.runs * L.tile_rows;
     L.piece_o = reinterpret_cast<float*>(take(pieces * p.d * 4));
     L.piece_ml = reinterpret_cast<float2*>(take(pieces * 8));
     L.row_o = reinterpret_cast<float*>(take(rows * p.d * 4));
     L.row_ml = reinterpret_cast<float2*>(take(rows * 8));
   }
+  // (Joining a segment with the prefix's pieces as well, in the line kernel's
+  // epilogue, was slower: eight warps an SM wait for those loads, 105 to 168 us
+  // at 512 requests of 64 heads, against 9 us less in the merge.)
+  a->join = p.prefix_len == 0;
+  a->side_schedule = p.prefix_len > 0 && p.n_req <= kMaxSideRequests;
   return at;
+}
+
+template <int D, bool kHalf, int NT>
+cudaError_t launch_line(const Args& a, int which, const CUtensorMap& mk, const CUtensorMap& mv,
+                        cudaStream_t s) {
+  using R = Ring<D>;
+  cudaError_t e = cudaFuncSetAttribute(prefix_line_kernel<D, kHalf, NT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.p.num_sms);
+  cfg.blockDim = dim3(R::kWarps * 32);
+  cfg.dynamicSmemBytes = R::kSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = which == 0 ? 1 : 0;  // the own tokens': set up while the kernel before ends
+  return cudaLaunchKernelEx(&cfg, prefix_line_kernel<D, kHalf, NT>, mk, mv, a, which);
+}
+template <int D, bool kHalf>
+cudaError_t launch_line(const Args& a, int which, const CUtensorMap& mk, const CUtensorMap& mv,
+                        cudaStream_t s) {
+  return a.line[which].tile_rows == 8 ? launch_line<D, kHalf, 1>(a, which, mk, mv, s)
+                                      : launch_line<D, kHalf, 2>(a, which, mk, mv, s);
 }
 
 template <int D, bool kHalf>
 cudaError_t run(const Args& a, cudaStream_t s) {
   const PrefixParams& p = a.p;
-  cudaError_t e = cudaFuncSetAttribute(prefix_line_kernel<D, kHalf>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<D>::kSmem);
-  if (e != cudaSuccess) return e;
   CUtensorMap mk, mv;
-  e = make_page_map(&mk, p.k_pages, D, p.hkv, p.num_pages, true);
+  cudaError_t e = make_page_map(&mk, p.k_pages, D, p.hkv, p.num_pages, true);
   if (e != cudaSuccess) return e;
   e = make_page_map(&mv, p.v_pages, D, p.hkv, p.num_pages, true);
   if (e != cudaSuccess) return e;
+  if (!a.side_schedule) {
+    prefix_schedule_kernel<<<1, 1024, 0, s>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   if (p.prefix_len > 0) {
     if (by_tiles(p)) {
       CUtensorMap half;  // one 64-column half of a page-head
       e = make_page_map(&half, p.k_pages, D, p.hkv, p.num_pages, false);
       if (e != cudaSuccess) return e;
       e = launch_prefix_tiles(a, half, mv, s);
-      if (e != cudaSuccess) return e;
     } else {
-      prefix_line_kernel<D, kHalf><<<p.num_sms, kWarps * 32, Ring<D>::kSmem, s>>>(mk, mv, a, 1);
+      e = launch_line<D, kHalf>(a, 1, mk, mv, s);
     }
+    if (e != cudaSuccess) return e;
   }
-  prefix_schedule_kernel<<<1, 1024, 0, s>>>(a);
-  prefix_line_kernel<D, kHalf><<<p.num_sms, kWarps * 32, Ring<D>::kSmem, s>>>(mk, mv, a, 0);
+  e = launch_line<D, kHalf>(a, 0, mk, mv, s);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
   const long long rows = (long long)p.n_tokens * p.hq;
-  prefix_merge_kernel<D, kHalf><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a);
-  return cudaGetLastError();
+  cfg.gridDim = dim3((unsigned)((rows + 15) / 16));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, kHalf>, a);
 }
 
 }  // namespace

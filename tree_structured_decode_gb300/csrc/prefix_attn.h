@@ -9,6 +9,8 @@
 
 namespace ta {
 
+constexpr int kMinPages = 4;    // shortest run of a warp of the line kernel
+
 // What the kernels know of a request, checked: its first token and row count
 // lie in the batch, its pages in the table.
 struct Request {
@@ -16,32 +18,152 @@ struct Request {
   int len, n, tok0, np;  // tokens held, queries, the first one, steps of a segment
 };
 
+// One division; most are of 32-bit numbers, which takes a third of the time.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 // One line of segments (a tile of query rows of one kv head against one
 // request's keys), cut into equal runs of steps: the requests' own tokens, or
 // the prefix as a request of its own whose rows are all tokens'.
 struct Line {
-  Request* req;       // null: `one`
-  long long* sizes;   // [0] steps in the line, [1] a run; null: `total`, `run`
+  Request* req;       // null: the prefix, see prefix_of()
+  long long* sizes;   // [0] steps in the line, [1] a run
   float* piece_o;     // [2 * runs][tile_rows][d]
   float2* piece_ml;   // [2 * runs][tile_rows]: {m, l}
   float* row_o;       // [tokens * hq][d]: segments in one run
   float2* row_ml;
   const int32_t* table;
   long long table_stride;
-  long long total, run;
-  Request one;
-  int n_req, width, causal, tile_rows;
-
-  __device__ __forceinline__ Request request(int b) const { return req ? req[b] : one; }
-  __device__ __forceinline__ long long steps() const { return sizes ? sizes[0] : total; }
-  __device__ __forceinline__ long long length() const { return sizes ? sizes[1] : run; }
+  int n_req, width, causal, tile_rows, step;  // step: keys
+  int runs;           // warps (or CTAs) that the line is cut for
 };
 
 struct Args {
   PrefixParams p;
   Line line[2];  // own tokens, prefix
+  int side_schedule;  // the prefix kernel checks and sums up the requests on the side
+  int join;           // own segments in one run are final
 };
 
+__device__ __forceinline__ int tiles_of(const Request& r, int gqa, int tile_rows) {
+  return (r.n * gqa + tile_rows - 1) / tile_rows;
+}
+
+// The prefix's line: one request of all queries.  Tokens of no request (the
+// padding of a batch of fixed size) are not counted.
+struct Cuts {
+  Request one;
+  long long total, run;
+};
+__device__ __forceinline__ Cuts prefix_cuts(const Args& a) {
+  const PrefixParams& p = a.p;
+  const Line& L = a.line[1];
+  Cuts c;
+  c.one.p0 = 0;
+  c.one.len = p.prefix_len;
+  c.one.tok0 = 0;
+  c.one.n = p.cu ? min(max(p.cu[p.n_req], 0), p.n_tokens) : p.n_tokens;
+  c.one.np = (p.prefix_len + L.step - 1) / max(L.step, 1);
+  c.total = (long long)tiles_of(c.one, p.gqa, L.tile_rows) * p.hkv * c.one.np;
+  c.run = max(quotient(c.total + L.runs - 1, L.runs), L.step == kPage ? (long long)kMinPages : 1ll);
+  return c;
+}
+__device__ __forceinline__ Cuts own_cuts(const Args& a) {
+  Cuts c;
+  c.one = Request{};
+  c.total = a.line[0].sizes[0];
+  c.run = a.line[0].sizes[1];
+  return c;
+}
+
+// Where a line's pieces of one query row lie: n of them (0: the line has no
+// keys for it), piece k in o(k) and ml(k).
+struct Pieces {
+  const Line* L;
+  long long w0, row;
+  int n, in;
+  __device__ __forceinline__ long long slot(int k) const {
+    return (2 * (w0 + k) + (k == 0 ? 1 : 0)) * L->tile_rows + in;
+  }
+  __device__ __forceinline__ const float* o(int k, int d) const {
+    return n == 1 ? L->row_o + row * d : L->piece_o + slot(k) * d;
+  }
+  __device__ __forceinline__ float2 ml(int k) const {
+    return __ldcg(n == 1 ? L->row_ml + row : L->piece_ml + slot(k));
+  }
+};
+// Pieces of token tok's q head h in line L, whose request there is r.
+__device__ __forceinline__ Pieces pieces_of(const Line& L, const Request& r, long long run,
+                                            const PrefixParams& p, int tok, int h) {
+  Pieces q{&L, 0, (long long)tok * p.hq + h, 0, 0};
+  if (r.np == 0) return q;
+  const int in = (tok - r.tok0) * p.gqa + h % p.gqa;
+  const long long seg = (long long)(h / p.gqa) * tiles_of(r, p.gqa, L.tile_rows) + in / L.tile_rows;
+  const long long first = r.p0 + seg * r.np;
+  q.w0 = quotient(first, run);
+  q.n = (int)(quotient(first + r.np - 1, run) - q.w0) + 1;
+  q.in = in % L.tile_rows;
+  return q;
+}
+
+// Checks lengths and offsets and sums up the line of the requests' own pages:
+// tid of `threads` (a multiple of 32) threads, which meet at named barrier
+// `bar`; s_warp holds a word per warp.
+__device__ inline void schedule_own(const Args& a, int tid, int threads, int bar, long long* s_warp);
+
+
+
+__device__ inline void schedule_own(const Args& a, int tid, int threads, int bar, long long* s_warp) {
+  const PrefixParams& p = a.p;
+  const int lane = tid & 31, warp = tid >> 5;
+  const int per = (p.n_req + threads - 1) / threads;
+  const int b0 = min(tid * per, p.n_req), b1 = min(b0 + per, p.n_req);
+  int bad = 0;
+  auto request = [&](int b) {
+    Request r;
+    int len = p.lens[b], first = b, last = b + 1;
+    if (p.cu) first = p.cu[b], last = p.cu[b + 1];
+    if (len < 0 || len > p.width * kPage || first < 0 || last < first || last > p.n_tokens)
+      bad |= kBatchBadInput;
+    r.len = min(max(len, 0), p.width * kPage);
+    r.tok0 = min(max(first, 0), p.n_tokens);
+    r.n = min(max(last, r.tok0), p.n_tokens) - r.tok0;
+    r.np = (r.len + kPage - 1) / kPage;
+    r.p0 = 0;
+    return r;
+  };
+  auto work = [&](const Request& r) {
+    return (long long)tiles_of(r, p.gqa, a.line[0].tile_rows) * r.np * p.hkv;
+  };
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += work(request(b));
+  long long v = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, v, off);
+    if (lane >= off) v += o;
+  }
+  if (lane == 31) s_warp[warp] = v;
+  asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
+  long long at = v - mine, total = 0;
+  for (int w = 0; w < threads / 32; ++w) {
+    if (w == warp) at += total;
+    total += s_warp[w];
+  }
+  for (int b = b0; b < b1; ++b) {
+    Request r = request(b);
+    r.p0 = at;
+    a.line[0].req[b] = r;
+    at += work(r);
+  }
+  if (bad && p.status) atomicOr(p.status, bad);
+  if (tid == 0) {
+    a.line[0].sizes[0] = total;
+    a.line[0].sizes[1] = max((total + a.line[0].runs - 1) / a.line[0].runs, (long long)kMinPages);
+  }
+}
 
 // Most query rows of a tile of the tensor-core prefix kernel: two of 128.
 constexpr int kTileRows = 256;

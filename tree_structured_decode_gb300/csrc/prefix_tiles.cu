@@ -55,7 +55,7 @@ struct Cfg {
   static constexpr int kOffStage = 2 * kQBytes;
   static constexpr int kOffBar = kOffStage + kStages * kStageBytes;
   static constexpr int kBars = 3 * kStages + 11;
-  static constexpr int kSmem = kOffBar + kBars * 8 + 16;
+  static constexpr int kSmem = kOffBar + kBars * 8 + 8 + 16;  // TMEM address, abort flag, the schedule's two sums
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 
@@ -130,11 +130,11 @@ struct Walk {
     return true;
   }
 };
-__device__ __forceinline__ Walk walk_of(const Line& L, int rows) {
+__device__ __forceinline__ Walk walk_of(const Cuts& cuts, int rows) {
   Walk w;
-  w.x = min((long long)blockIdx.x * L.run, L.total);
-  w.x1 = min(w.x + L.run, L.total);
-  w.n = L.one.np;
+  w.x = min((long long)blockIdx.x * cuts.run, cuts.total);
+  w.x1 = min(w.x + cuts.run, cuts.total);
+  w.n = cuts.one.np;
   w.blocks = (rows + kTileRows - 1) / kTileRows;
   return w;
 }
@@ -142,7 +142,7 @@ __device__ __forceinline__ Walk walk_of(const Line& L, int rows) {
 // ------------------------------------------------------------- copies
 template <int D>
 __device__ void stream_kv(const CUtensorMap* tmk, const CUtensorMap* tmv, const Args& a,
-                          const Cta<D>& c, int rows) {
+                          const Cta<D>& c, const Cuts& cuts, int rows) {
   using C = Cfg<D>;
   const PrefixParams& p = a.p;
   const Line& L = a.line[1];
@@ -156,7 +156,7 @@ __device__ void stream_kv(const CUtensorMap* tmk, const CUtensorMap* tmv, const 
     if (p.status) atomicOr(p.status, kBatchBadSlot);
     return p.num_pages;  // outside the tensor map: read as zeros
   };
-  Walk walk = walk_of(L, rows);
+  Walk walk = walk_of(cuts, rows);
   Segment s;
   uint32_t g = 0;
   uint32_t zeroed = 0;  // phase of each stage's land barrier
@@ -223,15 +223,15 @@ __device__ void stream_kv(const CUtensorMap* tmk, const CUtensorMap* tmv, const 
 
 // ------------------------------------------------------------- products
 template <int D, bool kHalf>
-__device__ void issue_products(const Args& a, const Cta<D>& c, int rows, uint32_t tmem) {
+__device__ void issue_products(const Args& a, const Cta<D>& c, const Cuts& cuts, int rows,
+                               uint32_t tmem) {
   using C = Cfg<D>;
   constexpr uint32_t kType = kHalf ? 0u : (1u << 7) | (1u << 10);
   constexpr uint32_t kDescQK =
       (ptx::idesc_bf16(128, kTileTokens, 0) & ~((1u << 7) | (1u << 10))) | kType;
   constexpr uint32_t kDescPV = (ptx::idesc_bf16(128, D, 1) & ~((1u << 7) | (1u << 10))) | kType;
-  const Line& L = a.line[1];
   const int n_pages = (a.p.prefix_len + kPage - 1) / kPage;
-  Walk walk = walk_of(L, rows);
+  Walk walk = walk_of(cuts, rows);
   Segment s;
   uint32_t g = 0;             // steps before this segment: K is ring entry 2 g, V 2 g + 1
   uint32_t done[2] = {0, 0};  // steps of each tile before this segment
@@ -348,7 +348,8 @@ __device__ __noinline__ void rescale_o(uint32_t o, float alpha) {
 }
 
 template <int D, bool kHalf>
-__device__ void softmax_rows(const Args& a, const Cta<D>& c, int rows, uint32_t tmem, int t) {
+__device__ void softmax_rows(const Args& a, const Cta<D>& c, const Cuts& cuts, int rows,
+                             uint32_t tmem, int t) {
   using C = Cfg<D>;
   const PrefixParams& p = a.p;
   const Line& L = a.line[1];
@@ -356,7 +357,7 @@ __device__ void softmax_rows(const Args& a, const Cta<D>& c, int rows, uint32_t 
   const uint32_t lanes = (uint32_t)(warp * 32) << 16;
   const uint32_t s_tmem = tmem + lanes + t * 128, o_tmem = tmem + lanes + 256 + t * 128;
   const uint32_t q_smem = c.base + t * C::kQBytes;
-  Walk walk = walk_of(L, rows);
+  Walk walk = walk_of(cuts, rows);
   // the walk's next segment that has rows in this tile
   auto next = [&](Segment& s) {
     while (walk.next(s))
@@ -438,7 +439,7 @@ __device__ void softmax_rows(const Args& a, const Cta<D>& c, int rows, uint32_t 
     if (!ok) break;
     ptx::tc_fence_after();
     if (act) {
-      const bool whole = s.j0 == 0 && s.j1 == L.one.np;
+      const bool whole = s.j0 == 0 && s.j1 == cuts.one.np;
       const long long slot = (2ll * blockIdx.x + (s.j0 == 0 ? 1 : 0)) * kTileRows + t * 128 + tid;
       const long long at = (long long)(row / p.gqa) * p.hq + s.head * p.gqa + row % p.gqa;
       float* dst = whole ? L.row_o + at * D : L.piece_o + slot * D;
@@ -479,11 +480,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::kOffBar + C::kBars * 8);
   c.abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffBar + C::kBars * 8 + 4);
   const int warp = threadIdx.x >> 5;
-  const int rows = a.p.n_tokens * a.p.gqa;
+  const Cuts cuts = prefix_cuts(a);
+  const int rows = cuts.one.n * a.p.gqa;
   if (c.base & 1023) {  // the swizzled layouts need it
     if (threadIdx.x == 0 && c.status) atomicOr(c.status, kBatchTimeout);
     return;
   }
+  asm volatile("griddepcontrol.launch_dependents;");  // the next kernel waits for this grid's end
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       ptx::mbar_init(c.full(s), 1);
@@ -511,13 +514,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   if (warp < 8) {
     ptx::setmaxnreg_inc<kSoftmaxRegs>();
-    softmax_rows<D, kHalf>(a, c, rows, tmem, warp >> 2);
+    softmax_rows<D, kHalf>(a, c, cuts, rows, tmem, warp >> 2);
   } else {
     ptx::setmaxnreg_dec<kIssueRegs>();
     if (warp == 8)
-      stream_kv<D>(&tmk, &tmv, a, c, rows);
+      stream_kv<D>(&tmk, &tmv, a, c, cuts, rows);
     else if (warp == 9)
-      issue_products<D, kHalf>(a, c, rows, tmem);
+      issue_products<D, kHalf>(a, c, cuts, rows, tmem);
+    else if (blockIdx.x == 0 && a.side_schedule)  // two warps that have nothing else to do
+      schedule_own(a, threadIdx.x - 320, 64, 1, reinterpret_cast<long long*>(smem + C::kOffBar + C::kBars * 8 + 8));
     __syncwarp();
   }
   ptx::tc_fence_before();
@@ -533,8 +538,12 @@ cudaError_t launch(const Args& a, const CUtensorMap& mk, const CUtensorMap& mv, 
   cudaError_t e = cudaFuncSetAttribute(prefix_tile_kernel<D, kHalf>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  const long long grid = (a.line[1].total + a.line[1].run - 1) / a.line[1].run;
-  prefix_tile_kernel<D, kHalf><<<(unsigned)grid, kThreads, Cfg<D>::kSmem, s>>>(mk, mv, a);
+  // as many CTAs as there can be steps
+  const PrefixParams& p = a.p;
+  const long long blocks = ((long long)p.n_tokens * p.gqa + kTileRows - 1) / kTileRows;
+  const long long steps = blocks * p.hkv * ((p.prefix_len + kTileTokens - 1) / kTileTokens);
+  const unsigned grid = (unsigned)(steps < p.num_sms ? steps : p.num_sms);
+  prefix_tile_kernel<D, kHalf><<<grid, kThreads, Cfg<D>::kSmem, s>>>(mk, mv, a);
   return cudaGetLastError();
 }
 
