@@ -422,28 +422,30 @@ __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
 }
 
 // ------------------------------------------------------------- merge
-// Half a warp a row (token, q head): joins the pieces of both lines, where the
-// line kernel has not.  The pieces' {m, l} are read by 16 lanes at once, their O
-// four at a time: a row of many pieces costs few dependent loads.  Bound by the
-// latency of that chain (request, {m, l}, O); the rows in flight hide it.
-template <int D, bool kHalf>
+// Joins a row's (token, q head) pieces of both lines, where the line kernel has
+// not.  Bound by the latency of its chain of loads (request, {m, l}, O), which
+// the rows in flight hide where they are many: half a warp takes one then.  Few
+// rows have many pieces: a block takes one, its half-warps every 16th piece.
+template <int D, bool kHalf, bool kBlock>
 __global__ void __launch_bounds__(256) prefix_merge_kernel(const Args a) {
   const PrefixParams& p = a.p;
   constexpr int E = D / 16;  // columns of a lane
-  const int lane = threadIdx.x & 31, in = lane & 15;
-  const long long pair = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  constexpr int kParts = kBlock ? 16 : 1;
+  const int lane = threadIdx.x & 31, in = lane & 15, half = threadIdx.x >> 4;
   const long long rows = (long long)p.n_tokens * p.hq;
+  const long long want = kBlock ? (long long)blockIdx.x : (long long)blockIdx.x * 16 + half;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (2 * pair >= rows) return;
-  const long long row = min(2 * pair + (lane >> 4), rows - 1);
+  if (!kBlock && want - (half & 1) >= rows) return;  // the whole warp
+  const long long row = min(want, rows - 1);
   const int tok = (int)((uint32_t)row / (uint32_t)p.hq), h = (int)((uint32_t)row % (uint32_t)p.hq);
   int b = tok;
   if (p.cu) {
     auto first = [&](int i) { return (long long)a.line[0].req[i].tok0; };
-    b = find_warp(p.n_req, __shfl_sync(0xffffffffu, tok, 0), lane, first);
-    if (__any_sync(0xffffffffu, tok != __shfl_sync(0xffffffffu, tok, 0))) {
-      const int b2 = find_warp(p.n_req, __shfl_sync(0xffffffffu, tok, 31), lane, first);
-      if (lane >= 16) b = b2;
+    const int tok0 = __shfl_sync(0xffffffffu, tok, 0), tok1 = __shfl_sync(0xffffffffu, tok, 31);
+    b = find_warp(p.n_req, tok0, lane, first);
+    if (tok1 != tok0) {
+      const int b1 = find_warp(p.n_req, tok1, lane, first);
+      if (lane >= 16) b = b1;
     }
   }
   const Request own = a.line[0].req[b];
@@ -461,8 +463,9 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const Args a) {
   int most = done ? 0 : n;
   most = max(most, __shfl_xor_sync(0xffffffffu, most, 16));
   float M = -INFINITY, den = 0.f, acc[E] = {};
-  for (int k0 = 0; k0 < most; k0 += 16) {
-    const int k = k0 + in;
+  for (int k0 = 0; k0 < most; k0 += 16 * kParts) {
+    // this half-warp's pieces are k0 + part + kParts i; lane i reads its {m, l}
+    const int k = k0 + (kBlock ? half : 0) + kParts * in;
     float2 ml = make_float2(-INFINITY, 0.f);
     const float* src = a.line[0].row_o;  // anything that may be read
     if (k < po.n)
@@ -482,8 +485,8 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const Args a) {
     M = m_new;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] *= a0;
-    const int cnt = min(16, n - k0), all = min(16, most - k0);
-    const unsigned long long at = reinterpret_cast<unsigned long long>(src);
+    const int all = min(16, (most - k0 + kParts - 1) / kParts);
+    const unsigned long long at = k < n ? reinterpret_cast<unsigned long long>(src) : 0ull;
     for (int j = 0; j < all; j += 4) {
       float4 v[4][E / 4];
       float wj[4];
@@ -491,13 +494,13 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const Args a) {
       for (int i = 0; i < 4; ++i) {
         const float4* s = reinterpret_cast<const float4*>(__shfl_sync(0xffffffffu, at, (lane & 16) + min(j + i, 15)));
         wj[i] = __shfl_sync(0xffffffffu, w, (lane & 16) + min(j + i, 15));
+        const bool mine = j + i < 16 && s != nullptr;
+        if (!mine) wj[i] = 0.f;
 #pragma unroll
-        for (int e = 0; e < E / 4; ++e)
-          v[i][e] = j + i < cnt ? __ldcg(s + 16 * e + in) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int e = 0; e < E / 4; ++e) v[i][e] = mine ? __ldcg(s + 16 * e + in) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (j + i >= cnt) wj[i] = 0.f;
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int e = 0; e < E / 4; ++e) {
           acc[4 * e] = fmaf(v[i][e].x, wj[i], acc[4 * e]);
@@ -505,17 +508,42 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const Args a) {
           acc[4 * e + 2] = fmaf(v[i][e].z, wj[i], acc[4 * e + 2]);
           acc[4 * e + 3] = fmaf(v[i][e].w, wj[i], acc[4 * e + 3]);
         }
-      }
     }
   }
-  if (done || 2 * pair + (lane >> 4) >= rows) return;
-  const float inv = den > 0.f ? 1.f / den : den == 0.f ? 0.f : den;  // a NaN stays one
+  if constexpr (kBlock) {
+    __shared__ float2 s_ml[16];
+    __shared__ float s_o[16][D];
+    if (in == 0) s_ml[half] = make_float2(M, den);
 #pragma unroll
-  for (int e = 0; e < E / 4; ++e)
-    *reinterpret_cast<uint2*>(p.out + row * D + 64 * e + 4 * in) =
-        make_uint2(pack2<kHalf>(acc[4 * e] * inv, acc[4 * e + 1] * inv),
-                   pack2<kHalf>(acc[4 * e + 2] * inv, acc[4 * e + 3] * inv));
-  if (in == 0 && p.lse) p.lse[row] = den == 0.f ? -INFINITY : (M + log2f(den)) * kLn2;
+    for (int e = 0; e < E; ++e) s_o[half][64 * (e / 4) + 4 * in + e % 4] = acc[e];
+    __syncthreads();
+    if (done || threadIdx.x >= 32) return;
+    M = -INFINITY;
+    for (int k = 0; k < 16; ++k) M = fmaxf(M, s_ml[k].x);
+    const float base = M == -INFINITY ? 0.f : M;
+    den = 0.f;
+    float o[D / 32] = {};
+    for (int k = 0; k < 16; ++k) {
+      const float w = ptx::ex2(s_ml[k].x - base);
+      den += w * s_ml[k].y;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) o[e] = fmaf(w, s_o[k][lane * (D / 32) + e], o[e]);
+    }
+    const float inv = den > 0.f ? 1.f / den : den == 0.f ? 0.f : den;  // a NaN stays one
+#pragma unroll
+    for (int e = 0; e < D / 32; e += 2)
+      *reinterpret_cast<uint32_t*>(p.out + row * D + lane * (D / 32) + e) = pack2<kHalf>(o[e] * inv, o[e + 1] * inv);
+    if (lane == 0 && p.lse) p.lse[row] = den == 0.f ? -INFINITY : (M + log2f(den)) * kLn2;
+  } else {
+    if (done || want >= rows) return;
+    const float inv = den > 0.f ? 1.f / den : den == 0.f ? 0.f : den;
+#pragma unroll
+    for (int e = 0; e < E / 4; ++e)
+      *reinterpret_cast<uint2*>(p.out + row * D + 64 * e + 4 * in) =
+          make_uint2(pack2<kHalf>(acc[4 * e] * inv, acc[4 * e + 1] * inv),
+                     pack2<kHalf>(acc[4 * e + 2] * inv, acc[4 * e + 3] * inv));
+    if (in == 0 && p.lse) p.lse[row] = den == 0.f ? -INFINITY : (M + log2f(den)) * kLn2;
+  }
 }
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
@@ -525,6 +553,8 @@ constexpr int kTileMinRows = 17;
 bool by_tiles(const PrefixParams& p) { return (long long)p.n_tokens * p.gqa >= kTileMinRows; }
 
 constexpr int kMaxSideRequests = 2048;
+// Rows an SM up to which the merge takes a block a row.
+constexpr int kBlockRows = 8;
 
 // Lays the workspace out; returns its size.
 size_t lay_out(const PrefixParams& p, uint8_t* base, Args* a) {
@@ -628,12 +658,14 @@ cudaError_t run(const Args& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   const long long rows = (long long)p.n_tokens * p.hq;
-  cfg.gridDim = dim3((unsigned)((rows + 15) / 16));
+  const bool block = rows <= (long long)kBlockRows * p.num_sms;
+  cfg.gridDim = dim3((unsigned)(block ? rows : (rows + 15) / 16));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, kHalf>, a);
+  return block ? cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, kHalf, true>, a)
+               : cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, kHalf, false>, a);
 }
 
 }  // namespace
