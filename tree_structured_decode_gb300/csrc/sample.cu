@@ -13,9 +13,12 @@
 // read from DRAM once; the passes over them work there, and what the CTAs have
 // to tell one another goes through distributed shared memory.
 //   top-k / top-p   a prefix of the order (logit descending, index ascending).
-//                   Its end is found by histograms: first over the exponent of
-//                   the weight (2048 bins of 1/46 of a power of two), then over
-//                   the float's bits inside that bin until one value is left.
+//                   One histogram over the exponent of the weight (2048 bins of
+//                   1/128 of a power of two, and a second for what is below
+//                   2^-16) gives the bin in which it ends.  A bin of one value
+//                   is done; the values of a small one are compared all with
+//                   all by one CTA; a large one is cut further by the float's
+//                   bits until one value is left.
 //   min-p           a least logit.
 //   draw            per-warp sums in index order, their scan, and one walk
 //                   through the 32-element groups of the warp that holds u S.
@@ -25,6 +28,7 @@
 #include <cuda_fp16.h>
 
 #include <cstdint>
+#include <cstring>
 
 #include "batch.h"
 #include "ptx.cuh"
@@ -38,7 +42,9 @@ typedef unsigned long long u64;
 constexpr int kThreads = 512;
 constexpr int kNumWarps = kThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kMaxSlice = 32768;   // logits of a CTA (128 KB)
+constexpr int kSlice = 16384;      // two CTAs fit an SM: one loads while the other computes
+constexpr int kFew = 256;          // values of a bin that are compared all with all
+constexpr float kNear = 16.f;      // the first histogram's range of exponents
 constexpr int kMaxRanks = 8;
 constexpr u64 kOne = 1ull << 42;   // the weight of the largest logit
 constexpr float kLeast = -44.f;    // below 2^-44 a weight rounds to 0
@@ -79,11 +85,15 @@ __device__ __forceinline__ float of_key(uint32_t k) {
 //   t = (x - max) c
 // is a pair (th, tl): the difference's rounding error is exact (two-sum), the
 // product's too (fma).  2^t = 2^e 2^(j/1024) 2^r with |r| <= 2^-11: the table
-// gives the second factor to 2^-42, 2^r = 1 + q + q^2/2 + q^3/6 with q = r ln 2
-// as a pair; q^4/24 is below 2^-50.
+// gives the second factor as a pair, 2^r = 1 + q + q^2/2 + q^3/6 with q = r ln 2
+// as a pair; q^4/24 is below 2^-50.  The product is rounded to a multiple of
+// 2^-20 by adding 12 (an ulp there is 2^-20) and what is left of it to one of
+// 2^-42 in the same way, so two integers come out of a float's bits without a
+// conversion: 0.67 units off at most over 4 million samples (a half is the
+// rounding), 0.29 in the mean square.
 struct Weights {
   float top, ch, cl;
-  const u64* table;  // shared: 2^(j/1024) in units of 2^-42
+  const float2* table;  // shared: 2^(j/1024) as a pair
 
   // th: the float next to t (monotone in x); the bins go by it
   __device__ __forceinline__ float coarse(float x) const { return x == top ? 0.f : __fmul_rn(x - top, ch); }
@@ -96,30 +106,38 @@ struct Weights {
     tl = fmaf(s, ch, -th) + fmaf(s, cl, err * ch);
   }
 
-  __device__ __forceinline__ u64 operator()(float x) const {
-    if (x == top) return kOne;
+  // The weight is hi 2^22 + lo.  Returns th.
+  __device__ __forceinline__ float parts(float x, int& hi, int& lo) const {
     float th, tl;
     exponent(x, th, tl);
-    if (!(th > kLeast)) return 0;  // also where the exponent is not a number (-inf times 0)
     const float magic = 12582912.f;  // 1.5 * 2^23: the sum's low bits are the rounded integer
     const float fm = fmaf(th, 1024.f, magic);
-    const int n = __float_as_int(fm) - 0x4B400000;
+    const int bits = __float_as_int(fm);
     const float r = fmaf(fm - magic, -1.f / 1024.f, th);  // exact
     const float qh = __fmul_rn(r, kLn2Hi);  // not contracted: its error is added below
     const float ql = fmaf(r, kLn2Hi, -qh) + fmaf(r, kLn2Lo, tl * kLn2Hi);
     const float q = qh + ql;  // tl may be as large as r's last bits
     const float y = fmaf(q * q, fmaf(q, 1.f / 6.f, 0.5f), ql - (q - qh));
-    // q + y in units of 2^-42: whole multiples of 2^-22 first, then the rest
-    const float m1 = 3.f;  // 1.5 * 2^1: an ulp of 2^-22
-    const float a = q + m1;
-    const float m2 = 1.5f / 524288.f;  // 1.5 * 2^-19: an ulp of 2^-42
-    const float b = ((q - (a - m1)) + y) + m2;
-    const long long part = (long long)(__float_as_int(a) - __float_as_int(m1)) * (1 << 20) +
-                           (__float_as_int(b) - __float_as_int(m2));
-    const u64 base = table[n & 1023];
-    const u64 v = base + (u64)((part * (long long)(base >> 11)) >> 31);
-    const int e = -(n >> 10);  // >= 0
-    return e ? (v + (1ull << (e - 1))) >> e : v;
+    const float2 f = table[bits & 1023];
+    const float scale = __int_as_float(0x3F800000 + ((bits << 13) & 0xFF800000));  // 2^e
+    const float p = __fmul_rn(f.x, q);
+    const float low = fmaf(f.y, q, fmaf(f.x, y, fmaf(f.x, q, -p))) + f.y;
+    const float s1 = __fadd_rn(f.x, p);
+    const float e1 = p - (s1 - f.x);
+    const float a = fmaf(s1, scale, 12.f);
+    const float rem = fmaf(s1, scale, -(a - 12.f));
+    const float b = fmaf(e1 + low, scale, rem) + 1.5f / 524288.f;
+    hi = __float_as_int(a) - __float_as_int(12.f);
+    lo = __float_as_int(b) - __float_as_int(1.5f / 524288.f);
+    const bool some = th > kLeast;  // not where the exponent is no number either (-inf times 0)
+    if (!some) hi = lo = 0;
+    if (x == top) hi = 1 << 20, lo = 0, th = 0.f;
+    return th;
+  }
+  __device__ __forceinline__ u64 operator()(float x) const {
+    int hi, lo;
+    parts(x, hi, lo);
+    return (u64)((long long)hi * (1 << 22) + lo);
   }
 };
 
@@ -139,6 +157,14 @@ __device__ __forceinline__ CountWeight scan_warp(CountWeight v, int lane) {
   return v;
 }
 
+// The end of a prefix of the order: every logit above key (weight above), then
+// the first m of those at key, each of weight w.
+struct Cut {
+  uint32_t key;
+  int m;
+  u64 above, w;
+};
+
 // What a CTA shows the others of its cluster.
 struct Shown {
   float top;         // its largest logit, and the first index that has it
@@ -149,14 +175,8 @@ struct Shown {
   int bin, bin_n;
   int ties;          // final pass
   u64 kept;
-};
-
-// The end of a prefix of the order: every logit above key (weight above), then
-// the first m of those at key, each of weight w.
-struct Cut {
-  uint32_t key;
-  int m;
-  u64 above, w;
+  int few;           // values gathered (in the first CTA's list)
+  Cut cut;
 };
 
 template <typename T>
@@ -173,8 +193,9 @@ struct Row {
   const SampleParams& p;
   cg::cluster_group cluster;
   float* x;          // this CTA's logits
-  u64* table;
   uint32_t *hn, *hlo, *hhi;
+  uint32_t* few_key; // [kFew]
+  u64* few_w;        // [kFew]
   Shown* shown;
   CountWeight* warp_sum;  // [32]
   int rank, ranks, v0, size;
@@ -263,24 +284,64 @@ struct Row {
     return true;
   }
 
-  // The shortest prefix of the order that has `target` elements, or weight.
-  __device__ bool select(bool by_weight, u64 target, Cut& cut) {
-    constexpr float kScale = kBins / -kLeast;
+  // The part of the row whose exponent lies in (-to, -from], in the bins.  With
+  // `sum`, also this lane's sum of all weights.
+  __device__ u64 fill(float from, float to, bool sum) {
     clear();
-    for (int i = threadIdx.x; i < size; i += kThreads) {
-      const float th = weight.coarse(x[i]);
-      if (th > kLeast) put(min((int)(-th * kScale), kBins - 1), weight(x[i]));
+    const float scale = kBins / (to - from);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int c0, c1;
+    chunk(warp, c0, c1);
+    int all_hi = 0, all_lo = 0;  // at most 64 of 2^20 and 2^21
+    for (int i = c0 + lane; i < c1; i += 32) {
+      const float v = x[i];
+      if (!sum && !(weight.coarse(v) > -to)) continue;
+      int hi, lo;
+      const float th = weight.parts(v, hi, lo);
+      all_hi += hi;
+      all_lo += lo;
+      if (th > -to && th <= -from)
+        put(min((int)((-th - from) * scale), kBins - 1), (u64)((long long)hi * (1 << 22) + lo));
     }
+    return (u64)((long long)all_hi * (1 << 22) + all_lo);
+  }
+
+  // A warp's share of the CTA's logits.
+  __device__ void chunk(int warp, int& c0, int& c1) const {
+    const int n = ((size + kThreads - 1) / kThreads) * 32;
+    c0 = min(warp * n, size);
+    c1 = min(c0 + n, size);
+  }
+
+  // The shortest prefix of the order that has `target` elements, or weight.
+  // near: the bins hold the part up to kNear; they do again on return, or
+  // near is false.
+  __device__ bool select(bool by_weight, u64 target, Cut& cut, bool& near) {
     CountWeight before{0, 0};
     int bin, bin_n;
-    if (!cross(by_weight, target, before, bin, bin_n)) return false;
+    float from = 0.f, to = kNear;
+    if (!near) fill(from, to, false), near = true;
+    if (!cross(by_weight, target, before, bin, bin_n)) {
+      // below it: what is above are all of the first bins
+      for (int r = 0; r < ranks; ++r) before = before + peer(r).total;
+      from = kNear, to = -kLeast;
+      cluster.sync();
+      fill(from, to, false);
+      near = false;
+      if (!cross(by_weight, target, before, bin, bin_n)) return false;
+    }
     // the values in that bin
+    const float scale = kBins / (to - from);
     uint32_t kmin = 0xffffffffu, kmax = 0;
+    Shown& lead = peer(0);
+    uint32_t* list = cluster.map_shared_rank(few_key, 0);
     for (int i = threadIdx.x; i < size; i += kThreads) {
       const float th = weight.coarse(x[i]);
-      if (th > kLeast && min((int)(-th * kScale), kBins - 1) == bin) {
-        kmin = min(kmin, key_of(x[i]));
-        kmax = max(kmax, key_of(x[i]));
+      if (th > -to && th <= -from && min((int)((-th - from) * scale), kBins - 1) == bin) {
+        const uint32_t k = key_of(x[i]);
+        kmin = min(kmin, k);
+        kmax = max(kmax, k);
+        if (bin_n <= kFew) list[atomicAdd(&lead.few, 1)] = k;
       }
     }
     kmin = __reduce_min_sync(0xffffffffu, kmin);
@@ -296,31 +357,58 @@ struct Row {
       kmin = min(kmin, peer(r).kmin);
       kmax = max(kmax, peer(r).kmax);
     }
-    for (;;) {
+    if (kmin != kmax && bin_n <= kFew) {
+      if (rank == 0) {
+        if ((int)threadIdx.x < bin_n) few_w[threadIdx.x] = weight(of_key(few_key[threadIdx.x]));
+        __syncthreads();
+        if ((int)threadIdx.x < bin_n) {
+          const uint32_t key = few_key[threadIdx.x];
+          CountWeight above = before;
+          int same = 0;
+          for (int j = 0; j < bin_n; ++j) {
+            if (few_key[j] > key) above = above + CountWeight{few_w[j], 1};
+            same += few_key[j] == key;
+          }
+          const u64 w = few_w[threadIdx.x];
+          const u64 lo = by_weight ? above.w : (u64)above.n;
+          const u64 hi = by_weight ? above.w + same * w : (u64)above.n + same;
+          if (lo < target && hi >= target)  // one value: its threads write the same
+            shown->cut = end_at(by_weight, target, key, above, same, w);
+        }
+        if (threadIdx.x == 0) shown->few = 0;
+      }
+      cluster.sync();
+      cut = lead.cut;
+      return true;
+    }
+    if (rank == 0 && threadIdx.x == 0) shown->few = 0;
+    while (kmin != kmax) {
       const uint32_t span = kmax - kmin;
       const int shift = max(0, 32 - __clz(span) - 11);
       clear();
+      near = false;
       for (int i = threadIdx.x; i < size; i += kThreads) {
         const uint32_t k = key_of(x[i]);
         if (k >= kmin && k <= kmax) put((int)((kmax - k) >> shift), weight(x[i]));
       }
       if (!cross(by_weight, target, before, bin, bin_n)) return false;
       kmax -= (uint32_t)bin << shift;
-      if (shift == 0) break;
       const uint32_t width = (1u << shift) - 1;
       kmin = kmax - kmin > width ? kmax - width : kmin;
     }
-    cut.key = kmax;
-    cut.above = before.w;
-    cut.w = weight(of_key(kmax));
-    const u64 need = by_weight ? (target - before.w + cut.w - 1) / cut.w : target - before.n;
-    cut.m = (int)min(need, (u64)bin_n);
+    cut = end_at(by_weight, target, kmax, before, bin_n, weight(of_key(kmax)));
     return true;
+  }
+
+  __device__ static Cut end_at(bool by_weight, u64 target, uint32_t key, const CountWeight& above,
+                               int same, u64 w) {
+    const u64 need = by_weight ? (target - above.w + w - 1) / w : target - (u64)above.n;
+    return {key, (int)min(need, (u64)same), above.w, w};
   }
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Shown s_shown;
   __shared__ CountWeight s_warp[32];
@@ -329,33 +417,68 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
   __shared__ double s_c, s_least;  // log2(e) / T, T ln(min_p)
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  u64* table = reinterpret_cast<u64*>(smem);
+  float2* table = reinterpret_cast<float2*>(smem);
   uint32_t* hist = reinterpret_cast<uint32_t*>(table + 1024);
-  float* x = reinterpret_cast<float*>(hist + 3 * kBins);
+  u64* few_w = reinterpret_cast<u64*>(hist + 3 * kBins);
+  uint32_t* few_key = reinterpret_cast<uint32_t*>(few_w + kFew);
+  float* x = reinterpret_cast<float*>(few_key + kFew);
   const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int row = blockIdx.x / ranks;
   const int v0 = min(rank * p.slice, p.vocab), size = min(p.slice, p.vocab - v0);
-  Row<T> R{p, cluster, x, table, hist, hist + kBins, hist + 2 * kBins, &s_shown, s_warp, rank, ranks, v0, size, {}};
+  Row<T> R{p, cluster, x, hist, hist + kBins, hist + 2 * kBins, few_key, few_w, &s_shown, s_warp, rank, ranks, v0, size, {}};
   const float temperature = p.temperature ? p.temperature[row] : p.temperature_all;
   const float min_p = p.min_p ? p.min_p[row] : p.min_p_all;
   if (tid == 0) {  // 64-bit arithmetic is slow here: once a CTA
     s_bad = 0;
+    s_shown.few = 0;
     s_c = 1.4426950408889634074 / (double)temperature;
     s_least = min_p > 0.f ? (double)temperature * log((double)fminf(min_p, 1.f)) : 0.0;
   }
-  for (int j = tid; j < 1024; j += kThreads)
-    table[j] = (__umul64hi(kCoarse[j >> 5], kFine[j & 31]) + (1ull << 17)) >> 18;  // 2^-60 to 2^-42
+  for (int j = tid; j < 1024; j += kThreads) {
+    const u64 v = __umul64hi(kCoarse[j >> 5], kFine[j & 31]);  // units of 2^-60
+    const float hi = (float)v;
+    table[j] = make_float2(hi * 0x1p-60f, (float)(long long)(v - (u64)hi) * 0x1p-60f);
+  }
 
   // ---- the logits, their largest, and whether one is not a number
   const T* src = reinterpret_cast<const T*>(p.logits) + row * p.stride + v0;
   float top = -INFINITY;
   int first = p.vocab;
   bool nan = false;
-  for (int i = tid; i < size; i += kThreads) {
-    const float v = to_float<T>(src[i]) + 0.f;  // -0 becomes 0: equal logits have equal bits
+  auto take = [&](int i, T y) {
+    const float v = to_float<T>(y) + 0.f;  // -0 becomes 0: equal logits have equal bits
     x[i] = v;
     nan |= v != v;
     if (v > top) top = v, first = v0 + i;
+  };
+  constexpr int kVec = 16 / sizeof(T);
+  int done = 0;
+  if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {  // 16 bytes a load, four in flight
+    done = size / kVec * kVec;
+    for (int i0 = tid * kVec; i0 < done; i0 += 4 * kThreads * kVec) {
+      uint4 raw[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i0 + k * kThreads * kVec < done)
+          raw[k] = __ldg(reinterpret_cast<const uint4*>(src + i0 + k * kThreads * kVec));
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i0 + k * kThreads * kVec < done) {
+          T y[kVec];
+          memcpy(y, &raw[k], 16);
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) take(i0 + k * kThreads * kVec + j, y[j]);
+        }
+    }
+  }
+  for (int i0 = done + tid; i0 < size; i0 += 8 * kThreads) {
+    T y[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (i0 + k * kThreads < size) y[k] = src[i0 + k * kThreads];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (i0 + k * kThreads < size) take(i0 + k * kThreads, y[k]);
   }
 #pragma unroll
   for (int off = 16; off; off >>= 1) {
@@ -408,32 +531,51 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
   auto shorten = [&](const Cut& o) {
     if (o.key > cut.key || (o.key == cut.key && o.m < cut.m)) cut = o;
   };
-  if (top_k > 0 && top_k < p.vocab) {
-    Cut o;
-    if (R.select(false, (u64)top_k, o)) shorten(o);
-  }
-  if (top_p < 1.f) {
-    u64 total = cut.above + (u64)cut.m * cut.w;
-    if (cut.w == 0) {  // no top-k: the whole row's weight
-      u64 sum = 0;
-      for (int i = tid; i < size; i += kThreads) sum += R.weight(x[i]);
-      CountWeight v = scan_warp({sum, 0}, lane);
-      if (lane == 31) s_warp[warp] = v;
+  const bool use_k = top_k > 0 && top_k < p.vocab, use_p = top_p < 1.f;
+  if (use_k || use_p) {
+    // one pass: the bins, and with top-p alone the whole row's weight
+    u64 sum = R.fill(0.f, kNear, !use_k);
+    bool near = true;
+    if (!use_k) {
+#pragma unroll
+      for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      if (lane == 0) s_warp[warp].w = sum;
       __syncthreads();
       if (tid == 0) {
-        for (int w = 0; w < kNumWarps - 1; ++w) v.w = w ? v.w + s_warp[w].w : s_warp[0].w;
-        s_shown.kept = v.w + s_warp[kNumWarps - 1].w;
+        sum = 0;
+        for (int w = 0; w < kNumWarps; ++w) sum += s_warp[w].w;
+        s_shown.kept = sum;
       }
-      cluster.sync();
-      total = 0;
-      for (int r = 0; r < ranks; ++r) total += R.peer(r).kept;
-      cluster.sync();
+      __syncthreads();
     }
-    u64 want = 0;
-    if (lane == 0) want = max((u64)ceil((double)fmaxf(top_p, 0.f) * (double)total), 1ull);
-    want = __shfl_sync(0xffffffffu, want, 0);
+    u64 total = 0;
     Cut o;
-    if (R.select(true, want, o)) shorten(o);
+    if (use_k) {
+      if (R.select(false, (u64)top_k, o, near)) shorten(o), total = o.above + (u64)o.m * o.w;
+    }
+    if (use_p) {
+      cluster.sync();
+      if (use_k && total == 0) {  // fewer than k have a weight: all of it counts
+        sum = R.fill(0.f, kNear, true);
+        near = true;
+#pragma unroll
+        for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        if (lane == 0) s_warp[warp].w = sum;
+        __syncthreads();
+        if (tid == 0) {
+          sum = 0;
+          for (int w = 0; w < kNumWarps; ++w) sum += s_warp[w].w;
+          s_shown.kept = sum;
+        }
+        cluster.sync();
+      }
+      if (total == 0)
+        for (int r = 0; r < ranks; ++r) total += R.peer(r).kept;
+      u64 want = 0;
+      if (lane == 0) want = max((u64)ceil((double)fmaxf(top_p, 0.f) * (double)total), 1ull);
+      want = __shfl_sync(0xffffffffu, want, 0);
+      if (R.select(true, want, o, near)) shorten(o);
+    }
   }
   if (min_p > 0.f && temperature < INFINITY) {
     // w >= min_p * w_max is x >= top + T ln(min_p): the least float that is
@@ -450,15 +592,20 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
   }
 
   // ---- sums of the kept weights, warp by warp in index order
-  const int chunk = ((size + kNumWarps * 32 - 1) / (kNumWarps * 32)) * 32;
-  const int c0 = min(warp * chunk, size), c1 = min(c0 + chunk, size);
-  u64 sum = 0;
-  int ties = 0;
+  int c0, c1;
+  R.chunk(warp, c0, c1);
+  int hi_sum = 0, lo_sum = 0, ties = 0;
   for (int i = c0 + lane; i < c1; i += 32) {
     const uint32_t k = key_of(x[i]);
-    if (k > cut.key) sum += R.weight(x[i]);
+    if (k > cut.key) {
+      int hi, lo;
+      R.weight.parts(x[i], hi, lo);
+      hi_sum += hi;
+      lo_sum += lo;
+    }
     ties += k == cut.key;
   }
+  u64 sum = (u64)((long long)hi_sum * (1 << 22) + lo_sum);
   const float tie_x = of_key(cut.key);
   const u64 w_tie = tie_x == tie_x ? R.weight(tie_x) : 0;
 #pragma unroll
@@ -542,7 +689,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
 template <typename T>
 cudaError_t run(SampleParams p, int ranks, cudaStream_t s) {
   p.slice = ((p.vocab + ranks - 1) / ranks + 31) / 32 * 32;
-  const size_t smem = 1024 * 8 + 3 * kBins * 4 + (size_t)p.slice * 4;
+  const size_t smem = 1024 * 8 + 3 * kBins * 4 + kFew * 12 + (size_t)p.slice * 4;
   cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -565,7 +712,7 @@ cudaError_t run(SampleParams p, int ranks, cudaStream_t s) {
 cudaError_t launch_sample(const SampleParams& p, cudaStream_t s) {
   if (p.rows == 0 || p.draws == 0) return cudaSuccess;
   int ranks = 1;
-  while (ranks < kMaxRanks && (p.vocab + ranks - 1) / ranks > kMaxSlice) ranks *= 2;
+  while (ranks < kMaxRanks && (p.vocab + ranks - 1) / ranks > kSlice) ranks *= 2;
   // few rows: more CTAs a row while SMs are free
   while (ranks < kMaxRanks && (long long)p.rows * ranks * 2 <= p.num_sms && p.vocab / ranks > 2048) ranks *= 2;
   if (p.dtype == kFp32) return run<float>(p, ranks, s);
