@@ -100,7 +100,7 @@ def test_masks_infinities_and_nan():
     x[6] *= 1e30                  # differences beyond the range of exp
     x[7] = torch.finfo(torch.float32).max
     x[7, 1::2] = torch.finfo(torch.float32).min
-    for kw in ({}, dict(top_k=2), dict(top_p=0.7), dict(min_p=0.5), dict(temperature=0.0), dict(temperature=1e-30),
+    for kw in ({}, dict(top_k=2), dict(top_p=0.7), dict(min_p=0.5), dict(temperature=0.0), dict(temperature=1e-30), dict(temperature=1e-45),
                dict(temperature=1e30, top_k=100, top_p=0.9)):
         check(x, numbers(5, 9, 4), **kw)
     tokens, logprobs = ta.sample(x, numbers(5, 9))

@@ -75,7 +75,7 @@ struct SampleParams {
   int32_t* tokens;               // [rows][draws]
   float* logprobs;               // [rows][draws] or null
   int num_sms;
-  int slice;                     // logits of a CTA (set by the launch)
+  int slice, held;               // logits of a CTA, whether in shared memory (set by the launch)
 };
 cudaError_t launch_sample(const SampleParams& p, cudaStream_t s);
 

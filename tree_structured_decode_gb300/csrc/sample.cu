@@ -9,19 +9,22 @@
 // does not depend on the order or the grid, and agrees with 64-bit arithmetic
 // except where u lies within about 2^-42 of a border.
 //
-// A cluster of up to eight CTAs holds a row in shared memory, so that logits are
-// read from DRAM once; the passes over them work there, and what the CTAs have
-// to tell one another goes through distributed shared memory.
-//   top-k / top-p   a prefix of the order (logit descending, index ascending).
-//                   One histogram over the exponent of the weight (2048 bins of
-//                   1/128 of a power of two, and a second for what is below
-//                   2^-16) gives the bin in which it ends.  A bin of one value
-//                   is done; the values of a small one are compared all with
-//                   all by one CTA; a large one is cut further by the float's
-//                   bits until one value is left.
-//   min-p           a least logit.
-//   draw            per-warp sums in index order, their scan, and one walk
-//                   through the 32-element groups of the warp that holds u S.
+// A row belongs to one CTA, or to a cluster of up to eight where rows are few;
+// what the CTAs of a cluster have to tell one another goes through distributed
+// shared memory.  A part that fits lies in shared memory; a larger one is read
+// again, by then from L2.  The passes:
+//   1  the largest logit (and NaNs);
+//   2  with top-k or top-p: the bins, a histogram of counts and weights over the
+//      weight's exponent (2048 bins of 1/128 of a power of two; a second one for
+//      what is below 2^-16 where the first does not suffice), and the row's
+//      weight.  The bin where the kept prefix of the order (logit descending,
+//      index ascending) ends follows by a scan;
+//   3  for each such bin, the sums of what lies above it, segment by segment in
+//      index order, and a list of the bin's values, which one CTA compares all
+//      with all.  (A bin of more values is cut further by the float's bits.)
+// What is kept is then: bits above `key`, or equal and index at most `last`.
+// A draw finds its segment by the segments' running sums and walks through it.
+// Each pass is bound by the ~50 instructions of a weight, not by memory.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -42,12 +45,14 @@ typedef unsigned long long u64;
 constexpr int kThreads = 512;
 constexpr int kNumWarps = kThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kSlice = 16384;      // two CTAs fit an SM: one loads while the other computes
-constexpr int kFew = 256;          // values of a bin that are compared all with all
-constexpr float kNear = 16.f;      // the first histogram's range of exponents
+constexpr int kSegments = 256;     // of a CTA's part, at most
+constexpr int kHeld = 65536;       // bytes of logits held in shared memory: two CTAs fit an SM
+constexpr int kFew = 512;          // values of a bin that are compared all with all (at most the threads of a CTA)
+constexpr float kNear = 11.0903549f;   // the first histogram's range of exponents: 2^-16
+constexpr int kSafe = 1023;            // values of a bin whose two 32-bit sums cannot overflow
 constexpr int kMaxRanks = 8;
 constexpr u64 kOne = 1ull << 42;   // the weight of the largest logit
-constexpr float kLeast = -44.f;    // below 2^-44 a weight rounds to 0
+constexpr float kLeast = -30.498476f;  // below exp(this) = 2^-44 a weight rounds to 0
 
 // 2^(i / 32) and 2^(i / 1024), i = 0..31, in units of 2^-62
 __constant__ u64 kCoarse[32] = {
@@ -70,68 +75,69 @@ __constant__ u64 kFine[32] = {
     0x410c57a1b9fe12f6ull, 0x41179e3d5902e44dull, 0x4122e6cd59676024ull, 0x412e315211e89f86ull,
     0x41397dcbd952c4a6ull, 0x4144cc3b0680fd7aull, 0x41501c9ff05d8654ull, 0x415b6efaede1ac83ull,
 };
-constexpr float kLn2Hi = 0x1.62e4300000000p-1f, kLn2Lo = -0x1.05c6100000000p-29f;  // ln 2 = hi + lo to 2^-50
+// ln 2 / 1024 = hi + lo, hi a multiple of 2^-34 (n hi is exact where it is subtracted)
+constexpr float kStepHi = 0x1.62e43p-11f, kStepLo = -0x1.05c61p-39f;
+constexpr float kSteps = 0x1.715476p+10f;  // 1024 / ln 2
 
-// Order-preserving bits of a float (no NaN, no -0).
+// Order-preserving bits of a float (no NaN); -0 and 0 have the same.
 __device__ __forceinline__ uint32_t key_of(float x) {
-  const uint32_t b = __float_as_uint(x);
+  const uint32_t b = __float_as_uint(x + 0.f);
   return b ^ (b >> 31 ? 0xffffffffu : 0x80000000u);
 }
 __device__ __forceinline__ float of_key(uint32_t k) {
   return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xffffffffu));
 }
 
-// A row's weights.  With c = log2(e) / T as a pair of floats, the exponent
+// A row's weights.  With c = 1 / T as a pair of floats, the exponent
 //   t = (x - max) c
 // is a pair (th, tl): the difference's rounding error is exact (two-sum), the
-// product's too (fma).  2^t = 2^e 2^(j/1024) 2^r with |r| <= 2^-11: the table
-// gives the second factor as a pair, 2^r = 1 + q + q^2/2 + q^3/6 with q = r ln 2
-// as a pair; q^4/24 is below 2^-50.  The product is rounded to a multiple of
-// 2^-20 by adding 12 (an ulp there is 2^-20) and what is left of it to one of
-// 2^-42 in the same way, so two integers come out of a float's bits without a
-// conversion: 0.67 units off at most over 4 million samples (a half is the
-// rounding), 0.29 in the mean square.
+// product's too (fma).  With n the integer next to 1024 t / ln 2,
+//   exp(t) = 2^(n/1024) exp(r),  r = t - n ln2/1024,  |r| <= 2^-11.5:
+// a table gives 2^(j/1024) as a pair, exp(r) = 1 + r + r^2/2 + r^3/6 (r^4/24 is
+// below 2^-50).  The product is rounded to a multiple of 2^-20 by adding 12 (an
+// ulp there is 2^-20) and what is left of it to one of 2^-42 in the same way, so
+// two integers come out of a float's bits without a conversion.  0.67 units off
+// at most over 4 million samples (a half is the rounding), 0.28 in the mean
+// square; 42 instructions.
 struct Weights {
   float top, ch, cl;
   const float2* table;  // shared: 2^(j/1024) as a pair
 
   // th: the float next to t (monotone in x); the bins go by it
-  __device__ __forceinline__ float coarse(float x) const { return x == top ? 0.f : __fmul_rn(x - top, ch); }
+  __device__ __forceinline__ float coarse(float x) const { return __fmul_rn(x - top, ch); }
 
   __device__ __forceinline__ void exponent(float x, float& th, float& tl) const {
     const float s = x - top;
     const float bb = s - x;
     const float err = (x - (s - bb)) + (-top - bb);
     th = __fmul_rn(s, ch);
-    tl = fmaf(s, ch, -th) + fmaf(s, cl, err * ch);
+    tl = fmaf(s, cl, fmaf(err, ch, fmaf(s, ch, -th)));
   }
 
   // The weight is hi 2^22 + lo.  Returns th.
   __device__ __forceinline__ float parts(float x, int& hi, int& lo) const {
     float th, tl;
     exponent(x, th, tl);
-    const float magic = 12582912.f;  // 1.5 * 2^23: the sum's low bits are the rounded integer
-    const float fm = fmaf(th, 1024.f, magic);
+    // 1.5 * 2^23: the sum's low bits are the integer; 127 * 1024: the exponent's bias
+    const float magic = 12582912.f + 127 * 1024;
+    const float fm = fmaf(th, kSteps, magic);
     const int bits = __float_as_int(fm);
-    const float r = fmaf(fm - magic, -1.f / 1024.f, th);  // exact
-    const float qh = __fmul_rn(r, kLn2Hi);  // not contracted: its error is added below
-    const float ql = fmaf(r, kLn2Hi, -qh) + fmaf(r, kLn2Lo, tl * kLn2Hi);
-    const float q = qh + ql;  // tl may be as large as r's last bits
-    const float y = fmaf(q * q, fmaf(q, 1.f / 6.f, 0.5f), ql - (q - qh));
+    const float n = fm - magic;
+    const float r = fmaf(n, -kStepHi, th);  // exact
+    const float rl = fmaf(n, -kStepLo, tl);  // as large as r's last bits, or larger
+    const float q = r + rl;
+    const float y = fmaf(q * q, fmaf(q, 1.f / 6.f, 0.5f), rl - (q - r));
     const float2 f = table[bits & 1023];
-    const float scale = __int_as_float(0x3F800000 + ((bits << 13) & 0xFF800000));  // 2^e
-    const float p = __fmul_rn(f.x, q);
-    const float low = fmaf(f.y, q, fmaf(f.x, y, fmaf(f.x, q, -p))) + f.y;
-    const float s1 = __fadd_rn(f.x, p);
-    const float e1 = p - (s1 - f.x);
+    const float scale = __int_as_float((bits << 13) & 0xFF800000);  // 2^floor(n/1024)
+    const float s1 = fmaf(f.x, q, f.x);
+    const float e1 = fmaf(f.x, q, f.x - s1);
+    const float low = fmaf(f.x, y, fmaf(f.y, q, f.y + e1));
     const float a = fmaf(s1, scale, 12.f);
     const float rem = fmaf(s1, scale, -(a - 12.f));
-    const float b = fmaf(e1 + low, scale, rem) + 1.5f / 524288.f;
-    hi = __float_as_int(a) - __float_as_int(12.f);
-    lo = __float_as_int(b) - __float_as_int(1.5f / 524288.f);
+    const float b = fmaf(low, scale, rem) + 1.5f / 524288.f;
     const bool some = th > kLeast;  // not where the exponent is no number either (-inf times 0)
-    if (!some) hi = lo = 0;
-    if (x == top) hi = 1 << 20, lo = 0, th = 0.f;
+    hi = some ? __float_as_int(a) - __float_as_int(12.f) : 0;
+    lo = some ? __float_as_int(b) - __float_as_int(1.5f / 524288.f) : 0;
     return th;
   }
   __device__ __forceinline__ u64 operator()(float x) const {
@@ -157,26 +163,30 @@ __device__ __forceinline__ CountWeight scan_warp(CountWeight v, int lane) {
   return v;
 }
 
-// The end of a prefix of the order: every logit above key (weight above), then
-// the first m of those at key, each of weight w.
+// The end of a prefix of the order: every logit of bits above key, and those
+// of key itself up to index last.
 struct Cut {
   uint32_t key;
-  int m;
-  u64 above, w;
+  int last;
+  __device__ __forceinline__ bool has(uint32_t k, int index) const {
+    return k > key || (k == key && index <= last);
+  }
 };
 
 // What a CTA shows the others of its cluster.
 struct Shown {
-  float top;         // its largest logit, and the first index that has it
+  float top;         // its largest logit, and (greedy) the first index that has it
   int first, bad;
   uint32_t kmin, kmax;
   CountWeight total; // of the bins that it sums up
   CountWeight before;
   int bin, bin_n;
-  int ties;          // final pass
+  int ties;
   u64 kept;
+  int over;          // a bin of more than kSafe values
   int few;           // values gathered (in the first CTA's list)
   Cut cut;
+  u64 weight;        // of the prefix up to the cut
 };
 
 template <typename T>
@@ -188,40 +198,162 @@ __device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 v) { retu
 template <>
 __device__ __forceinline__ float to_float<__half>(__half v) { return __half2float(v); }
 
+
+constexpr float kMostFinite = 3.402823466e38f;
+
 template <typename T>
 struct Row {
-  const SampleParams& p;
   cg::cluster_group cluster;
-  float* x;          // this CTA's logits
+  const T* global;   // this CTA's part of the row
+  const T* held;     // the same in shared memory, or null
+  bool vector;       // `global` may be read four logits at a time
   uint32_t *hn, *hlo, *hhi;
   uint32_t* few_key; // [kFew]
+  int* few_at;       // [kFew] index
   u64* few_w;        // [kFew]
+  u64* seg_sum;      // [kSegments]
   Shown* shown;
   CountWeight* warp_sum;  // [32]
-  int rank, ranks, v0, size;
+  float* queue;      // [64] this warp's, and the places
+  int* queue_at;
+  bool safe;         // how the bins hold their sums, see put()
+  bool infinite;     // the largest logit is +inf
+  int rank, ranks, v0, size, seg;  // seg: logits of a segment, a multiple of 128
   Weights weight;
 
   __device__ Shown& peer(int r) { return *cluster.map_shared_rank(shown, r); }
+  __device__ void sync() {
+    if (ranks > 1)
+      cluster.sync();
+    else
+      __syncthreads();
+  }
+
+  // Logits i .. i + 3 (i a multiple of 4), -inf past the part's end; all: there
+  // are four.  Past pass 1 +inf counts as the largest finite number.
+  __device__ __forceinline__ void load4(int i, float (&v)[4], bool all) const {
+    T y[4];
+    if (held) {
+      if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(held + i);
+      else
+        *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(held + i);
+    } else if (vector && (all || i + 4 <= size)) {
+      if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<uint4*>(y) = __ldg(reinterpret_cast<const uint4*>(global + i));
+      else
+        *reinterpret_cast<uint2*>(y) = __ldg(reinterpret_cast<const uint2*>(global + i));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[k] = global[min(i + k, size - 1)];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = to_float<T>(y[k]);
+    if (!all) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = i + k < size ? v[k] : -INFINITY;
+    }
+    if (infinite) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = fminf(v[k], kMostFinite);
+    }
+  }
+
+  // f(i, four logits) over the CTA's part by whole warps, end(s) after each
+  // segment: a warp takes every 16th segment, a lane four logits of 128, kAhead
+  // loads in flight.
+  template <int kAhead, class F, class End>
+  __device__ __forceinline__ void each(F f, End end) const {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int s = warp; s * seg < size; s += kNumWarps) {
+      const int e = min((s + 1) * seg, size);
+      for (int i0 = s * seg; i0 < e; i0 += 128 * kAhead) {
+        float v[kAhead][4];
+        if (i0 + 128 * kAhead <= e) {
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) load4(i0 + 128 * k + 4 * lane, v[k], true);
+        } else {
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k)
+            if (i0 + 128 * k < e) load4(i0 + 128 * k + 4 * lane, v[k], false);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (i0 + 128 * k < e) f(i0 + 128 * k + 4 * lane, v[k]);
+      }
+      end(s);
+    }
+  }
+
+  // Collects some lanes' logits (and their places) until a warp is full of them,
+  // so that what is done with a few of many is done by whole warps.
+  struct Queue {
+    float* at;
+    int* place;
+    int n;
+    template <class F>
+    __device__ __forceinline__ void push(bool take, float v, int i, F f) {
+      const unsigned who = __ballot_sync(0xffffffffu, take);
+      if (who == 0) return;
+      const int lane = threadIdx.x & 31;
+      const int to = n + __popc(who & ((1u << lane) - 1));
+      if (take) at[to] = v, place[to] = i;
+      n += __popc(who);
+      __syncwarp();
+      if (n >= 32) {
+        f(at[lane], place[lane]);
+        n -= 32;
+        const float rest = at[32 + lane];
+        const int rest_at = place[32 + lane];
+        __syncwarp();
+        if (lane < n) at[lane] = rest, place[lane] = rest_at;
+        __syncwarp();
+      }
+    }
+    template <class F>
+    __device__ __forceinline__ void flush(F f) {
+      const int lane = threadIdx.x & 31;
+      if (lane < n) f(at[lane], place[lane]);
+      n = 0;
+      __syncwarp();
+    }
+  };
+
+  // A logit at or below which no exponent is above th (row values: a little
+  // lower than the exact one).
+  __device__ __forceinline__ float below(float th) const {
+    const float d = -th / weight.ch;
+    return weight.top - d - 2e-6f * (fabsf(weight.top) + d);
+  }
 
   __device__ void clear() {
     for (int i = threadIdx.x; i < kBins; i += kThreads) hn[i] = hlo[i] = hhi[i] = 0;
     __syncthreads();
   }
-  // A 64-bit sum in two 32-bit words: the low word's carry goes to the high
-  // one, so the pair is exact whatever the order of the additions.
-  __device__ void put(int bin, u64 w) {
+  // A bin's count and 64-bit sum of weights.  The sums of hi (up to 2^20) and lo
+  // (to +-2^21) by themselves, exact for up to kSafe values of a bin; or, safe,
+  // in two words with the low one's carry to the high one, for any number.
+  __device__ __forceinline__ void put(int bin, int hi, int lo) {
     atomicAdd(hn + bin, 1u);
-    const uint32_t lo = (uint32_t)w;
-    const uint32_t old = atomicAdd(hlo + bin, lo);
-    const uint32_t hi = (uint32_t)(w >> 32) + (old + lo < old ? 1u : 0u);
-    if (hi) atomicAdd(hhi + bin, hi);
+    if (!safe) {
+      atomicAdd(hhi + bin, (uint32_t)hi);
+      atomicAdd(hlo + bin, (uint32_t)lo);
+    } else {
+      const u64 w = (u64)((long long)hi * (1 << 22) + lo);
+      const uint32_t old = atomicAdd(hlo + bin, (uint32_t)w);
+      const uint32_t up = (uint32_t)(w >> 32) + (old + (uint32_t)w < old ? 1u : 0u);
+      if (up) atomicAdd(hhi + bin, up);
+    }
   }
 
   // Sums the cluster's histograms, each CTA a share of the bins, and finds the
   // bin in which `before` plus the bins so far first reaches the target.
-  // Returns false where it never does; else before is what lies above the bin.
-  __device__ bool cross(bool by_weight, u64 target, CountWeight& before, int& bin, int& bin_n) {
-    cluster.sync();  // every histogram is complete
+  // kNever where it does not, kFull where the sums may have overflowed; else
+  // before is what lies above the bin.
+  enum Crossing { kNever, kFound, kFull };
+  __device__ Crossing cross(bool by_weight, u64 target, CountWeight& before, int& bin, int& bin_n) {
+    if (threadIdx.x == 0) shown->over = 0;
+    sync();  // every histogram is complete
     const int share = kBins / ranks, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (share + kThreads - 1) / kThreads;  // bins of a thread: 1, 2 or 4
     const int first = rank * share + threadIdx.x * per;
@@ -230,13 +362,17 @@ struct Row {
 #pragma unroll
     for (int k = 0; k < 4; ++k) sum[k] = {0, 0};
     if (mine) {
+#pragma unroll 4
       for (int r = 0; r < ranks; ++r) {
         const uint32_t *n = cluster.map_shared_rank(hn, r), *lo = cluster.map_shared_rank(hlo, r),
                        *hi = cluster.map_shared_rank(hhi, r);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (k < per)
-            sum[k] = sum[k] + CountWeight{((u64)hi[first + k] << 32) + lo[first + k], (int)n[first + k]};
+          if (k < per) {
+            const uint32_t h = hi[first + k], l = lo[first + k], c = n[first + k];
+            sum[k] = sum[k] + CountWeight{safe ? ((u64)h << 32) + l : ((u64)h << 22) + (u64)(long long)(int)l, (int)c};
+            if (!safe && c > kSafe) shown->over = 1;
+          }
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) all = all + sum[k];
@@ -250,9 +386,10 @@ struct Row {
       total = total + warp_sum[k];
     }
     if (threadIdx.x == 0) shown->total = total;
-    cluster.sync();
-    int owner = -1;
+    sync();
+    int owner = -1, over = 0;
     CountWeight sofar = before;
+    for (int r = 0; r < ranks; ++r) over |= peer(r).over;
     for (int r = 0; r < ranks; ++r) {
       const CountWeight next = sofar + peer(r).total;
       if ((by_weight ? next.w : (u64)next.n) >= target) {
@@ -276,74 +413,231 @@ struct Row {
           c = next;
         }
     }
-    cluster.sync();
-    if (owner < 0) return false;
+    sync();
+    if (over) return kFull;
+    if (owner < 0) return kNever;
     before = peer(owner).before;
     bin = peer(owner).bin;
     bin_n = peer(owner).bin_n;
-    return true;
+    return kFound;
   }
 
-  // The part of the row whose exponent lies in (-to, -from], in the bins.  With
-  // `sum`, also this lane's sum of all weights.
-  __device__ u64 fill(float from, float to, bool sum) {
-    clear();
-    const float scale = kBins / (to - from);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int c0, c1;
-    chunk(warp, c0, c1);
-    int all_hi = 0, all_lo = 0;  // at most 64 of 2^20 and 2^21
-    for (int i = c0 + lane; i < c1; i += 32) {
-      const float v = x[i];
-      if (!sum && !(weight.coarse(v) > -to)) continue;
-      int hi, lo;
-      const float th = weight.parts(v, hi, lo);
-      all_hi += hi;
-      all_lo += lo;
-      if (th > -to && th <= -from)
-        put(min((int)((-th - from) * scale), kBins - 1), (u64)((long long)hi * (1 << 22) + lo));
+  // The bins' range of exponents: (-to, -from].
+  struct Range {
+    float from, to;
+    __device__ __forceinline__ bool has(float th) const { return th > -to && th <= -from; }
+    __device__ __forceinline__ int bin(float th) const {  // rounded: monotone as well
+      const float scale = kBins / (to - from), magic = 12582912.f;
+      return min(max(__float_as_int(fmaf(-th - from, scale, magic)) - 0x4B400000, 0), kBins - 1);
     }
-    return (u64)((long long)all_hi * (1 << 22) + all_lo);
+  };
+
+  // Pass 2.  With `sum`, also this lane's sum of all weights.
+  __device__ u64 fill(Range range, bool sum) {
+    clear();
+    long long all_hi = 0, all_lo = 0;
+    int seg_hi = 0, seg_lo = 0;  // at most 32 of 2^20 and 2^21
+    if (sum) {
+      each<2>(
+          [&](int, const float (&v)[4]) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              int hi, lo;
+              const float th = weight.parts(v[k], hi, lo);
+              seg_hi += hi;
+              seg_lo += lo;
+              if (range.has(th)) put(range.bin(th), hi, lo);
+            }
+          },
+          [&](int) { all_hi += seg_hi, all_lo += seg_lo, seg_hi = seg_lo = 0; });
+    } else {
+      Queue q{queue, queue_at, 0};
+      const float low = below(-range.to);
+      auto bin = [&](float v, int) {
+        int hi, lo;
+        const float th = weight.parts(v, hi, lo);
+        if (range.has(th)) put(range.bin(th), hi, lo);
+      };
+      each<2>(
+          [&](int i, const float (&v)[4]) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) q.push(v[k] >= low, v[k], i + k, bin);
+          },
+          [](int) {});
+      q.flush(bin);
+    }
+    return (u64)(all_hi * (1 << 22) + all_lo);
+  }
+  // The cluster's sum of v.
+  __device__ u64 total_of(u64 v) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    __syncthreads();
+    if (lane == 0) warp_sum[warp].w = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      v = 0;
+      for (int w = 0; w < kNumWarps; ++w) v += warp_sum[w].w;
+      shown->kept = v;
+    }
+    sync();
+    v = 0;
+    for (int r = 0; r < ranks; ++r) v += peer(r).kept;
+    sync();  // before it is set again
+    return v;
   }
 
-  // A warp's share of the CTA's logits.
-  __device__ void chunk(int warp, int& c0, int& c1) const {
-    const int n = ((size + kThreads - 1) / kThreads) * 32;
-    c0 = min(warp * n, size);
-    c1 = min(c0 + n, size);
+  __device__ void store_segment(int s, int hi, int lo) {
+    u64 v = (u64)((long long)hi * (1 << 22) + lo);
+#pragma unroll
+    for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if ((threadIdx.x & 31) == 0) seg_sum[s] = v;
   }
 
-  // The shortest prefix of the order that has `target` elements, or weight.
-  // near: the bins hold the part up to kNear; they do again on return, or
-  // near is false.
-  __device__ bool select(bool by_weight, u64 target, Cut& cut, bool& near) {
+  // The segments' sums of what the cut keeps.
+  __device__ void sum_kept(const Cut& cut) {
+    int hi_sum = 0, lo_sum = 0;
+    auto add = [&](float v, int) {
+      int hi, lo;
+      weight.parts(v, hi, lo);
+      hi_sum += hi;
+      lo_sum += lo;
+    };
+    if (cut.key == 0) {  // all: no need to collect them
+      each<2>(
+          [&](int, const float (&v)[4]) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) add(v[k], 0);
+          },
+          [&](int s) { store_segment(s, hi_sum, lo_sum), hi_sum = lo_sum = 0; });
+      return;
+    }
+    Queue q{queue, queue_at, 0};
+    each<2>(
+        [&](int i, const float (&v)[4]) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) q.push(cut.has(key_of(v[k]), v0 + i + k), v[k], i + k, add);
+        },
+        [&](int s) { q.flush(add), store_segment(s, hi_sum, lo_sum), hi_sum = lo_sum = 0; });
+  }
+
+  // The shortest prefix of the order that has `target` elements, or weight:
+  // its cut and weight.  near: the bins hold the part up to kNear (on return as
+  // well).  With `sums`, the segments' sums of it (of what has bits least or
+  // above) are taken on the way; summed says whether they could be.
+  __device__ bool select(bool by_weight, u64 target, uint32_t least, bool sums, Cut& cut, u64& cut_weight,
+                         bool& near, bool& summed) {
     CountWeight before{0, 0};
     int bin, bin_n;
-    float from = 0.f, to = kNear;
-    if (!near) fill(from, to, false), near = true;
-    if (!cross(by_weight, target, before, bin, bin_n)) {
+    Range range{0.f, kNear};
+    if (!near) fill(range, false), near = true;
+    Crossing got = cross(by_weight, target, before, bin, bin_n);
+    if (got == kFull) {
+      safe = true;
+      fill(range, false);
+      got = cross(by_weight, target, before, bin, bin_n);
+    }
+    if (got == kNever) {
       // below it: what is above are all of the first bins
       for (int r = 0; r < ranks; ++r) before = before + peer(r).total;
-      from = kNear, to = -kLeast;
-      cluster.sync();
-      fill(from, to, false);
+      range = {kNear, -kLeast};
+      sync();
+      fill(range, true);  // most logits lie there: they are not collected
       near = false;
-      if (!cross(by_weight, target, before, bin, bin_n)) return false;
+      got = cross(by_weight, target, before, bin, bin_n);
+      if (got == kFull) {
+        safe = true;
+        fill(range, true);
+        got = cross(by_weight, target, before, bin, bin_n);
+      }
+      if (got == kNever) return false;
     }
-    // the values in that bin
-    const float scale = kBins / (to - from);
+    const bool few = bin_n <= kFew;
+    sums &= few;
+    // pass 3
     uint32_t kmin = 0xffffffffu, kmax = 0;
     Shown& lead = peer(0);
-    uint32_t* list = cluster.map_shared_rank(few_key, 0);
-    for (int i = threadIdx.x; i < size; i += kThreads) {
-      const float th = weight.coarse(x[i]);
-      if (th > -to && th <= -from && min((int)((-th - from) * scale), kBins - 1) == bin) {
-        const uint32_t k = key_of(x[i]);
-        kmin = min(kmin, k);
-        kmax = max(kmax, k);
-        if (bin_n <= kFew) list[atomicAdd(&lead.few, 1)] = k;
+    uint32_t* list_key = cluster.map_shared_rank(few_key, 0);
+    int* list_at = cluster.map_shared_rank(few_at, 0);
+    int hi_sum = 0, lo_sum = 0;
+    Queue q{queue, queue_at, 0};
+    auto sort = [&](float v, int i) {
+      const float th = weight.coarse(v);
+      const int b = th > -range.from ? -1 : th > -range.to ? range.bin(th) : kBins;
+      const uint32_t key = key_of(v);
+      if (b == bin) {
+        kmin = min(kmin, key);
+        kmax = max(kmax, key);
+        if (few) {
+          const int n = atomicAdd(&lead.few, 1);
+          list_key[n] = key;
+          list_at[n] = v0 + i;
+        }
+      } else if (sums && b < bin && key >= least) {
+        int hi, lo;
+        weight.parts(v, hi, lo);
+        hi_sum += hi;
+        lo_sum += lo;
       }
+    };
+    // the bin's lower end, or the logit of bits least where that is higher
+    const float low = below(-(range.from + (bin + 1) * ((range.to - range.from) / kBins)));
+    each<2>(
+        [&](int i, const float (&v)[4]) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) q.push(v[k] >= low, v[k], i + k, sort);
+        },
+        [&](int s) {
+          if (sums) q.flush(sort), store_segment(s, hi_sum, lo_sum), hi_sum = lo_sum = 0;
+        });
+    q.flush(sort);
+    if (few) {
+      sync();  // the list is complete
+      if (rank == 0) {
+        const int t = threadIdx.x;
+        if (t < bin_n) few_w[t] = weight(of_key(few_key[t]));
+        __syncthreads();
+        if (t < bin_n) {
+          const uint32_t key = few_key[t];
+          const int at = few_at[t];
+          CountWeight above = before;
+          int same = 0, lower = 0;  // values equal to this, those of lower index
+          for (int j = 0; j < bin_n; ++j) {
+            const uint32_t k = few_key[j];
+            if (k > key) above = above + CountWeight{few_w[j], 1};
+            same += k == key;
+            lower += k == key && few_at[j] < at;
+          }
+          const u64 w = few_w[t];
+          const u64 lo = by_weight ? above.w : (u64)above.n;
+          const u64 hi = by_weight ? above.w + same * w : (u64)above.n + same;
+          if (lo < target && hi >= target) {  // the prefix ends among the values equal to this
+            const u64 need = by_weight ? (target - lo + w - 1) / w : target - lo;
+            if ((u64)lower + 1 == need) {
+              shown->cut = {key, at};
+              shown->weight = above.w + need * w;
+            }
+          }
+        }
+        if (t == 0) shown->few = 0;
+      }
+      sync();
+      cut = lead.cut;
+      cut_weight = lead.weight;
+      if (sums) {  // the bin's kept values
+        const u64* list_w = cluster.map_shared_rank(few_w, 0);
+        const int t = threadIdx.x;
+        if (t < bin_n) {
+          const uint32_t key = list_key[t];
+          const int at = list_at[t] - v0;
+          if (key >= least && cut.has(key, v0 + at) && at >= 0 && at < size) atomicAdd(seg_sum + at / seg, list_w[t]);
+        }
+        summed = true;
+      }
+      return true;
     }
+    // many values: cut the range of bits until one is left
     kmin = __reduce_min_sync(0xffffffffu, kmin);
     kmax = __reduce_max_sync(0xffffffffu, kmax);
     if (threadIdx.x == 0) shown->kmin = 0xffffffffu, shown->kmax = 0;
@@ -352,58 +646,94 @@ struct Row {
       atomicMin(&shown->kmin, kmin);
       atomicMax(&shown->kmax, kmax);
     }
-    cluster.sync();
+    sync();
     for (int r = 0; r < ranks; ++r) {
       kmin = min(kmin, peer(r).kmin);
       kmax = max(kmax, peer(r).kmax);
     }
-    if (kmin != kmax && bin_n <= kFew) {
-      if (rank == 0) {
-        if ((int)threadIdx.x < bin_n) few_w[threadIdx.x] = weight(of_key(few_key[threadIdx.x]));
-        __syncthreads();
-        if ((int)threadIdx.x < bin_n) {
-          const uint32_t key = few_key[threadIdx.x];
-          CountWeight above = before;
-          int same = 0;
-          for (int j = 0; j < bin_n; ++j) {
-            if (few_key[j] > key) above = above + CountWeight{few_w[j], 1};
-            same += few_key[j] == key;
-          }
-          const u64 w = few_w[threadIdx.x];
-          const u64 lo = by_weight ? above.w : (u64)above.n;
-          const u64 hi = by_weight ? above.w + same * w : (u64)above.n + same;
-          if (lo < target && hi >= target)  // one value: its threads write the same
-            shown->cut = end_at(by_weight, target, key, above, same, w);
-        }
-        if (threadIdx.x == 0) shown->few = 0;
-      }
-      cluster.sync();
-      cut = lead.cut;
-      return true;
-    }
-    if (rank == 0 && threadIdx.x == 0) shown->few = 0;
     while (kmin != kmax) {
       const uint32_t span = kmax - kmin;
       const int shift = max(0, 32 - __clz(span) - 11);
       clear();
       near = false;
-      for (int i = threadIdx.x; i < size; i += kThreads) {
-        const uint32_t k = key_of(x[i]);
-        if (k >= kmin && k <= kmax) put((int)((kmax - k) >> shift), weight(x[i]));
-      }
-      if (!cross(by_weight, target, before, bin, bin_n)) return false;
+      safe = true;
+      each<2>(
+          [&](int, const float (&v)[4]) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t key = key_of(v[k]);
+              int hi, lo;
+              if (key >= kmin && key <= kmax) weight.parts(v[k], hi, lo), put((int)((kmax - key) >> shift), hi, lo);
+            }
+          },
+          [](int) {});
+      if (cross(by_weight, target, before, bin, bin_n) != kFound) return false;
       kmax -= (uint32_t)bin << shift;
       const uint32_t width = (1u << shift) - 1;
       kmin = kmax - kmin > width ? kmax - width : kmin;
     }
-    cut = end_at(by_weight, target, kmax, before, bin_n, weight(of_key(kmax)));
+    const u64 w = weight(of_key(kmax));
+    const u64 need = by_weight ? (target - before.w + w - 1) / w : target - (u64)before.n;
+    cut = {kmax, need < (u64)bin_n ? index_of(kmax, (int)need) : 0x7fffffff};
+    cut_weight = before.w + min(need, (u64)bin_n) * w;
     return true;
   }
 
-  __device__ static Cut end_at(bool by_weight, u64 target, uint32_t key, const CountWeight& above,
-                               int same, u64 w) {
-    const u64 need = by_weight ? (target - above.w + w - 1) / w : target - (u64)above.n;
-    return {key, (int)min(need, (u64)same), above.w, w};
+  // The index of the n-th logit (from 1) of these bits.
+  __device__ int index_of(uint32_t key, int n) {
+    int count = 0;
+    each<2>(
+        [&](int, const float (&v)[4]) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) count += key_of(v[k]) == key;
+        },
+        [&](int s) {
+          count = (int)__reduce_add_sync(0xffffffffu, (unsigned)count);
+          if ((threadIdx.x & 31) == 0) seg_sum[s] = count;
+          count = 0;
+        });
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      int all = 0;
+      for (int s = 0; s * seg < size; ++s) all += (int)seg_sum[s];
+      shown->ties = all;
+    }
+    sync();
+    for (int r = 0; r < rank; ++r) n -= peer(r).ties;
+    const bool mine = n > 0 && n <= shown->ties;
+    if (mine && threadIdx.x < 32) {
+      const int lane = threadIdx.x;
+      int s = 0;
+      for (; n > (int)seg_sum[s]; ++s) n -= (int)seg_sum[s];
+      for (int i = s * seg + 4 * lane; n > 0; i += 128) {
+        float v[4];
+        load4(min(i, (size - 1) / 4 * 4), v, false);
+        int c = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c += i + k < size && key_of(v[k]) == key;
+        int upto = c;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, upto, off);
+          if (lane >= off) upto += o;
+        }
+        const int all = __shfl_sync(0xffffffffu, upto, 31);
+        if (upto >= n && upto - c < n) {
+          int left = n - (upto - c);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (i + k < size && key_of(v[k]) == key && --left == 0) shown->cut.last = v0 + i + k;
+        }
+        n -= all;
+      }
+    }
+    if (threadIdx.x == 0) shown->bin = mine;
+    sync();
+    int at = 0x7fffffff;
+    for (int r = 0; r < ranks; ++r)
+      if (peer(r).bin) at = peer(r).cut.last;
+    sync();
+    return at;
   }
 };
 
@@ -413,25 +743,34 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   __shared__ Shown s_shown;
   __shared__ CountWeight s_warp[32];
   __shared__ float s_top[32];
-  __shared__ int s_first[32], s_bad;
-  __shared__ double s_c, s_least;  // log2(e) / T, T ln(min_p)
+  __shared__ int s_bad;
+  __shared__ double s_c, s_least;  // 1 / T, T ln(min_p)
+  __shared__ float s_queue[kNumWarps][64];
+  __shared__ int s_queue_at[kNumWarps][64];
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float2* table = reinterpret_cast<float2*>(smem);
-  uint32_t* hist = reinterpret_cast<uint32_t*>(table + 1024);
-  u64* few_w = reinterpret_cast<u64*>(hist + 3 * kBins);
+  u64* seg_sum = reinterpret_cast<u64*>(table + 1024);
+  u64* few_w = seg_sum + kSegments;
   uint32_t* few_key = reinterpret_cast<uint32_t*>(few_w + kFew);
-  float* x = reinterpret_cast<float*>(few_key + kFew);
+  int* few_at = reinterpret_cast<int*>(few_key + kFew);
+  uint32_t* hist = reinterpret_cast<uint32_t*>(few_at + kFew);
+  T* held = reinterpret_cast<T*>(hist + 3 * kBins);
   const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int row = blockIdx.x / ranks;
   const int v0 = min(rank * p.slice, p.vocab), size = min(p.slice, p.vocab - v0);
-  Row<T> R{p, cluster, x, hist, hist + kBins, hist + 2 * kBins, few_key, few_w, &s_shown, s_warp, rank, ranks, v0, size, {}};
+  const T* global = reinterpret_cast<const T*>(p.logits) + row * p.stride + v0;
+  Row<T> R{cluster, global, nullptr, (reinterpret_cast<uintptr_t>(global) & (4 * sizeof(T) - 1)) == 0,
+           hist, hist + kBins, hist + 2 * kBins, few_key, few_at, few_w, seg_sum, &s_shown, s_warp,
+           s_queue[warp], s_queue_at[warp], false, false, rank, ranks, v0, size, 128 * ((p.slice + 128 * kSegments - 1) / (128 * kSegments)), {}};
+  // segments of up to 1024 logits, of fewer where a warp would have none
+  R.seg = max(R.seg, min(1024, 128 * ((p.slice + 128 * kNumWarps - 1) / (128 * kNumWarps))));
   const float temperature = p.temperature ? p.temperature[row] : p.temperature_all;
   const float min_p = p.min_p ? p.min_p[row] : p.min_p_all;
   if (tid == 0) {  // 64-bit arithmetic is slow here: once a CTA
     s_bad = 0;
     s_shown.few = 0;
-    s_c = 1.4426950408889634074 / (double)temperature;
+    s_c = 1.0 / (double)temperature;
     s_least = min_p > 0.f ? (double)temperature * log((double)fminf(min_p, 1.f)) : 0.0;
   }
   for (int j = tid; j < 1024; j += kThreads) {
@@ -440,143 +779,85 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     table[j] = make_float2(hi * 0x1p-60f, (float)(long long)(v - (u64)hi) * 0x1p-60f);
   }
 
-  // ---- the logits, their largest, and whether one is not a number
-  const T* src = reinterpret_cast<const T*>(p.logits) + row * p.stride + v0;
+  // ---- pass 1: the largest logit, and whether one is not a number
   float top = -INFINITY;
-  int first = p.vocab;
   bool nan = false;
-  auto take = [&](int i, T y) {
-    const float v = to_float<T>(y) + 0.f;  // -0 becomes 0: equal logits have equal bits
-    x[i] = v;
-    nan |= v != v;
-    if (v > top) top = v, first = v0 + i;
-  };
-  constexpr int kVec = 16 / sizeof(T);
-  int done = 0;
-  if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {  // 16 bytes a load, four in flight
-    done = size / kVec * kVec;
-    for (int i0 = tid * kVec; i0 < done; i0 += 4 * kThreads * kVec) {
-      uint4 raw[4];
+  R.template each<4>(
+      [&](int i, const float (&v)[4]) {
+        if (p.held) {
+          T y[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (i0 + k * kThreads * kVec < done)
-          raw[k] = __ldg(reinterpret_cast<const uint4*>(src + i0 + k * kThreads * kVec));
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (i0 + k * kThreads * kVec < done) {
-          T y[kVec];
-          memcpy(y, &raw[k], 16);
-#pragma unroll
-          for (int j = 0; j < kVec; ++j) take(i0 + k * kThreads * kVec + j, y[j]);
+          for (int k = 0; k < 4; ++k) y[k] = T(v[k]);  // exact: it came from a T
+          if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<uint4*>(held + i) = *reinterpret_cast<const uint4*>(y);
+          else
+            *reinterpret_cast<uint2*>(held + i) = *reinterpret_cast<const uint2*>(y);
         }
-    }
-  }
-  for (int i0 = done + tid; i0 < size; i0 += 8 * kThreads) {
-    T y[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (i0 + k * kThreads < size) y[k] = src[i0 + k * kThreads];
+        for (int k = 0; k < 4; ++k) {
+          nan |= v[k] != v[k];
+          top = fmaxf(top, v[k]);
+        }
+      },
+      [](int) {});
+  if (p.held) R.held = held;
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (i0 + k * kThreads < size) take(i0 + k * kThreads, y[k]);
-  }
-#pragma unroll
-  for (int off = 16; off; off >>= 1) {
-    const float o = __shfl_xor_sync(0xffffffffu, top, off);
-    const int f = __shfl_xor_sync(0xffffffffu, first, off);
-    if (o > top || (o == top && f < first)) top = o, first = f;
-  }
-  if (lane == 0) s_top[warp] = top, s_first[warp] = first;
+  for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  if (lane == 0) s_top[warp] = top;
   __syncthreads();
   if (nan) s_bad = 1;
   __syncthreads();
   if (tid == 0) {
-    for (int w = 1; w < kNumWarps; ++w)
-      if (s_top[w] > top || (s_top[w] == top && s_first[w] < first)) top = s_top[w], first = s_first[w];
+    for (int w = 1; w < kNumWarps; ++w) top = fmaxf(top, s_top[w]);
     s_shown.top = top;
-    s_shown.first = first;
     s_shown.bad = s_bad;
   }
-  cluster.sync();
+  R.sync();
   int bad = 0;
   top = -INFINITY;
-  first = p.vocab;
   for (int r = 0; r < ranks; ++r) {
-    const Shown& o = R.peer(r);
-    bad |= o.bad;
-    if (o.top > top || (o.top == top && o.first < first)) top = o.top, first = o.first;
+    bad |= R.peer(r).bad;
+    top = fmaxf(top, R.peer(r).top);
   }
   int32_t* tokens = p.tokens + (long long)row * p.draws;
   float* logprobs = p.logprobs ? p.logprobs + (long long)row * p.draws : nullptr;
   const bool none = bad || top == -INFINITY;
-  if (none || !(temperature > 0.f)) {  // nothing to draw from, or the largest
+  R.infinite = top == INFINITY;
+  if (none || !(temperature > 0.f)) {  // nothing to draw from, or the first of the largest
+    int first = 0x7fffffff;
+    if (!none) {
+      const float most = R.infinite ? kMostFinite : top;
+      R.template each<4>(
+          [&](int i, const float (&v)[4]) {
+#pragma unroll
+            for (int k = 3; k >= 0; --k)
+              if (v[k] == most) first = min(first, v0 + i + k);
+          },
+          [](int) {});
+    }
+    first = __reduce_min_sync(0xffffffffu, first);
+    if (tid == 0) s_shown.first = 0x7fffffff;
+    __syncthreads();
+    if (lane == 0) atomicMin(&s_shown.first, first);
+    R.sync();
+    for (int r = 0; r < ranks; ++r) first = min(first, R.peer(r).first);
     if (rank == 0)
       for (int j = tid; j < p.draws; j += kThreads) {
         tokens[j] = none ? -1 : first;
         if (logprobs) logprobs[j] = none ? NAN : 0.f;
       }
-    cluster.sync();  // this CTA's words may still be read
+    R.sync();  // this CTA's words may still be read
     return;
   }
+  top = fminf(top, kMostFinite);
   const double c = s_c;
   R.weight.top = top;
-  R.weight.ch = (float)c;
-  R.weight.cl = isinf(R.weight.ch) ? 0.f : (float)(c - (double)R.weight.ch);
+  R.weight.ch = fminf((float)c, kMostFinite);
+  R.weight.cl = R.weight.ch == kMostFinite ? 0.f : (float)(c - (double)R.weight.ch);
   R.weight.table = table;
 
   // ---- the kept prefix of the order
-  Cut cut{0, 0x7fffffff, 0, 0};  // everything
-  const int top_k = p.top_k ? p.top_k[row] : p.top_k_all;
-  const float top_p = p.top_p ? p.top_p[row] : p.top_p_all;
-  auto shorten = [&](const Cut& o) {
-    if (o.key > cut.key || (o.key == cut.key && o.m < cut.m)) cut = o;
-  };
-  const bool use_k = top_k > 0 && top_k < p.vocab, use_p = top_p < 1.f;
-  if (use_k || use_p) {
-    // one pass: the bins, and with top-p alone the whole row's weight
-    u64 sum = R.fill(0.f, kNear, !use_k);
-    bool near = true;
-    if (!use_k) {
-#pragma unroll
-      for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-      if (lane == 0) s_warp[warp].w = sum;
-      __syncthreads();
-      if (tid == 0) {
-        sum = 0;
-        for (int w = 0; w < kNumWarps; ++w) sum += s_warp[w].w;
-        s_shown.kept = sum;
-      }
-      __syncthreads();
-    }
-    u64 total = 0;
-    Cut o;
-    if (use_k) {
-      if (R.select(false, (u64)top_k, o, near)) shorten(o), total = o.above + (u64)o.m * o.w;
-    }
-    if (use_p) {
-      cluster.sync();
-      if (use_k && total == 0) {  // fewer than k have a weight: all of it counts
-        sum = R.fill(0.f, kNear, true);
-        near = true;
-#pragma unroll
-        for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        if (lane == 0) s_warp[warp].w = sum;
-        __syncthreads();
-        if (tid == 0) {
-          sum = 0;
-          for (int w = 0; w < kNumWarps; ++w) sum += s_warp[w].w;
-          s_shown.kept = sum;
-        }
-        cluster.sync();
-      }
-      if (total == 0)
-        for (int r = 0; r < ranks; ++r) total += R.peer(r).kept;
-      u64 want = 0;
-      if (lane == 0) want = max((u64)ceil((double)fmaxf(top_p, 0.f) * (double)total), 1ull);
-      want = __shfl_sync(0xffffffffu, want, 0);
-      if (R.select(true, want, o, near)) shorten(o);
-    }
-  }
+  Cut cut{0, 0x7fffffff};  // everything
   if (min_p > 0.f && temperature < INFINITY) {
     // w >= min_p * w_max is x >= top + T ln(min_p): the least float that is
     float f = top;
@@ -588,108 +869,113 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       if (isnan(f) || f > top) f = top;
     }
     f = __shfl_sync(0xffffffffu, f, 0);
-    shorten({key_of(f), 0x7fffffff, 0, 0});
+    cut.key = key_of(f);
   }
-
-  // ---- sums of the kept weights, warp by warp in index order
-  int c0, c1;
-  R.chunk(warp, c0, c1);
-  int hi_sum = 0, lo_sum = 0, ties = 0;
-  for (int i = c0 + lane; i < c1; i += 32) {
-    const uint32_t k = key_of(x[i]);
-    if (k > cut.key) {
-      int hi, lo;
-      R.weight.parts(x[i], hi, lo);
-      hi_sum += hi;
-      lo_sum += lo;
+  const uint32_t least = cut.key;
+  auto shorten = [&](const Cut& o) {
+    if (o.key > cut.key || (o.key == cut.key && o.last < cut.last)) cut = o;
+  };
+  const int top_k = p.top_k ? p.top_k[row] : p.top_k_all;
+  const float top_p = p.top_p ? p.top_p[row] : p.top_p_all;
+  const bool use_k = top_k > 0 && top_k < p.vocab, use_p = top_p < 1.f;
+  bool summed = false;
+  if (use_k || use_p) {
+    u64 total = R.fill({0.f, kNear}, !use_k);
+    bool near = true;
+    Cut o;
+    u64 w = 0;
+    if (use_k && R.select(false, (u64)top_k, least, !use_p, o, w, near, summed)) shorten(o);
+    if (use_p) {
+      if (use_k && w == 0)  // fewer than k have a weight: all of it counts
+        R.sync(), total = R.fill({0.f, kNear}, true), near = true;
+      total = w ? w : R.total_of(total);
+      u64 want = 0;
+      if (lane == 0) want = max((u64)ceil((double)fmaxf(top_p, 0.f) * (double)total), 1ull);
+      want = __shfl_sync(0xffffffffu, want, 0);
+      if (R.select(true, want, least, true, o, w, near, summed)) shorten(o);
     }
-    ties += k == cut.key;
   }
-  u64 sum = (u64)((long long)hi_sum * (1 << 22) + lo_sum);
-  const float tie_x = of_key(cut.key);
-  const u64 w_tie = tie_x == tie_x ? R.weight(tie_x) : 0;
-#pragma unroll
-  for (int off = 16; off; off >>= 1) {
-    sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    ties += __shfl_xor_sync(0xffffffffu, ties, off);
-  }
-  if (lane == 0) s_warp[warp] = {sum, ties};
+  if (!summed) R.sum_kept(cut);
   __syncthreads();
-  int ties_before = 0, all_ties = 0;
-  for (int w = 0; w < kNumWarps; ++w) {
-    if (w == warp) ties_before = all_ties;
-    all_ties += s_warp[w].n;
+
+  // ---- running sums over the segments
+  u64 mine = tid < kSegments && tid * R.seg < size ? seg_sum[tid] : 0;
+  const CountWeight upto = scan_warp({mine, 0}, lane);
+  if (lane == 31) s_warp[warp] = upto;
+  __syncthreads();
+  u64 before = 0, cta = 0;
+  for (int k = 0; k < kNumWarps; ++k) {
+    if (k == warp) before = cta;
+    cta += s_warp[k].w;
   }
-  if (tid == 0) s_shown.ties = all_ties;
-  cluster.sync();
-  int cta_ties = 0;
-  for (int r = 0; r < rank; ++r) cta_ties += R.peer(r).ties;
-  auto kept_of = [&](int before, int n) { return max(0, min(n, cut.m - before)); };
-  u64 before = 0, cta = 0, own = 0;
-  {
-    int t = cta_ties;
-    for (int w = 0; w < kNumWarps; ++w) {
-      const u64 s = s_warp[w].w + (u64)kept_of(t, s_warp[w].n) * w_tie;
-      if (w == warp) before = cta, own = s;
-      cta += s;
-      t += s_warp[w].n;
-    }
-  }
+  if (tid < kSegments) seg_sum[tid] = before + upto.w;  // up to and with segment tid
   if (tid == 0) s_shown.kept = cta;
-  cluster.sync();
-  u64 total = 0;
+  R.sync();
+  u64 total = 0, start = 0;
   for (int r = 0; r < ranks; ++r) {
-    if (r == rank) before += total;
+    if (r == rank) start = total;
     total += R.peer(r).kept;
   }
-  ties_before += cta_ties;
 
-  // ---- the draws whose place lies in this warp's part
-  if (own > 0) {
-    const float whole = log2f((float)((double)total * (1.0 / (double)kOne)));
-    for (int j = 0; j < p.draws; ++j) {
-      const float u = p.u[(long long)row * p.draws + j];
-      const double place = (u > 0.f ? fmin((double)u, 1.0) : 0.0) * (double)total;
-      const u64 target = min((u64)place, total - 1);
-      if (target < before || target - before >= own) continue;
-      u64 at = before;
-      int tie = ties_before;
-      for (int i0 = c0; i0 < c1; i0 += 32) {
-        const int i = i0 + lane;
-        u64 w = 0;
-        bool is_tie = false;
-        if (i < c1) {
-          const uint32_t k = key_of(x[i]);
-          if (k > cut.key) w = R.weight(x[i]);
-          is_tie = k == cut.key;
+  // ---- the draws whose place lies in this CTA's part, a warp each
+  const float whole = logf((float)((double)total * (1.0 / (double)kOne)));
+  for (int j = warp; j < p.draws; j += kNumWarps) {
+    const float u = p.u[(long long)row * p.draws + j];
+    const double place = (u > 0.f ? fmin((double)u, 1.0) : 0.0) * (double)total;
+    u64 target = min((u64)place, total - 1);
+    if (target < start || target - start >= cta) continue;
+    target -= start;
+    int s = 0;  // segments that end at or before the target
+#pragma unroll
+    for (int k = 0; k < kSegments / 32; ++k) s += seg_sum[32 * k + lane] <= target;
+    s = __reduce_add_sync(0xffffffffu, s);
+    u64 at = s ? seg_sum[s - 1] : 0;
+    const int end = min((s + 1) * R.seg, size);
+    for (int i = s * R.seg + 4 * lane; i - 4 * lane < end; i += 128) {
+      u64 w[4] = {0, 0, 0, 0}, sum = 0;
+      float v[4];
+      if (i < end) {
+        R.load4(i, v, false);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (cut.has(key_of(v[k]), v0 + i + k)) w[k] = R.weight(v[k]);
+          sum += w[k];
         }
-        const unsigned t = __ballot_sync(0xffffffffu, is_tie);
-        if (is_tie && tie + __popc(t & ((1u << lane) - 1)) < cut.m) w = w_tie;
-        tie += __popc(t);
-        const u64 c_i = at + scan_warp({w, 0}, lane).w;
-        const unsigned past = __ballot_sync(0xffffffffu, c_i > target);
-        if (past) {
-          if (lane == __ffs(past) - 1) {
-            tokens[j] = v0 + i;
-            if (logprobs) {
-              float th = 0.f, tl = 0.f;
-              if (x[i] != R.weight.top) R.weight.exponent(x[i], th, tl);
-              logprobs[j] = ((th - whole) + tl) * kLn2Hi;
-            }
-          }
-          break;
-        }
-        at = __shfl_sync(0xffffffffu, c_i, 31);
       }
+      const u64 with = at + scan_warp({sum, 0}, lane).w;
+      const unsigned past = __ballot_sync(0xffffffffu, with > target);
+      if (past) {
+        if (lane == __ffs(past) - 1) {
+          u64 c_i = with - sum;
+          int hit = 3;
+#pragma unroll
+          for (int k = 3; k >= 0; --k) {  // the first k whose running sum passes the target
+            u64 run = c_i;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) run += q <= k ? w[q] : 0;
+            if (run > target) hit = k;
+          }
+          const float x = hit == 0 ? v[0] : hit == 1 ? v[1] : hit == 2 ? v[2] : v[3];
+          tokens[j] = v0 + i + hit;
+          if (logprobs) {
+            float th, tl;
+            R.weight.exponent(x, th, tl);
+            logprobs[j] = (th - whole) + tl;
+          }
+        }
+        break;
+      }
+      at = __shfl_sync(0xffffffffu, with, 31);
     }
   }
-  cluster.sync();  // this CTA's words may still be read
+  R.sync();  // this CTA's words may still be read
 }
 
 template <typename T>
 cudaError_t run(SampleParams p, int ranks, cudaStream_t s) {
-  p.slice = ((p.vocab + ranks - 1) / ranks + 31) / 32 * 32;
-  const size_t smem = 1024 * 8 + 3 * kBins * 4 + kFew * 12 + (size_t)p.slice * 4;
+  p.slice = ((p.vocab + ranks - 1) / ranks + 127) / 128 * 128;
+  p.held = p.slice * sizeof(T) <= kHeld;
+  const size_t smem = 1024 * 8 + kSegments * 8 + kFew * 16 + 3 * kBins * 4 + (p.held ? p.slice * sizeof(T) : 0);
   cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -711,10 +997,9 @@ cudaError_t run(SampleParams p, int ranks, cudaStream_t s) {
 
 cudaError_t launch_sample(const SampleParams& p, cudaStream_t s) {
   if (p.rows == 0 || p.draws == 0) return cudaSuccess;
+  // few rows: more CTAs a row while there is room on the SMs (two fit one)
   int ranks = 1;
-  while (ranks < kMaxRanks && (p.vocab + ranks - 1) / ranks > kSlice) ranks *= 2;
-  // few rows: more CTAs a row while SMs are free
-  while (ranks < kMaxRanks && (long long)p.rows * ranks * 2 <= p.num_sms && p.vocab / ranks > 2048) ranks *= 2;
+  while (ranks < kMaxRanks && (long long)p.rows * ranks <= p.num_sms && p.vocab / ranks > 4096) ranks *= 2;
   if (p.dtype == kFp32) return run<float>(p, ranks, s);
   if (p.dtype == kBf16) return run<__nv_bfloat16>(p, ranks, s);
   return run<__half>(p, ranks, s);
