@@ -12,85 +12,83 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 
 from ._abi import check, load_library
 
-_DTYPE = None
+_NOTHING = contextlib.nullcontext()
 
 
-def _dtype(t):
-    global _DTYPE
-    if _DTYPE is None:
-        import torch
-
-        _DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-    return _DTYPE.get(t.dtype, -1)
-
-
-def _launch_on(device, stream):
-    """(a context that makes `device` and `stream` current, the stream's handle)."""
+@functools.lru_cache(maxsize=None)
+def _codes():
+    """tree_attn_dtype of torch's types."""
     import torch
 
-    index = device.index
+    return {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _index(name, t):
+    """The CUDA device's index of a tensor."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return index
+
+
+def _launch_on(index, stream):
+    """(a context that makes the device and the stream current, the stream's handle)."""
+    import torch
+
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(index)
-        if index == torch.cuda.current_device():
-            return contextlib.nullcontext(), handle
-        return torch.cuda.device(index), handle
+        return (_NOTHING if index == torch._C._cuda_getDevice() else torch.cuda.device(index)), handle
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    if stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        stream = torch.cuda.ExternalStream(int(stream), device=torch.device("cuda", index))
+    if stream.device_index != index:
+        raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on cuda:{index}")
     return torch.cuda.stream(stream), stream.cuda_stream
 
 
-def _ints(name, t, shape, device):
-    import torch
-
-    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor on {device}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} shape {tuple(t.shape)} != {shape}")
+def _vector(name, t, n, index, kind):
+    """Address of a contiguous tensor of n elements."""
+    if t.dtype is not kind or t.get_device() != index or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {kind} tensor of {n} on cuda:{index}, not {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _status(t, device):
-    return None if t is None else _ints("status", t, (1,), device)
+def _table(t, rows, index, kind):
+    """Address, row stride and width of a block table."""
+    if t.dtype is not kind or t.get_device() != index or t.dim() != 2:
+        raise ValueError(f"block_table must be a 2-d {kind} tensor on cuda:{index}")
+    n, width = t.shape
+    stride = t.stride(0)
+    if n != rows:
+        raise ValueError(f"block_table has {n} rows for {rows} requests")
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError("block_table must have contiguous rows")
+    return t.data_ptr(), stride if rows > 1 and stride > width else width if rows <= 1 else stride, width
 
 
-def _table(t, rows, device):
-    import torch
-
-    if t.dtype != torch.int32 or t.device != device or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"block_table must be a 2-d int32 tensor on {device} with contiguous rows")
-    if t.shape[0] != rows:
-        raise ValueError(f"block_table has {t.shape[0]} rows for {rows} requests")
-    stride = t.stride(0) if rows > 1 else t.shape[1]
-    return t.data_ptr(), max(stride, t.shape[1]) if rows <= 1 else stride, t.shape[1]
-
-
-def _cuda(name, t):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+def _pools(k_pages, v_pages, index):
+    """The pools' shape [pages, kv heads, 16, d], checked."""
+    shape = k_pages.shape
+    if _codes().get(k_pages.dtype, 2) > 1 or len(shape) != 4 or shape[2] != 16 or not k_pages.is_contiguous():
+        raise ValueError("k_pages must be a contiguous bf16 or fp16 tensor [pages, kv heads, 16, d]")
+    if (v_pages.dtype is not k_pages.dtype or v_pages.shape != shape or not v_pages.is_contiguous()
+            or v_pages.get_device() != index or k_pages.get_device() != index):
+        raise ValueError(f"v_pages must be as k_pages, {k_pages.dtype} {tuple(shape)}, both on cuda:{index}")
+    return shape
 
 
-def _pools(k_pages, v_pages, device):
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if _dtype(t) not in (0, 1) or t.device != device or not t.is_contiguous() or t.dim() != 4:
-            raise ValueError(f"{name} must be a contiguous bf16 or fp16 tensor [pages, kv heads, 16, d] on {device}")
-    if k_pages.dtype != v_pages.dtype or k_pages.shape != v_pages.shape or k_pages.shape[2] != 16:
-        raise ValueError("k_pages and v_pages must have one type and one shape [pages, kv heads, 16, d]")
-
-
-def _rows(name, t, pools):
-    """Token stride of a [tokens, heads, d] tensor whose tokens are whole rows."""
-    if t.dtype != pools.dtype or t.device != pools.device or t.dim() != 3:
-        raise ValueError(f"{name} must be a [tokens, heads, d] tensor of the pools' type and device")
-    n, h, d = t.shape
-    if d != pools.shape[3] or t.stride(2) != 1 or (h > 1 and t.stride(1) != d):
-        raise ValueError(f"{name}: each token's [heads, d={pools.shape[3]}] must be contiguous")
-    return t.stride(0) if n > 1 else h * d
+def _rows(name, t, kind, d, index):
+    """Shape and token stride of a [tokens, heads, d] tensor whose tokens are whole rows."""
+    if t.dtype is not kind or t.get_device() != index or t.dim() != 3:
+        raise ValueError(f"{name} must be a {kind} tensor [tokens, heads, {d}] on cuda:{index}")
+    shape, (stride, head, one) = t.shape, t.stride()
+    if shape[2] != d or one != 1 or (head != d and shape[1] > 1):
+        raise ValueError(f"{name}: each token's [heads, {d}] must be contiguous")
+    return shape, stride if shape[0] > 1 else shape[1] * d
 
 
 def extend_tables(lens, n_new, block_table, free_pages, n_free, max_new, position_base=0, status=None, stream=None):
@@ -102,43 +100,51 @@ def extend_tables(lens, n_new, block_table, free_pages, n_free, max_new, positio
     ``status`` (int32 ``[1]``, OR-ed) and ``include/tree_attn.h``."""
     import torch
 
-    device = _cuda("lens", lens)
-    b = lens.shape[0]
-    table, stride, width = _table(block_table, b, device)
-    args = (_ints("lens", lens, (b,), device), _ints("n_new", n_new, (b,), device), b, table, stride, width,
-            _ints("free_pages", free_pages, (free_pages.numel(),), device), free_pages.numel(),
-            _ints("n_free", n_free, (1,), device))
-    max_new = int(max_new)
+    index, kind = _index("lens", lens), torch.int32
+    b, cap = lens.numel(), free_pages.numel()
+    table, stride, width = _table(block_table, b, index, kind)
+    lens_at, new_at = _vector("lens", lens, b, index, kind), _vector("n_new", n_new, b, index, kind)
+    free_at, n_free_at = _vector("free_pages", free_pages, cap, index, kind), _vector("n_free", n_free, 1, index, kind)
+    status_at = None if status is None else _vector("status", status, 1, index, kind)
     if max_new < 0:
         raise ValueError("max_new is negative")
-    context, handle = _launch_on(device, stream)
+    context, handle = _launch_on(index, stream)
     with context:
         # one allocation: slots, positions, cu_new
-        out = torch.empty(2 * max_new + b + 1, dtype=torch.int32, device=device)
-        slots, positions, cu = out.split_with_sizes((max_new, max_new, b + 1))
+        out = torch.empty(2 * max_new + b + 1, dtype=kind, device=lens.device)
         at = out.data_ptr()
-        check(load_library().tree_attn_extend_tables(*args, max_new, int(position_base), at, at + 4 * max_new,
-                                                     at + 8 * max_new, _status(status, device), handle),
-              "tree_attn_extend_tables")
-    return slots, positions, cu
+        check(load_library().tree_attn_extend_tables(
+            lens_at, new_at, b, table, stride, width, free_at, cap, n_free_at, max_new, position_base, at,
+            at + 4 * max_new, at + 8 * max_new, status_at, handle), "tree_attn_extend_tables")
+        return out.split_with_sizes((max_new, max_new, b + 1))
 
 
 def append_slots(k_new, v_new, slots, k_pages, v_pages, status=None, stream=None):
     """``tree_attn_append_slots``: write ``k_new``, ``v_new`` (``[tokens, kv heads, d]``, each token's row contiguous) to
     ``slots`` (int32 ``[tokens]``, -1: none) of the page pools, in place."""
-    device = _cuda("k_pages", k_pages)
-    _pools(k_pages, v_pages, device)
-    ks, vs = _rows("k_new", k_new, k_pages), _rows("v_new", v_new, k_pages)
-    t, h, d = k_new.shape
-    if k_new.shape != v_new.shape or h != k_pages.shape[1]:
-        raise ValueError(f"k_new {tuple(k_new.shape)} and v_new {tuple(v_new.shape)} must be "
-                         f"[tokens, {k_pages.shape[1]}, {d}]")
-    slots_at = _ints("slots", slots, (t,), device)
-    context, handle = _launch_on(device, stream)
+    import torch
+
+    index, kind = _index("k_pages", k_pages), torch.int32
+    pages, hkv, _, d = _pools(k_pages, v_pages, index)
+    (t, h, _), ks = _rows("k_new", k_new, k_pages.dtype, d, index)
+    shape, vs = _rows("v_new", v_new, k_pages.dtype, d, index)
+    if h != hkv or shape[0] != t or shape[1] != hkv:
+        raise ValueError(f"k_new {tuple(k_new.shape)} and v_new {tuple(v_new.shape)} must be [tokens, {hkv}, {d}]")
+    slots_at = _vector("slots", slots, t, index, kind)
+    status_at = None if status is None else _vector("status", status, 1, index, kind)
+    context, handle = _launch_on(index, stream)
     with context:
-        check(load_library().tree_attn_append_slots(k_new.data_ptr(), v_new.data_ptr(), ks, vs, slots_at, t, h, d,
-                                                    k_pages.data_ptr(), v_pages.data_ptr(), k_pages.shape[0],
-                                                    _status(status, device), handle), "tree_attn_append_slots")
+        check(load_library().tree_attn_append_slots(
+            k_new.data_ptr(), v_new.data_ptr(), ks, vs, slots_at, t, h, d, k_pages.data_ptr(), v_pages.data_ptr(),
+            pages, status_at, handle), "tree_attn_append_slots")
+
+
+@functools.lru_cache(maxsize=4096)
+def _prefix_workspace(index, *sizes):
+    """Bytes; by the sizes alone (on this device)."""
+    need = ctypes.c_size_t(0)
+    check(load_library().tree_attn_prefix_workspace(*sizes, ctypes.byref(need)), "tree_attn_prefix_workspace")
+    return need.value
 
 
 def prefix_attention(q, k_pages, v_pages, block_table, lens, cu_new=None, prefix_pages=None, prefix_len=0,
@@ -151,39 +157,39 @@ def prefix_attention(q, k_pages, v_pages, block_table, lens, cu_new=None, prefix
     fp32 ``[tokens, q heads]`` (None without ``want_lse``)."""
     import torch
 
-    device = _cuda("q", q)
-    _pools(k_pages, v_pages, device)
-    q_stride = _rows("q", q, k_pages)
-    t, hq, d = q.shape
-    b = lens.shape[0]
-    table, stride, width = _table(block_table, b, device)
-    lens_at = _ints("lens", lens, (b,), device)
-    cu_at = None if cu_new is None else _ints("cu_new", cu_new, (b + 1,), device)
-    prefix_len, prefix_at = int(prefix_len), None
-    if prefix_pages is not None:
-        prefix_at = _ints("prefix_pages", prefix_pages, (prefix_pages.numel(),), device)
-    if prefix_len > 0 and (prefix_pages is None or prefix_pages.numel() * 16 < prefix_len):
-        raise ValueError(f"prefix_pages holds fewer than prefix_len = {prefix_len} tokens")
-    for name, x, shape, dtype in (("out", out, (t, hq, d), q.dtype), ("lse", lse, (t, hq), torch.float32)):
-        if x is not None and (x.dtype != dtype or x.device != device or not x.is_contiguous() or tuple(x.shape) != shape):
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on {device}")
-    lib = load_library()
-    context, handle = _launch_on(device, stream)
+    index, kind, dtype = _index("q", q), torch.int32, q.dtype
+    pages, hkv, _, d = _pools(k_pages, v_pages, index)
+    if dtype is not k_pages.dtype:
+        raise ValueError(f"q must be of the pools' type {k_pages.dtype}")
+    (t, hq, _), q_stride = _rows("q", q, dtype, d, index)
+    b = lens.numel()
+    table, stride, width = _table(block_table, b, index, kind)
+    lens_at = _vector("lens", lens, b, index, kind)
+    cu_at = None if cu_new is None else _vector("cu_new", cu_new, b + 1, index, kind)
+    prefix_at = None
+    if prefix_len > 0:
+        if prefix_pages is None or prefix_pages.numel() * 16 < prefix_len:
+            raise ValueError(f"prefix_pages holds fewer than prefix_len = {prefix_len} tokens")
+        prefix_at = _vector("prefix_pages", prefix_pages, prefix_pages.numel(), index, kind)
+    status_at = None if status is None else _vector("status", status, 1, index, kind)
+    if out is not None:
+        _vector("out", out, t * hq * d, index, dtype)
+    if lse is not None:
+        _vector("lse", lse, t * hq, index, torch.float32)
+    context, handle = _launch_on(index, stream)
     with context:
-        need = ctypes.c_size_t(0)
-        check(lib.tree_attn_prefix_workspace(b, t, prefix_len, hq, k_pages.shape[1], d, ctypes.byref(need)),
-              "tree_attn_prefix_workspace")
+        need = _prefix_workspace(index, b, t, prefix_len, hq, hkv, d)
         # from torch's allocator, call by call: runs on other streams or in other graphs have their own
-        work = torch.empty(need.value, dtype=torch.uint8, device=device)
+        device = q.device
+        work = torch.empty(need, dtype=torch.uint8, device=device)
         if out is None:
-            out = torch.empty((t, hq, d), dtype=q.dtype, device=device)
+            out = torch.empty((t, hq, d), dtype=dtype, device=device)
         if lse is None and want_lse:
             lse = torch.empty((t, hq), dtype=torch.float32, device=device)
-        check(lib.tree_attn_prefix_run(q.data_ptr(), q_stride, k_pages.data_ptr(), v_pages.data_ptr(), k_pages.shape[0],
-                                       table, stride, width, lens_at, cu_at, b, t, prefix_at, prefix_len, hq,
-                                       k_pages.shape[1], d, _dtype(q), float(softmax_scale), out.data_ptr(),
-                                       None if lse is None else lse.data_ptr(), _status(status, device), work.data_ptr(),
-                                       need.value, handle), "tree_attn_prefix_run")
+        check(load_library().tree_attn_prefix_run(
+            q.data_ptr(), q_stride, k_pages.data_ptr(), v_pages.data_ptr(), pages, table, stride, width, lens_at, cu_at,
+            b, t, prefix_at, prefix_len, hq, hkv, d, _codes()[dtype], softmax_scale, out.data_ptr(),
+            None if lse is None else lse.data_ptr(), status_at, work.data_ptr(), need, handle), "tree_attn_prefix_run")
     return out, lse
 
 
@@ -197,28 +203,33 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=Non
     nothing to draw."""
     import torch
 
-    device = _cuda("logits", logits)
-    code = _dtype(logits)
-    if code < 0 or logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
-        raise ValueError("logits must be a bf16, fp16 or fp32 tensor [rows, vocab] with contiguous rows")
-    rows, vocab = logits.shape
-    if u.dtype != torch.float32 or u.device != device or not u.is_contiguous() or u.dim() not in (1, 2) or u.shape[0] != rows:
-        raise ValueError(f"u must be a contiguous fp32 tensor [{rows}] or [{rows}, draws] on {device}")
-    draws = u.shape[1] if u.dim() == 2 else 1
+    index, real = _index("logits", logits), torch.float32
+    code = _codes().get(logits.dtype)
+    if code is None or logits.dim() != 2:
+        raise ValueError("logits must be a bf16, fp16 or fp32 tensor [rows, vocab]")
+    (rows, vocab), (stride, one) = logits.shape, logits.stride()
+    if one != 1 and vocab > 1:
+        raise ValueError("logits must have contiguous rows")
+    shape = u.shape
+    if len(shape) not in (1, 2) or shape[0] != rows:
+        raise ValueError(f"u must be [{rows}] or [{rows}, draws], not {tuple(shape)}")
+    u_at = _vector("u", u, u.numel(), index, real)
+    draws = shape[1] if len(shape) == 2 else 1
     args = []
-    for name, x, off, kind in (("temperature", temperature, 1.0, torch.float32), ("top_k", top_k, 0, torch.int32),
-                               ("top_p", top_p, 1.0, torch.float32), ("min_p", min_p, 0.0, torch.float32)):
-        if isinstance(x, torch.Tensor):
-            if x.dtype != kind or x.device != device or not x.is_contiguous() or x.dim() != 1 or x.shape[0] != rows:
-                raise ValueError(f"{name} must be a number or a contiguous {kind} tensor [{rows}] on {device}")
-            args += [x.data_ptr(), off]
+    for name, x, off, kind in (("temperature", temperature, 1.0, real), ("top_k", top_k, 0, torch.int32),
+                               ("top_p", top_p, 1.0, real), ("min_p", min_p, 0.0, real)):
+        if x is None:
+            args += (None, off)
+        elif isinstance(x, torch.Tensor):
+            args += (_vector(name, x, rows, index, kind), off)
         else:
-            args += [None, off if x is None else type(off)(x)]
-    context, handle = _launch_on(device, stream)
+            args += (None, type(off)(x))
+    context, handle = _launch_on(index, stream)
     with context:
-        tokens = torch.empty(u.shape, dtype=torch.int32, device=device)
-        logprobs = torch.empty(u.shape, dtype=torch.float32, device=device)
-        check(load_library().tree_attn_sample(logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, code, rows, vocab,
-                                              u.data_ptr(), draws, *args, tokens.data_ptr(), logprobs.data_ptr(), handle),
-              "tree_attn_sample")
+        device = logits.device
+        tokens = torch.empty(shape, dtype=torch.int32, device=device)
+        logprobs = torch.empty(shape, dtype=real, device=device)
+        check(load_library().tree_attn_sample(
+            logits.data_ptr(), stride if rows > 1 else vocab, code, rows, vocab, u_at, draws, *args, tokens.data_ptr(),
+            logprobs.data_ptr(), handle), "tree_attn_sample")
     return tokens, logprobs

@@ -32,7 +32,8 @@ constexpr float kGrowLog2 = 8.f;  // the running maximum is raised when a score 
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr long long kWaitLimitNs = 2000000000ll;
 
-// Last i in [0, n) with key(i) <= x, 32 probes a step (key ascending, key(0) <= x).
+// Last i in [0, n) with key(i) <= x, 32 probes a step (key ascending); an index
+// in range whatever the keys are (they come from the caller's offsets).
 template <class Key>
 __device__ __forceinline__ int find_warp(int n, long long x, int lane, Key key) {
   int lo = 0, hi = n;
@@ -40,7 +41,7 @@ __device__ __forceinline__ int find_warp(int n, long long x, int lane, Key key) 
     const int step = (hi - lo + 31) / 32;
     const int i = lo + lane * step;
     const unsigned below = __ballot_sync(0xffffffffu, i < hi && key(i) <= x);
-    lo += (__popc(below) - 1) * step;
+    lo += max(__popc(below) - 1, 0) * step;
     hi = min(hi, lo + step);
   }
   return lo;

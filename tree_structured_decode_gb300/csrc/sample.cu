@@ -9,7 +9,7 @@
 // does not depend on the order or the grid, and agrees with 64-bit arithmetic
 // except where u lies within about 2^-42 of a border.
 //
-// A row belongs to one CTA, or to a cluster of up to eight where rows are few;
+// A row belongs to one CTA, or to a cluster of two or four where rows are few;
 // what the CTAs of a cluster have to tell one another goes through distributed
 // shared memory.  A part that fits lies in shared memory; a larger one is read
 // again, by then from L2.  The passes:
@@ -46,11 +46,11 @@ constexpr int kThreads = 512;
 constexpr int kNumWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kSegments = 256;     // of a CTA's part, at most
-constexpr int kHeld = 65536;       // bytes of logits held in shared memory: two CTAs fit an SM
-constexpr int kFew = 512;          // values of a bin that are compared all with all (at most the threads of a CTA)
+constexpr int kHeld = 61440;       // bytes of logits held in shared memory: two CTAs fit an SM
+constexpr int kFew = 384;          // values of a bin that are compared all with all (at most the threads of a CTA)
 constexpr float kNear = 11.0903549f;   // the first histogram's range of exponents: 2^-16
 constexpr int kSafe = 1023;            // values of a bin whose two 32-bit sums cannot overflow
-constexpr int kMaxRanks = 8;
+constexpr int kMaxRanks = 4;
 constexpr u64 kOne = 1ull << 42;   // the weight of the largest logit
 constexpr float kLeast = -30.498476f;  // below exp(this) = 2^-44 a weight rounds to 0
 
@@ -178,13 +178,11 @@ struct Shown {
   float top;         // its largest logit, and (greedy) the first index that has it
   int first, bad;
   uint32_t kmin, kmax;
-  CountWeight total; // of the bins that it sums up
   CountWeight before;
   int bin, bin_n;
   int ties;
-  u64 kept;
-  int over;          // a bin of more than kSafe values
-  int few;           // values gathered (in the first CTA's list)
+  u64 kept, whole;   // of what is kept; of the row
+  int few[2];        // values gathered (in the first CTA's lists)
   Cut cut;
   u64 weight;        // of the prefix up to the cut
 };
@@ -208,8 +206,8 @@ struct Row {
   const T* held;     // the same in shared memory, or null
   bool vector;       // `global` may be read four logits at a time
   uint32_t *hn, *hlo, *hhi;
-  uint32_t* few_key; // [kFew]
-  int* few_at;       // [kFew] index
+  uint32_t* few_key; // [2][kFew]: for top-k and for top-p
+  int* few_at;       // [2][kFew] index
   u64* few_w;        // [kFew]
   u64* seg_sum;      // [kSegments]
   Shown* shown;
@@ -346,79 +344,65 @@ struct Row {
     }
   }
 
-  // Sums the cluster's histograms, each CTA a share of the bins, and finds the
-  // bin in which `before` plus the bins so far first reaches the target.
-  // kNever where it does not, kFull where the sums may have overflowed; else
-  // before is what lies above the bin.
+  // Finds the bin in which `before` plus the cluster's bins so far first reaches
+  // the target.  kNever where none does (before is then the sum of all), kFull
+  // where the sums may have overflowed; else before is what lies above the bin.
+  // Every CTA sums up all bins for itself: one cluster barrier behind the
+  // filling, and none for a second target.
   enum Crossing { kNever, kFound, kFull };
   __device__ Crossing cross(bool by_weight, u64 target, CountWeight& before, int& bin, int& bin_n) {
-    if (threadIdx.x == 0) shown->over = 0;
-    sync();  // every histogram is complete
-    const int share = kBins / ranks, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int per = (share + kThreads - 1) / kThreads;  // bins of a thread: 1, 2 or 4
-    const int first = rank * share + threadIdx.x * per;
-    const bool mine = (int)threadIdx.x * per < share;
-    CountWeight sum[4], all{0, 0};
+    constexpr int kPer = kBins / kThreads;
+    static_assert(kPer == 4, "a thread reads 16 bytes of a histogram");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    CountWeight sum[kPer], all{0, 0};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) sum[k] = {0, 0};
-    if (mine) {
-#pragma unroll 4
-      for (int r = 0; r < ranks; ++r) {
-        const uint32_t *n = cluster.map_shared_rank(hn, r), *lo = cluster.map_shared_rank(hlo, r),
-                       *hi = cluster.map_shared_rank(hhi, r);
+    for (int k = 0; k < kPer; ++k) sum[k] = {0, 0};
+    int most = 0;
+#pragma unroll 2
+    for (int r = 0; r < ranks; ++r) {
+      const uint4 n4 = reinterpret_cast<const uint4*>(cluster.map_shared_rank(hn, r))[tid];
+      const uint4 l4 = reinterpret_cast<const uint4*>(cluster.map_shared_rank(hlo, r))[tid];
+      const uint4 h4 = reinterpret_cast<const uint4*>(cluster.map_shared_rank(hhi, r))[tid];
+      const uint32_t n[4] = {n4.x, n4.y, n4.z, n4.w}, lo[4] = {l4.x, l4.y, l4.z, l4.w}, hi[4] = {h4.x, h4.y, h4.z, h4.w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (k < per) {
-            const uint32_t h = hi[first + k], l = lo[first + k], c = n[first + k];
-            sum[k] = sum[k] + CountWeight{safe ? ((u64)h << 32) + l : ((u64)h << 22) + (u64)(long long)(int)l, (int)c};
-            if (!safe && c > kSafe) shown->over = 1;
-          }
+      for (int k = 0; k < kPer; ++k) {
+        sum[k] = sum[k] + CountWeight{safe ? ((u64)hi[k] << 32) + lo[k] : ((u64)hi[k] << 22) + (u64)(long long)(int)lo[k], (int)n[k]};
+        most = max(most, (int)n[k]);
       }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) all = all + sum[k];
     }
-    CountWeight in = scan_warp(all, lane);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) all = all + sum[k];
+    const CountWeight in = scan_warp(all, lane);
     if (lane == 31) warp_sum[warp] = in;
-    __syncthreads();
-    CountWeight at{in.w - all.w, in.n - all.n}, total{0, 0};
+    if (tid == 0) shown->bin = -1;
+    const bool full = __syncthreads_or(!safe && most > kSafe);
+    CountWeight c{before.w + in.w - all.w, before.n + in.n - all.n}, total = before;
     for (int k = 0; k < kNumWarps; ++k) {
-      if (k == warp) at = at + total;
+      if (k < warp) c = c + warp_sum[k];
       total = total + warp_sum[k];
     }
-    if (threadIdx.x == 0) shown->total = total;
-    sync();
-    int owner = -1, over = 0;
-    CountWeight sofar = before;
-    for (int r = 0; r < ranks; ++r) over |= peer(r).over;
-    for (int r = 0; r < ranks; ++r) {
-      const CountWeight next = sofar + peer(r).total;
-      if ((by_weight ? next.w : (u64)next.n) >= target) {
-        owner = r;
-        break;
-      }
-      sofar = next;
-    }
-    if (owner == rank && mine) {
-      CountWeight c = sofar + at;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (k < per) {
-          const CountWeight next = c + sum[k];
-          const u64 lo = by_weight ? c.w : (u64)c.n, hi = by_weight ? next.w : (u64)next.n;
-          if (lo < target && hi >= target) {
-            shown->before = c;
-            shown->bin = first + k;
-            shown->bin_n = sum[k].n;
-          }
-          c = next;
-        }
+    for (int k = 0; k < kPer; ++k) {
+      const CountWeight next = c + sum[k];
+      const u64 lo = by_weight ? c.w : (u64)c.n, hi = by_weight ? next.w : (u64)next.n;
+      if (lo < target && hi >= target) {
+        shown->before = c;
+        shown->bin = kPer * tid + k;
+        shown->bin_n = sum[k].n;
+      }
+      c = next;
     }
-    sync();
-    if (over) return kFull;
-    if (owner < 0) return kNever;
-    before = peer(owner).before;
-    bin = peer(owner).bin;
-    bin_n = peer(owner).bin_n;
+    __syncthreads();
+    bin = shown->bin;
+    bin_n = shown->bin_n;
+    const CountWeight above = shown->before;
+    __syncthreads();  // warp_sum and the result may be set again
+    if (full) return kFull;
+    if (bin < 0) {
+      before = total;
+      return kNever;
+    }
+    before = above;
     return kFound;
   }
 
@@ -479,12 +463,11 @@ struct Row {
     if (threadIdx.x == 0) {
       v = 0;
       for (int w = 0; w < kNumWarps; ++w) v += warp_sum[w].w;
-      shown->kept = v;
+      shown->whole = v;
     }
     sync();
     v = 0;
-    for (int r = 0; r < ranks; ++r) v += peer(r).kept;
-    sync();  // before it is set again
+    for (int r = 0; r < ranks; ++r) v += peer(r).whole;
     return v;
   }
 
@@ -531,24 +514,26 @@ struct Row {
     CountWeight before{0, 0};
     int bin, bin_n;
     Range range{0.f, kNear};
-    if (!near) fill(range, false), near = true;
+    auto refill = [&](bool direct) {
+      sync();  // every CTA has read the bins
+      fill(range, direct);
+      sync();
+    };
+    if (!near) refill(false), near = true;
     Crossing got = cross(by_weight, target, before, bin, bin_n);
     if (got == kFull) {
       safe = true;
-      fill(range, false);
+      refill(false);
       got = cross(by_weight, target, before, bin, bin_n);
     }
-    if (got == kNever) {
-      // below it: what is above are all of the first bins
-      for (int r = 0; r < ranks; ++r) before = before + peer(r).total;
+    if (got == kNever) {  // below it: what is above are all of the first bins
       range = {kNear, -kLeast};
-      sync();
-      fill(range, true);  // most logits lie there: they are not collected
+      refill(true);  // most logits lie there: they are not collected
       near = false;
       got = cross(by_weight, target, before, bin, bin_n);
       if (got == kFull) {
         safe = true;
-        fill(range, true);
+        refill(true);
         got = cross(by_weight, target, before, bin, bin_n);
       }
       if (got == kNever) return false;
@@ -558,8 +543,11 @@ struct Row {
     // pass 3
     uint32_t kmin = 0xffffffffu, kmax = 0;
     Shown& lead = peer(0);
-    uint32_t* list_key = cluster.map_shared_rank(few_key, 0);
-    int* list_at = cluster.map_shared_rank(few_at, 0);
+    const int which = by_weight ? 1 : 0;  // lists of their own: some CTA may still read the first
+    uint32_t* my_key = few_key + which * kFew;
+    int* my_at = few_at + which * kFew;
+    uint32_t* list_key = cluster.map_shared_rank(my_key, 0);
+    int* list_at = cluster.map_shared_rank(my_at, 0);
     int hi_sum = 0, lo_sum = 0;
     Queue q{queue, queue_at, 0};
     auto sort = [&](float v, int i) {
@@ -570,7 +558,7 @@ struct Row {
         kmin = min(kmin, key);
         kmax = max(kmax, key);
         if (few) {
-          const int n = atomicAdd(&lead.few, 1);
+          const int n = atomicAdd(&lead.few[which], 1);
           list_key[n] = key;
           list_at[n] = v0 + i;
         }
@@ -593,46 +581,44 @@ struct Row {
         });
     q.flush(sort);
     if (few) {
-      sync();  // the list is complete
-      if (rank == 0) {
-        const int t = threadIdx.x;
-        if (t < bin_n) few_w[t] = weight(of_key(few_key[t]));
-        __syncthreads();
-        if (t < bin_n) {
-          const uint32_t key = few_key[t];
-          const int at = few_at[t];
-          CountWeight above = before;
-          int same = 0, lower = 0;  // values equal to this, those of lower index
-          for (int j = 0; j < bin_n; ++j) {
-            const uint32_t k = few_key[j];
-            if (k > key) above = above + CountWeight{few_w[j], 1};
-            same += k == key;
-            lower += k == key && few_at[j] < at;
-          }
-          const u64 w = few_w[t];
-          const u64 lo = by_weight ? above.w : (u64)above.n;
-          const u64 hi = by_weight ? above.w + same * w : (u64)above.n + same;
-          if (lo < target && hi >= target) {  // the prefix ends among the values equal to this
-            const u64 need = by_weight ? (target - lo + w - 1) / w : target - lo;
-            if ((u64)lower + 1 == need) {
-              shown->cut = {key, at};
-              shown->weight = above.w + need * w;
-            }
-          }
-        }
-        if (t == 0) shown->few = 0;
+      sync();  // the list is complete; every CTA works it out
+      const int t = threadIdx.x;
+      uint32_t key = 0;
+      int at = 0;
+      u64 w = 0;
+      if (t < bin_n) {
+        key = list_key[t];
+        at = list_at[t];
+        w = weight(of_key(key));
+        if (rank) my_key[t] = key, my_at[t] = at;
+        few_w[t] = w;
       }
-      sync();
-      cut = lead.cut;
-      cut_weight = lead.weight;
-      if (sums) {  // the bin's kept values
-        const u64* list_w = cluster.map_shared_rank(few_w, 0);
-        const int t = threadIdx.x;
-        if (t < bin_n) {
-          const uint32_t key = list_key[t];
-          const int at = list_at[t] - v0;
-          if (key >= least && cut.has(key, v0 + at) && at >= 0 && at < size) atomicAdd(seg_sum + at / seg, list_w[t]);
+      __syncthreads();
+      if (t < bin_n) {
+        CountWeight above = before;
+        int same = 0, lower = 0;  // values equal to this, those of lower index
+        for (int j = 0; j < bin_n; ++j) {
+          const uint32_t k = my_key[j];
+          if (k > key) above = above + CountWeight{few_w[j], 1};
+          same += k == key;
+          lower += k == key && my_at[j] < at;
         }
+        const u64 lo = by_weight ? above.w : (u64)above.n;
+        const u64 hi = by_weight ? above.w + same * w : (u64)above.n + same;
+        if (lo < target && hi >= target) {  // the prefix ends among the values equal to this
+          const u64 need = by_weight ? (target - lo + w - 1) / w : target - lo;
+          if ((u64)lower + 1 == need) {
+            shown->cut = {key, at};
+            shown->weight = above.w + need * w;
+          }
+        }
+      }
+      __syncthreads();
+      cut = shown->cut;
+      cut_weight = shown->weight;
+      if (sums) {  // the bin's kept values
+        if (t < bin_n && key >= least && cut.has(key, at) && at >= v0 && at - v0 < size)
+          atomicAdd(seg_sum + (at - v0) / seg, w);
         summed = true;
       }
       return true;
@@ -654,6 +640,7 @@ struct Row {
     while (kmin != kmax) {
       const uint32_t span = kmax - kmin;
       const int shift = max(0, 32 - __clz(span) - 11);
+      sync();  // every CTA has read the bins
       clear();
       near = false;
       safe = true;
@@ -667,6 +654,7 @@ struct Row {
             }
           },
           [](int) {});
+      sync();
       if (cross(by_weight, target, before, bin, bin_n) != kFound) return false;
       kmax -= (uint32_t)bin << shift;
       const uint32_t width = (1u << shift) - 1;
@@ -753,8 +741,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   u64* seg_sum = reinterpret_cast<u64*>(table + 1024);
   u64* few_w = seg_sum + kSegments;
   uint32_t* few_key = reinterpret_cast<uint32_t*>(few_w + kFew);
-  int* few_at = reinterpret_cast<int*>(few_key + kFew);
-  uint32_t* hist = reinterpret_cast<uint32_t*>(few_at + kFew);
+  int* few_at = reinterpret_cast<int*>(few_key + 2 * kFew);
+  uint32_t* hist = reinterpret_cast<uint32_t*>(few_at + 2 * kFew);
   T* held = reinterpret_cast<T*>(hist + 3 * kBins);
   const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int row = blockIdx.x / ranks;
@@ -769,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const float min_p = p.min_p ? p.min_p[row] : p.min_p_all;
   if (tid == 0) {  // 64-bit arithmetic is slow here: once a CTA
     s_bad = 0;
-    s_shown.few = 0;
+    s_shown.few[0] = s_shown.few[1] = 0;
     s_c = 1.0 / (double)temperature;
     s_least = min_p > 0.f ? (double)temperature * log((double)fminf(min_p, 1.f)) : 0.0;
   }
@@ -881,14 +869,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   bool summed = false;
   if (use_k || use_p) {
     u64 total = R.fill({0.f, kNear}, !use_k);
+    if (use_k)
+      R.sync();  // every histogram is complete
+    else
+      total = R.total_of(total);  // as well
     bool near = true;
     Cut o;
     u64 w = 0;
     if (use_k && R.select(false, (u64)top_k, least, !use_p, o, w, near, summed)) shorten(o);
     if (use_p) {
-      if (use_k && w == 0)  // fewer than k have a weight: all of it counts
-        R.sync(), total = R.fill({0.f, kNear}, true), near = true;
-      total = w ? w : R.total_of(total);
+      if (use_k && w == 0) {  // fewer than k have a weight: all of it counts
+        R.sync();
+        total = R.total_of(R.fill({0.f, kNear}, true));
+        near = true;
+      }
+      if (w) total = w;
       u64 want = 0;
       if (lane == 0) want = max((u64)ceil((double)fmaxf(top_p, 0.f) * (double)total), 1ull);
       want = __shfl_sync(0xffffffffu, want, 0);
@@ -975,7 +970,7 @@ template <typename T>
 cudaError_t run(SampleParams p, int ranks, cudaStream_t s) {
   p.slice = ((p.vocab + ranks - 1) / ranks + 127) / 128 * 128;
   p.held = p.slice * sizeof(T) <= kHeld;
-  const size_t smem = 1024 * 8 + kSegments * 8 + kFew * 16 + 3 * kBins * 4 + (p.held ? p.slice * sizeof(T) : 0);
+  const size_t smem = 1024 * 8 + kSegments * 8 + kFew * 24 + 3 * kBins * 4 + (p.held ? p.slice * sizeof(T) : 0);
   cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
