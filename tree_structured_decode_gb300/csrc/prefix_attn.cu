@@ -32,21 +32,6 @@ constexpr float kGrowLog2 = 8.f;  // the running maximum is raised when a score 
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr long long kWaitLimitNs = 2000000000ll;
 
-// Last i in [0, n) with key(i) <= x, 32 probes a step (key ascending); an index
-// in range whatever the keys are (they come from the caller's offsets).
-template <class Key>
-__device__ __forceinline__ int find_warp(int n, long long x, int lane, Key key) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32;
-    const int i = lo + lane * step;
-    const unsigned below = __ballot_sync(0xffffffffu, i < hi && key(i) <= x);
-    lo += max(__popc(below) - 1, 0) * step;
-    hi = min(hi, lo + step);
-  }
-  return lo;
-}
-
 // Batches without a prefix kernel that does it on the side, or with many
 // requests.
 __global__ void __launch_bounds__(1024) prefix_schedule_kernel(const Args a) {
@@ -194,7 +179,7 @@ __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
       const Request q = request(lo);
       const long long in = x - q.p0;
       const long long seg = quotient(in, q.np);
-      const int tiles = tiles_of(q, p.gqa, L.tile_rows);
+      const int tiles = tiles_of(q, p.gqa, L);
       r.b = lo;
       r.head = (int)quotient(seg, tiles);
       r.tile = (int)(seg - (long long)r.head * tiles);
@@ -423,128 +408,208 @@ __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
 }
 
 // ------------------------------------------------------------- merge
+// Folds up to 16 pieces' {m, l} (one a lane of half a warp) into a row's running
+// maximum and sum; returns this lane's piece's factor, a0 what was there before's.
+__device__ __forceinline__ float fold_ml(const float2 ml, float& M, float& den, float& a0) {
+  float m_new = ml.x;
+#pragma unroll
+  for (int off = 8; off; off >>= 1) m_new = fmaxf(m_new, __shfl_xor_sync(0xffffffffu, m_new, off));
+  m_new = fmaxf(M, m_new);
+  const float base = m_new == -INFINITY ? 0.f : m_new;
+  a0 = ptx::ex2(M - base);
+  const float w = ptx::ex2(ml.x - base);
+  float sum = w * ml.y;
+#pragma unroll
+  for (int off = 8; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  den = den * a0 + sum;
+  M = m_new;
+  return w;
+}
+// Adds the O rows of `all` pieces (lane i of half a warp holds piece i's address,
+// 0 for none, and factor), four loads in flight.
+template <int E>
+__device__ __forceinline__ void fold_o(unsigned long long at, float w, int all, float (&acc)[E]) {
+  const int lane = threadIdx.x & 31, in = lane & 15;
+  for (int j = 0; j < all; j += 4) {
+    float4 v[4][E / 4];
+    float wj[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4* s = reinterpret_cast<const float4*>(__shfl_sync(0xffffffffu, at, (lane & 16) + min(j + i, 15)));
+      wj[i] = __shfl_sync(0xffffffffu, w, (lane & 16) + min(j + i, 15));
+      const bool mine = j + i < 16 && s != nullptr;
+      if (!mine) wj[i] = 0.f;
+#pragma unroll
+      for (int e = 0; e < E / 4; ++e) v[i][e] = mine ? __ldcg(s + 16 * e + in) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < E / 4; ++e) {
+        acc[4 * e] = fmaf(v[i][e].x, wj[i], acc[4 * e]);
+        acc[4 * e + 1] = fmaf(v[i][e].y, wj[i], acc[4 * e + 1]);
+        acc[4 * e + 2] = fmaf(v[i][e].z, wj[i], acc[4 * e + 2]);
+        acc[4 * e + 3] = fmaf(v[i][e].w, wj[i], acc[4 * e + 3]);
+      }
+  }
+}
+__device__ __forceinline__ float inverse(float den) {
+  return den > 0.f ? 1.f / den : den == 0.f ? 0.f : den;  // a NaN stays one
+}
+
 // Joins a row's (token, q head) pieces of both lines, where the line kernel has
-// not.  Bound by the latency of its chain of loads (request, {m, l}, O), which
-// the rows in flight hide where they are many: half a warp takes one then.  Few
-// rows have many pieces: a block takes one, its half-warps every 16th piece.
-template <int D, bool kHalf, bool kBlock>
-__global__ void __launch_bounds__(256) prefix_merge_kernel(const Args a) {
+// not: half a warp a row, a block 16 rows of a kv head (which share their pieces
+// of the prefix).  What bounds it is the chain of loads (request, then {m, l} and
+// O at once), so up to four pieces are read together.
+constexpr int kMergeRows = 16;
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(256, 3) prefix_merge_kernel(const Args a) {
   const PrefixParams& p = a.p;
   constexpr int E = D / 16;  // columns of a lane
-  constexpr int kParts = kBlock ? 16 : 1;
-  const int lane = threadIdx.x & 31, in = lane & 15, half = threadIdx.x >> 4;
-  const long long rows = (long long)p.n_tokens * p.hq;
-  const long long want = kBlock ? (long long)blockIdx.x : (long long)blockIdx.x * 16 + half;
+  const int in = threadIdx.x & 15, half = threadIdx.x >> 4;
+  const int rows = p.n_tokens * p.gqa;  // of a kv head
+  const int chunks = (rows + kMergeRows - 1) / kMergeRows;
+  const int kvh = blockIdx.x / chunks, first = (blockIdx.x - kvh * chunks) * kMergeRows;
+  const int row = first + half;
+  // the prefix's pieces of the block's first row; the tokens of some request
+  __shared__ long long s_w0;
+  __shared__ int s_n, s_in, s_queries;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!kBlock && want - (half & 1) >= rows) return;  // the whole warp
-  const long long row = min(want, rows - 1);
-  const int tok = (int)((uint32_t)row / (uint32_t)p.hq), h = (int)((uint32_t)row % (uint32_t)p.hq);
+  if (threadIdx.x == 0) {
+    const Cuts cuts = prefix_cuts(a);
+    const int tok = first / p.gqa;
+    const Pieces q = pieces_of(a.line[1], cuts.one, cuts.run, p, tok, kvh, first - tok * p.gqa);
+    s_w0 = q.w0;
+    s_n = q.n;
+    s_in = q.in;
+    s_queries = cuts.one.n;
+  }
+  const int tok = row / p.gqa, in_head = row - tok * p.gqa;
+  const long long at_row = (long long)tok * p.hq + kvh * p.gqa + in_head;
+  const long long run = p.n_req > 0 ? a.line[0].sizes[1] : 1;
+  __syncthreads();
+  if (row >= rows) return;
   int b = tok;
-  if (p.cu) {
-    auto first = [&](int i) { return (long long)a.line[0].req[i].tok0; };
-    const int tok0 = __shfl_sync(0xffffffffu, tok, 0), tok1 = __shfl_sync(0xffffffffu, tok, 31);
-    b = find_warp(p.n_req, tok0, lane, first);
-    if (tok1 != tok0) {
-      const int b1 = find_warp(p.n_req, tok1, lane, first);
-      if (lane >= 16) b = b1;
-    }
+  if (p.cu) b = tok < s_queries ? a.request_of[tok] : -1;
+  Request own{};
+  if ((unsigned)b < (unsigned)p.n_req) own = a.line[0].req[b];
+  Pieces po{&a.line[0], 0, at_row, 0, 0}, pp{&a.line[1], 0, at_row, 0, 0};
+  if (tok >= own.tok0 && tok < own.tok0 + own.n) {
+    if (tok < s_queries) pp = Pieces{&a.line[1], s_w0, at_row, s_n, s_in + half};  // else cu is broken
+    po = pieces_of(a.line[0], own, run, p, tok, kvh, in_head);
   }
-  const Request own = a.line[0].req[b];
-  const bool there = p.n_req > 0 && tok >= own.tok0 && tok < own.tok0 + own.n;
-  Pieces po{}, pp{};
-  if (there) {
-    if (p.prefix_len > 0) {
-      const Cuts cuts = prefix_cuts(a);
-      if (tok < cuts.one.n) pp = pieces_of(a.line[1], cuts.one, cuts.run, p, tok, h);  // else cu is broken
-    }
-    po = pieces_of(a.line[0], own, a.line[0].sizes[1], p, tok, h);
-  }
+  if (a.join && po.n == 1) return;  // done by the line kernel
   const int n = po.n + pp.n;
-  const bool done = a.join && po.n == 1;  // by the line kernel
-  int most = done ? 0 : n;
-  most = max(most, __shfl_xor_sync(0xffffffffu, most, 16));
   float M = -INFINITY, den = 0.f, acc[E] = {};
-  for (int k0 = 0; k0 < most; k0 += 16 * kParts) {
-    // this half-warp's pieces are k0 + part + kParts i; lane i reads its {m, l}
-    const int k = k0 + (kBlock ? half : 0) + kParts * in;
-    float2 ml = make_float2(-INFINITY, 0.f);
-    const float* src = a.line[0].row_o;  // anything that may be read
-    if (k < po.n)
-      ml = po.ml(k), src = po.o(k, D);
-    else if (k < n)
-      ml = pp.ml(k - po.n), src = pp.o(k - po.n, D);
-    float m_new = ml.x;
+  for (int k0 = 0; k0 < n; k0 += 4) {
+    float2 ml[4];
+    float4 v[4][E / 4];
 #pragma unroll
-    for (int off = 8; off; off >>= 1) m_new = fmaxf(m_new, __shfl_xor_sync(0xffffffffu, m_new, off));
-    m_new = fmaxf(M, m_new);
+    for (int i = 0; i < 4; ++i) {
+      const int k = k0 + i;
+      ml[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int e = 0; e < E / 4; ++e) v[i][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k < n) {
+        const bool mine = k < po.n;
+        ml[i] = mine ? po.ml(k) : pp.ml(k - po.n);
+        const float4* src = reinterpret_cast<const float4*>(mine ? po.o(k, D) : pp.o(k - po.n, D));
+#pragma unroll
+        for (int e = 0; e < E / 4; ++e) v[i][e] = __ldcg(src + 16 * e + in);
+      }
+    }
+    const float m_new = fmaxf(fmaxf(M, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
     const float base = m_new == -INFINITY ? 0.f : m_new;
-    const float a0 = ptx::ex2(M - base), w = ptx::ex2(ml.x - base);
-    float sum = w * ml.y;
-#pragma unroll
-    for (int off = 8; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    den = den * a0 + sum;
+    const float a0 = ptx::ex2(M - base);
     M = m_new;
+    den *= a0;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] *= a0;
-    const int all = min(16, (most - k0 + kParts - 1) / kParts);
-    const unsigned long long at = k < n ? reinterpret_cast<unsigned long long>(src) : 0ull;
-    for (int j = 0; j < all; j += 4) {
-      float4 v[4][E / 4];
-      float wj[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4* s = reinterpret_cast<const float4*>(__shfl_sync(0xffffffffu, at, (lane & 16) + min(j + i, 15)));
-        wj[i] = __shfl_sync(0xffffffffu, w, (lane & 16) + min(j + i, 15));
-        const bool mine = j + i < 16 && s != nullptr;
-        if (!mine) wj[i] = 0.f;
+    for (int i = 0; i < 4; ++i) {
+      const float w = ptx::ex2(ml[i].x - base);
+      den = fmaf(w, ml[i].y, den);
 #pragma unroll
-        for (int e = 0; e < E / 4; ++e) v[i][e] = mine ? __ldcg(s + 16 * e + in) : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int e = 0; e < E / 4; ++e) {
+        acc[4 * e] = fmaf(v[i][e].x, w, acc[4 * e]);
+        acc[4 * e + 1] = fmaf(v[i][e].y, w, acc[4 * e + 1]);
+        acc[4 * e + 2] = fmaf(v[i][e].z, w, acc[4 * e + 2]);
+        acc[4 * e + 3] = fmaf(v[i][e].w, w, acc[4 * e + 3]);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < E / 4; ++e) {
-          acc[4 * e] = fmaf(v[i][e].x, wj[i], acc[4 * e]);
-          acc[4 * e + 1] = fmaf(v[i][e].y, wj[i], acc[4 * e + 1]);
-          acc[4 * e + 2] = fmaf(v[i][e].z, wj[i], acc[4 * e + 2]);
-          acc[4 * e + 3] = fmaf(v[i][e].w, wj[i], acc[4 * e + 3]);
-        }
     }
   }
-  if constexpr (kBlock) {
-    __shared__ float2 s_ml[16];
-    __shared__ float s_o[16][D];
-    if (in == 0) s_ml[half] = make_float2(M, den);
+  const float inv = inverse(den);
 #pragma unroll
-    for (int e = 0; e < E; ++e) s_o[half][64 * (e / 4) + 4 * in + e % 4] = acc[e];
-    __syncthreads();
-    if (done || threadIdx.x >= 32) return;
-    M = -INFINITY;
-    for (int k = 0; k < 16; ++k) M = fmaxf(M, s_ml[k].x);
-    const float base = M == -INFINITY ? 0.f : M;
-    den = 0.f;
-    float o[D / 32] = {};
-    for (int k = 0; k < 16; ++k) {
-      const float w = ptx::ex2(s_ml[k].x - base);
-      den += w * s_ml[k].y;
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) o[e] = fmaf(w, s_o[k][lane * (D / 32) + e], o[e]);
-    }
-    const float inv = den > 0.f ? 1.f / den : den == 0.f ? 0.f : den;  // a NaN stays one
-#pragma unroll
-    for (int e = 0; e < D / 32; e += 2)
-      *reinterpret_cast<uint32_t*>(p.out + row * D + lane * (D / 32) + e) = pack2<kHalf>(o[e] * inv, o[e + 1] * inv);
-    if (lane == 0 && p.lse) p.lse[row] = den == 0.f ? -INFINITY : (M + log2f(den)) * kLn2;
-  } else {
-    if (done || want >= rows) return;
-    const float inv = den > 0.f ? 1.f / den : den == 0.f ? 0.f : den;
-#pragma unroll
-    for (int e = 0; e < E / 4; ++e)
-      *reinterpret_cast<uint2*>(p.out + row * D + 64 * e + 4 * in) =
-          make_uint2(pack2<kHalf>(acc[4 * e] * inv, acc[4 * e + 1] * inv),
-                     pack2<kHalf>(acc[4 * e + 2] * inv, acc[4 * e + 3] * inv));
-    if (in == 0 && p.lse) p.lse[row] = den == 0.f ? -INFINITY : (M + log2f(den)) * kLn2;
+  for (int e = 0; e < E / 4; ++e)
+    *reinterpret_cast<uint2*>(p.out + at_row * D + 64 * e + 4 * in) =
+        make_uint2(pack2<kHalf>(acc[4 * e] * inv, acc[4 * e + 1] * inv),
+                   pack2<kHalf>(acc[4 * e + 2] * inv, acc[4 * e + 3] * inv));
+  if (in == 0 && p.lse) p.lse[at_row] = den == 0.f ? -INFINITY : (M + log2f(den)) * kLn2;
+}
+
+// The same for few rows, which have many pieces: a block a row, its half-warps
+// every 16th piece.
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(256) prefix_merge_row_kernel(const Args a) {
+  const PrefixParams& p = a.p;
+  constexpr int E = D / 16;
+  const int lane = threadIdx.x & 31, in = lane & 15, half = threadIdx.x >> 4;
+  const long long row = blockIdx.x;
+  const int tok = (int)((uint32_t)row / (uint32_t)p.hq), h = (int)((uint32_t)row % (uint32_t)p.hq);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  Pieces po{}, pp{};
+  const Cuts cuts = p.prefix_len > 0 || p.cu ? prefix_cuts(a) : Cuts{};
+  int b = tok;
+  if (p.cu) b = tok < cuts.one.n ? a.request_of[tok] : -1;
+  Request own{};
+  if ((unsigned)b < (unsigned)p.n_req) own = a.line[0].req[b];
+  if (tok >= own.tok0 && tok < own.tok0 + own.n) {
+    const int kvh = h / p.gqa;
+    if (p.prefix_len > 0 && tok < cuts.one.n)
+      pp = pieces_of(a.line[1], cuts.one, cuts.run, p, tok, kvh, h - kvh * p.gqa);
+    po = pieces_of(a.line[0], own, a.line[0].sizes[1], p, tok, kvh, h - kvh * p.gqa);
   }
+  const int n = po.n + pp.n;
+  if (a.join && po.n == 1) return;  // done by the line kernel (the whole block)
+  float M = -INFINITY, den = 0.f, acc[E] = {};
+  for (int k0 = 0; k0 < n; k0 += 256) {
+    // this half-warp's pieces are k0 + half + 16 i; lane i reads its {m, l}
+    const int k = k0 + half + 16 * in;
+    float2 x = make_float2(-INFINITY, 0.f);
+    unsigned long long at = 0;
+    if (k < n) {
+      x = k < po.n ? po.ml(k) : pp.ml(k - po.n);
+      at = reinterpret_cast<unsigned long long>(k < po.n ? po.o(k, D) : pp.o(k - po.n, D));
+    }
+    float a0;
+    const float w = fold_ml(x, M, den, a0);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= a0;
+    fold_o<E>(at, w, min(16, (n - k0 + 15) / 16), acc);
+  }
+  __shared__ float2 s_ml[16];
+  __shared__ float s_o[16][D];
+  if (in == 0) s_ml[half] = make_float2(M, den);
+#pragma unroll
+  for (int e = 0; e < E; ++e) s_o[half][64 * (e / 4) + 4 * in + e % 4] = acc[e];
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  M = -INFINITY;
+  for (int k = 0; k < 16; ++k) M = fmaxf(M, s_ml[k].x);
+  const float base = M == -INFINITY ? 0.f : M;
+  den = 0.f;
+  float o[D / 32] = {};
+  for (int k = 0; k < 16; ++k) {
+    const float w = ptx::ex2(s_ml[k].x - base);
+    den += w * s_ml[k].y;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) o[e] = fmaf(w, s_o[k][lane * (D / 32) + e], o[e]);
+  }
+  const float inv = inverse(den);
+#pragma unroll
+  for (int e = 0; e < D / 32; e += 2)
+    *reinterpret_cast<uint32_t*>(p.out + row * D + lane * (D / 32) + e) = pack2<kHalf>(o[e] * inv, o[e + 1] * inv);
+  if (lane == 0 && p.lse) p.lse[row] = den == 0.f ? -INFINITY : (M + log2f(den)) * kLn2;
 }
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
@@ -588,12 +653,14 @@ size_t lay_out(const PrefixParams& p, uint8_t* base, Args* a) {
       L.req = reinterpret_cast<Request*>(take(sizeof(Request) * (size_t)(L.n_req + 1)));
       L.sizes = reinterpret_cast<long long*>(take(16));
     }
+    for (L.tile_shift = 0; (1 << L.tile_shift) < L.tile_rows;) ++L.tile_shift;
     const size_t pieces = 2 * (size_t)L.runs * L.tile_rows;
     L.piece_o = reinterpret_cast<float*>(take(pieces * p.d * 4));
     L.piece_ml = reinterpret_cast<float2*>(take(pieces * 8));
     L.row_o = reinterpret_cast<float*>(take(rows * p.d * 4));
     L.row_ml = reinterpret_cast<float2*>(take(rows * 8));
   }
+  a->request_of = reinterpret_cast<int32_t*>(take(sizeof(int32_t) * (size_t)p.n_tokens));
   // (Joining a segment with the prefix's pieces as well, in the line kernel's
   // epilogue, was slower: eight warps an SM wait for those loads, 105 to 168 us
   // at 512 requests of 64 heads, against 9 us less in the merge.)
@@ -660,13 +727,14 @@ cudaError_t run(const Args& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   const long long rows = (long long)p.n_tokens * p.hq;
   const bool block = rows <= (long long)kBlockRows * p.num_sms;
-  cfg.gridDim = dim3((unsigned)(block ? rows : (rows + 15) / 16));
+  const long long chunks = ((long long)p.n_tokens * p.gqa + kMergeRows - 1) / kMergeRows;
+  cfg.gridDim = dim3((unsigned)(block ? rows : chunks * p.hkv));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return block ? cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, kHalf, true>, a)
-               : cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, kHalf, false>, a);
+  return block ? cudaLaunchKernelEx(&cfg, prefix_merge_row_kernel<D, kHalf>, a)
+               : cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, kHalf>, a);
 }
 
 }  // namespace

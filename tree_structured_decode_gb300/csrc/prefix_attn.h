@@ -9,6 +9,7 @@
 
 namespace ta {
 
+constexpr int kTileTokens = 128;  // keys of a step of the tensor-core tiles
 constexpr int kMinPages = 4;    // shortest run of a warp of the line kernel
 
 // What the kernels know of a request, checked: its first token and row count
@@ -36,19 +37,20 @@ struct Line {
   float2* row_ml;
   const int32_t* table;
   long long table_stride;
-  int n_req, width, causal, tile_rows, step;  // step: keys
+  int n_req, width, causal, tile_rows, tile_shift, step;  // tile_rows = 1 << tile_shift; step: keys
   int runs;           // warps (or CTAs) that the line is cut for
 };
 
 struct Args {
   PrefixParams p;
   Line line[2];  // own tokens, prefix
+  int32_t* request_of;  // [tokens] (of tokens that are some request's)
   int side_schedule;  // the prefix kernel checks and sums up the requests on the side
   int join;           // own segments in one run are final
 };
 
-__device__ __forceinline__ int tiles_of(const Request& r, int gqa, int tile_rows) {
-  return (r.n * gqa + tile_rows - 1) / tile_rows;
+__device__ __forceinline__ int tiles_of(const Request& r, int gqa, const Line& L) {
+  return (r.n * gqa + L.tile_rows - 1) >> L.tile_shift;
 }
 
 // The prefix's line: one request of all queries.  Tokens of no request (the
@@ -65,8 +67,8 @@ __device__ __forceinline__ Cuts prefix_cuts(const Args& a) {
   c.one.len = p.prefix_len;
   c.one.tok0 = 0;
   c.one.n = p.cu ? min(max(p.cu[p.n_req], 0), p.n_tokens) : p.n_tokens;
-  c.one.np = (p.prefix_len + L.step - 1) / max(L.step, 1);
-  c.total = (long long)tiles_of(c.one, p.gqa, L.tile_rows) * p.hkv * c.one.np;
+  c.one.np = L.step == kPage ? (p.prefix_len + kPage - 1) / kPage : (p.prefix_len + kTileTokens - 1) / kTileTokens;
+  c.total = (long long)tiles_of(c.one, p.gqa, L) * p.hkv * c.one.np;
   c.run = max(quotient(c.total + L.runs - 1, L.runs), L.step == kPage ? (long long)kMinPages : 1ll);
   return c;
 }
@@ -94,17 +96,19 @@ struct Pieces {
     return __ldcg(n == 1 ? L->row_ml + row : L->piece_ml + slot(k));
   }
 };
-// Pieces of token tok's q head h in line L, whose request there is r.
+// Pieces of token tok's q head h (of kv head kvh, its in-th) in line L, whose
+// request there is r.
 __device__ __forceinline__ Pieces pieces_of(const Line& L, const Request& r, long long run,
-                                            const PrefixParams& p, int tok, int h) {
-  Pieces q{&L, 0, (long long)tok * p.hq + h, 0, 0};
+                                            const PrefixParams& p, int tok, int kvh, int in_head) {
+  Pieces q{&L, 0, (long long)tok * p.hq + kvh * p.gqa + in_head, 0, 0};
   if (r.np == 0) return q;
-  const int in = (tok - r.tok0) * p.gqa + h % p.gqa;
-  const long long seg = (long long)(h / p.gqa) * tiles_of(r, p.gqa, L.tile_rows) + in / L.tile_rows;
+  const int in = (tok - r.tok0) * p.gqa + in_head;
+  const long long seg = (long long)kvh * tiles_of(r, p.gqa, L) + (in >> L.tile_shift);
   const long long first = r.p0 + seg * r.np;
   q.w0 = quotient(first, run);
-  q.n = (int)(quotient(first + r.np - 1, run) - q.w0) + 1;
-  q.in = in % L.tile_rows;
+  const long long past = first - q.w0 * run + r.np - 1;  // the last step, from the first run's start
+  q.n = past < run ? 1 : (int)quotient(past, run) + 1;
+  q.in = in & (L.tile_rows - 1);
   return q;
 }
 
@@ -135,7 +139,7 @@ __device__ inline void schedule_own(const Args& a, int tid, int threads, int bar
     return r;
   };
   auto work = [&](const Request& r) {
-    return (long long)tiles_of(r, p.gqa, a.line[0].tile_rows) * r.np * p.hkv;
+    return (long long)tiles_of(r, p.gqa, a.line[0]) * r.np * p.hkv;
   };
   long long mine = 0;
   for (int b = b0; b < b1; ++b) mine += work(request(b));
@@ -157,6 +161,8 @@ __device__ inline void schedule_own(const Args& a, int tid, int threads, int bar
     r.p0 = at;
     a.line[0].req[b] = r;
     at += work(r);
+    if (p.cu)
+      for (int t = r.tok0; t < r.tok0 + r.n; ++t) a.request_of[t] = b;
   }
   if (bad && p.status) atomicOr(p.status, bad);
   if (tid == 0) {
@@ -167,7 +173,6 @@ __device__ inline void schedule_own(const Args& a, int tid, int threads, int bar
 
 // Most query rows of a tile of the tensor-core prefix kernel: two of 128.
 constexpr int kTileRows = 256;
-constexpr int kTileTokens = 128;  // keys of a step
 // The prefix's pieces by tcgen05 (a.line[1] cut in steps of kTileTokens keys).
 cudaError_t launch_prefix_tiles(const Args& a, const CUtensorMap& mk_half, const CUtensorMap& mv,
                                 cudaStream_t s);
