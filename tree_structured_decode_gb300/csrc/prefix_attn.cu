@@ -138,8 +138,10 @@ __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
   // the next kernel may set itself up while this one runs
   asm volatile("griddepcontrol.launch_dependents;");
   if (which == 0) {
-    // the schedule and the prefix's pieces are the kernels' before this one
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // The schedule is the kernel's before this one, which has to end first; or,
+    // early, the one's before that, which has ended (the tensor-core kernel let
+    // this one start only then).
+    if (!a.early) asm volatile("griddepcontrol.wait;" ::: "memory");
   } else if (a.side_schedule && blockIdx.x == gridDim.x - 1 && warp == R::kWarps - 1) {
     schedule_own(a, lane, 32, 1, reinterpret_cast<long long*>(smem_raw + R::kSum));
   }
@@ -147,16 +149,22 @@ __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
   long long* places = reinterpret_cast<long long*>(smem_raw + R::kPlaces);
   const bool near = which == 0 && L.n_req <= kMaxPlaces;
   if (near) {
-    for (int b = threadIdx.x; b < L.n_req; b += R::kWarps * 32) places[b] = L.req[b].p0;
+    for (int b = threadIdx.x; b < L.n_req; b += R::kWarps * 32) places[b] = __ldcg(&L.req[b].p0);
     __syncthreads();
   }
   const Cuts cuts = which ? prefix_cuts(a) : own_cuts(a);
   const long long total = cuts.total, run = cuts.run;
-  auto request = [&](int b) { return which ? cuts.one : L.req[b]; };
+  auto request = [&](int b) {  // (past L1: see above)
+    if (which) return cuts.one;
+    const long long* src = reinterpret_cast<const long long*>(L.req + b);
+    Request r;
+    const long long w[3] = {__ldcg(src), __ldcg(src + 1), __ldcg(src + 2)};
+    memcpy(&r, w, sizeof r);
+    return r;
+  };
   const int w = warp * gridDim.x + blockIdx.x;
   const long long x0 = min((long long)w * run, total);
   const int count = (int)(min(x0 + run, total) - x0);
-  if (count <= 0) return;
 
   // Coordinates of 32 positions of the run at a time, one a lane: position
   // x0 + 32 k + lane.  The next 32 are looked up while these are used.
@@ -171,7 +179,7 @@ __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
       int lo = 0, hi = L.n_req;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if ((near ? places[mid] : L.req[mid].p0) <= x)
+        if ((near ? places[mid] : __ldcg(&L.req[mid].p0)) <= x)
           lo = mid;
         else
           hi = mid;
@@ -276,7 +284,7 @@ __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
           while (!ptx::mbar_try_wait(bars + 8 * (j % R::kStages), (j / R::kStages) & 1) &&
                  (long long)(ptx::globaltimer() - t0) < kWaitLimitNs) {
           }
-        return;
+        break;
       }
     }
     float sc[NT][4] = {};  // tokens g, g + 8; rows 2 t, 2 t + 1
@@ -405,6 +413,8 @@ __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
       }
     }
   }
+  // early: this kernel has ended only when the one before it has, for the merge
+  if (which == 0 && a.early) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ------------------------------------------------------------- merge
@@ -665,7 +675,8 @@ size_t lay_out(const PrefixParams& p, uint8_t* base, Args* a) {
   // epilogue, was slower: eight warps an SM wait for those loads, 105 to 168 us
   // at 512 requests of 64 heads, against 9 us less in the merge.)
   a->join = p.prefix_len == 0;
-  a->side_schedule = p.prefix_len > 0 && p.n_req <= kMaxSideRequests;
+  a->early = p.prefix_len > 0 && by_tiles(p);
+  a->side_schedule = p.prefix_len > 0 && !a->early && p.n_req <= kMaxSideRequests;
   return at;
 }
 

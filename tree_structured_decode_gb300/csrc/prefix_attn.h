@@ -14,7 +14,7 @@ constexpr int kMinPages = 4;    // shortest run of a warp of the line kernel
 
 // What the kernels know of a request, checked: its first token and row count
 // lie in the batch, its pages in the table.
-struct Request {
+struct Request {  // 24 bytes
   long long p0;  // steps in the line before it
   int len, n, tok0, np;  // tokens held, queries, the first one, steps of a segment
 };
@@ -45,7 +45,8 @@ struct Args {
   PrefixParams p;
   Line line[2];  // own tokens, prefix
   int32_t* request_of;  // [tokens] (of tokens that are some request's)
-  int side_schedule;  // the prefix kernel checks and sums up the requests on the side
+  int side_schedule;  // the prefix by lines checks and sums up the requests on the side
+  int early;          // the own tokens' kernel starts while the prefix's still runs
   int join;           // own segments in one run are final
 };
 
@@ -75,8 +76,8 @@ __device__ __forceinline__ Cuts prefix_cuts(const Args& a) {
 __device__ __forceinline__ Cuts own_cuts(const Args& a) {
   Cuts c;
   c.one = Request{};
-  c.total = a.line[0].sizes[0];
-  c.run = a.line[0].sizes[1];
+  c.total = __ldcg(a.line[0].sizes);
+  c.run = __ldcg(a.line[0].sizes + 1);
   return c;
 }
 

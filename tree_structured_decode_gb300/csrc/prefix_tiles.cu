@@ -55,7 +55,7 @@ struct Cfg {
   static constexpr int kOffStage = 2 * kQBytes;
   static constexpr int kOffBar = kOffStage + kStages * kStageBytes;
   static constexpr int kBars = 3 * kStages + 11;
-  static constexpr int kSmem = kOffBar + kBars * 8 + 8 + 16;  // TMEM address, abort flag, the schedule's two sums
+  static constexpr int kSmem = kOffBar + kBars * 8 + 8;  // TMEM address, abort flag
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 
@@ -486,7 +486,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0 && c.status) atomicOr(c.status, kBatchTimeout);
     return;
   }
-  asm volatile("griddepcontrol.launch_dependents;");  // the next kernel waits for this grid's end
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       ptx::mbar_init(c.full(s), 1);
@@ -521,8 +520,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       stream_kv<D>(&tmk, &tmv, a, c, cuts, rows);
     else if (warp == 9)
       issue_products<D, kHalf>(a, c, cuts, rows, tmem);
-    else if (blockIdx.x == 0 && a.side_schedule)  // two warps that have nothing else to do
-      schedule_own(a, threadIdx.x - 320, 64, 1, reinterpret_cast<long long*>(smem + C::kOffBar + C::kBars * 8 + 8));
+    else if (warp == 10) {
+      // The schedule's kernel has ended and its writes are there; only then may
+      // the own tokens' kernel, which reads them, start beside this one.
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      asm volatile("griddepcontrol.launch_dependents;");
+    }
     __syncwarp();
   }
   ptx::tc_fence_before();
@@ -543,8 +546,18 @@ cudaError_t launch(const Args& a, const CUtensorMap& mk, const CUtensorMap& mv, 
   const long long blocks = ((long long)p.n_tokens * p.gqa + kTileRows - 1) / kTileRows;
   const long long steps = blocks * p.hkv * ((p.prefix_len + kTileTokens - 1) / kTileTokens);
   const unsigned grid = (unsigned)(steps < p.num_sms ? steps : p.num_sms);
-  prefix_tile_kernel<D, kHalf><<<grid, kThreads, Cfg<D>::kSmem, s>>>(mk, mv, a);
-  return cudaGetLastError();
+  // a programmatic dependent of the schedule's kernel, of which it reads nothing
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Cfg<D>::kSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prefix_tile_kernel<D, kHalf>, mk, mv, a);
 }
 
 }  // namespace
