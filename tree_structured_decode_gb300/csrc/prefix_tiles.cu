@@ -117,32 +117,37 @@ struct Segment {
   int head, block, j0, j1;
 };
 struct Walk {
-  long long x, x1;
-  int n, blocks;
-  __device__ bool next(Segment& s) {
-    if (x >= x1) return false;
-    const long long u = x / n;
-    s.j0 = (int)(x - u * n);
-    s.j1 = (int)min((long long)n, s.j0 + (x1 - x));
-    s.head = (int)(u / blocks);
-    s.block = (int)(u % blocks);
-    x += s.j1 - s.j0;
+  int head, block, j, left;  // the next step's place, steps left
+  int n, blocks;             // steps of a segment, row blocks of a kv head
+  __device__ __forceinline__ bool next(Segment& s) {
+    if (left <= 0) return false;
+    s.head = head;
+    s.block = block;
+    s.j0 = j;
+    s.j1 = min(n, j + left);
+    left -= s.j1 - s.j0;
+    j = 0;
+    if (++block == blocks) block = 0, ++head;
     return true;
   }
 };
 __device__ __forceinline__ Walk walk_of(const Cuts& cuts, int rows) {
   Walk w;
-  w.x = min((long long)blockIdx.x * cuts.run, cuts.total);
-  w.x1 = min(w.x + cuts.run, cuts.total);
   w.n = cuts.one.np;
   w.blocks = (rows + kTileRows - 1) / kTileRows;
+  const long long x = min((long long)blockIdx.x * cuts.run, cuts.total);
+  w.left = (int)(min(x + cuts.run, cuts.total) - x);
+  const long long u = quotient(x, max(w.n, 1));
+  w.j = (int)(x - u * w.n);
+  w.head = (int)quotient(u, max(w.blocks, 1));
+  w.block = (int)(u - (long long)w.head * w.blocks);
   return w;
 }
 
 // ------------------------------------------------------------- copies
 template <int D>
 __device__ void stream_kv(const CUtensorMap* tmk, const CUtensorMap* tmv, const Args& a,
-                          const Cta<D>& c, const Cuts& cuts, int rows) {
+                          const Cta<D>& c, Walk walk) {
   using C = Cfg<D>;
   const PrefixParams& p = a.p;
   const Line& L = a.line[1];
@@ -156,7 +161,6 @@ __device__ void stream_kv(const CUtensorMap* tmk, const CUtensorMap* tmv, const 
     if (p.status) atomicOr(p.status, kBatchBadSlot);
     return p.num_pages;  // outside the tensor map: read as zeros
   };
-  Walk walk = walk_of(cuts, rows);
   Segment s;
   uint32_t g = 0;
   uint32_t zeroed = 0;  // phase of each stage's land barrier
@@ -223,7 +227,7 @@ __device__ void stream_kv(const CUtensorMap* tmk, const CUtensorMap* tmv, const 
 
 // ------------------------------------------------------------- products
 template <int D, bool kHalf>
-__device__ void issue_products(const Args& a, const Cta<D>& c, const Cuts& cuts, int rows,
+__device__ void issue_products(const Args& a, const Cta<D>& c, Walk walk, int rows,
                                uint32_t tmem) {
   using C = Cfg<D>;
   constexpr uint32_t kType = kHalf ? 0u : (1u << 7) | (1u << 10);
@@ -231,7 +235,6 @@ __device__ void issue_products(const Args& a, const Cta<D>& c, const Cuts& cuts,
       (ptx::idesc_bf16(128, kTileTokens, 0) & ~((1u << 7) | (1u << 10))) | kType;
   constexpr uint32_t kDescPV = (ptx::idesc_bf16(128, D, 1) & ~((1u << 7) | (1u << 10))) | kType;
   const int n_pages = (a.p.prefix_len + kPage - 1) / kPage;
-  Walk walk = walk_of(cuts, rows);
   Segment s;
   uint32_t g = 0;             // steps before this segment: K is ring entry 2 g, V 2 g + 1
   uint32_t done[2] = {0, 0};  // steps of each tile before this segment
@@ -348,7 +351,7 @@ __device__ __noinline__ void rescale_o(uint32_t o, float alpha) {
 }
 
 template <int D, bool kHalf>
-__device__ void softmax_rows(const Args& a, const Cta<D>& c, const Cuts& cuts, int rows,
+__device__ void softmax_rows(const Args& a, const Cta<D>& c, Walk walk, int rows,
                              uint32_t tmem, int t) {
   using C = Cfg<D>;
   const PrefixParams& p = a.p;
@@ -357,7 +360,6 @@ __device__ void softmax_rows(const Args& a, const Cta<D>& c, const Cuts& cuts, i
   const uint32_t lanes = (uint32_t)(warp * 32) << 16;
   const uint32_t s_tmem = tmem + lanes + t * 128, o_tmem = tmem + lanes + 256 + t * 128;
   const uint32_t q_smem = c.base + t * C::kQBytes;
-  Walk walk = walk_of(cuts, rows);
   // the walk's next segment that has rows in this tile
   auto next = [&](Segment& s) {
     while (walk.next(s))
@@ -439,7 +441,7 @@ __device__ void softmax_rows(const Args& a, const Cta<D>& c, const Cuts& cuts, i
     if (!ok) break;
     ptx::tc_fence_after();
     if (act) {
-      const bool whole = s.j0 == 0 && s.j1 == cuts.one.np;
+      const bool whole = s.j0 == 0 && s.j1 == walk.n;
       const long long slot = (2ll * blockIdx.x + (s.j0 == 0 ? 1 : 0)) * kTileRows + t * 128 + tid;
       const long long at = (long long)(row / p.gqa) * p.hq + s.head * p.gqa + row % p.gqa;
       float* dst = whole ? L.row_o + at * D : L.piece_o + slot * D;
@@ -480,8 +482,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::kOffBar + C::kBars * 8);
   c.abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffBar + C::kBars * 8 + 4);
   const int warp = threadIdx.x >> 5;
-  const Cuts cuts = prefix_cuts(a);
-  const int rows = cuts.one.n * a.p.gqa;
+  __shared__ Walk s_walk;
+  __shared__ int s_rows;
   if (c.base & 1023) {  // the swizzled layouts need it
     if (threadIdx.x == 0 && c.status) atomicOr(c.status, kBatchTimeout);
     return;
@@ -500,6 +502,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(c.o_empty(t), 128);
     }
     ptx::mbar_init(c.drain(), 1);
+    const Cuts cuts = prefix_cuts(a);
+    s_rows = cuts.one.n * a.p.gqa;
+    s_walk = walk_of(cuts, s_rows);
     *c.abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -511,15 +516,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const Walk walk = s_walk;
+  const int rows = s_rows;
   if (warp < 8) {
     ptx::setmaxnreg_inc<kSoftmaxRegs>();
-    softmax_rows<D, kHalf>(a, c, cuts, rows, tmem, warp >> 2);
+    softmax_rows<D, kHalf>(a, c, walk, rows, tmem, warp >> 2);
   } else {
     ptx::setmaxnreg_dec<kIssueRegs>();
     if (warp == 8)
-      stream_kv<D>(&tmk, &tmv, a, c, cuts, rows);
+      stream_kv<D>(&tmk, &tmv, a, c, walk);
     else if (warp == 9)
-      issue_products<D, kHalf>(a, c, cuts, rows, tmem);
+      issue_products<D, kHalf>(a, c, walk, rows, tmem);
     else if (warp == 10) {
       // The schedule's kernel has ended and its writes are there; only then may
       // the own tokens' kernel, which reads them, start beside this one.
