@@ -110,13 +110,14 @@ def extend_tables(lens, n_new, block_table, free_pages, n_free, max_new, positio
         raise ValueError("max_new is negative")
     context, handle = _launch_on(index, stream)
     with context:
-        # one allocation: slots, positions, cu_new
-        out = torch.empty(2 * max_new + b + 1, dtype=kind, device=lens.device)
-        at = out.data_ptr()
+        device = lens.device
+        slots = torch.empty(max_new, dtype=kind, device=device)
+        positions = torch.empty(max_new, dtype=kind, device=device)
+        cu = torch.empty(b + 1, dtype=kind, device=device)
         check(load_library().tree_attn_extend_tables(
-            lens_at, new_at, b, table, stride, width, free_at, cap, n_free_at, max_new, position_base, at,
-            at + 4 * max_new, at + 8 * max_new, status_at, handle), "tree_attn_extend_tables")
-        return out.split_with_sizes((max_new, max_new, b + 1))
+            lens_at, new_at, b, table, stride, width, free_at, cap, n_free_at, max_new, position_base, slots.data_ptr(),
+            positions.data_ptr(), cu.data_ptr(), status_at, handle), "tree_attn_extend_tables")
+    return slots, positions, cu
 
 
 def append_slots(k_new, v_new, slots, k_pages, v_pages, status=None, stream=None):

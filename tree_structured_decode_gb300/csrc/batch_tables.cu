@@ -231,9 +231,11 @@ __global__ void __launch_bounds__(256) append_slots_kernel(const AppendSlotsPara
 
 cudaError_t launch_extend_tables(const ExtendParams& p, cudaStream_t s) {
   const size_t smem = 3 * sizeof(int32_t) * ((size_t)p.n_req + 1);
-  cudaError_t e = cudaFuncSetAttribute(extend_tables_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+  if (smem > 40 * 1024) {  // more than any kernel may have unasked
+    const cudaError_t e = cudaFuncSetAttribute(
+        extend_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   const int ranks = p.max_new > 4 * kThreads ? 8 : 1;
   cfg.gridDim = dim3(ranks);
@@ -246,7 +248,7 @@ cudaError_t launch_extend_tables(const ExtendParams& p, cudaStream_t s) {
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = ranks > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, extend_tables_kernel, p);
 }
 

@@ -984,7 +984,7 @@ cudaError_t run(SampleParams p, int ranks, cudaStream_t s) {
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = ranks > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, sample_kernel<T>, p);
 }
 
