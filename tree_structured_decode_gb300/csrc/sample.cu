@@ -48,7 +48,11 @@ constexpr int kBins = 2048;
 constexpr int kSegments = 256;     // of a CTA's part, at most
 constexpr int kHeld = 61440;       // bytes of logits held in shared memory: two CTAs fit an SM
 constexpr int kFew = 384;          // values of a bin that are compared all with all (at most the threads of a CTA)
-constexpr float kNear = 11.0903549f;   // the first histogram's range of exponents: 2^-16
+// The first histogram's range of exponents: down to 2^-16 for top-k, which need
+// not look at more than the largest logits, and to 2^-24 for top-p alone, which
+// weighs all of them anyway (256 rows of 128000, top-p 0.7 to 1: with 2^-16 a
+// third of the rows needed a second one, 76 us for the slowest).
+constexpr float kNearK = 11.0903549f, kNearP = 16.6355323f;
 constexpr int kSafe = 1023;            // values of a bin whose two 32-bit sums cannot overflow
 constexpr int kMaxRanks = 4;
 constexpr u64 kOne = 1ull << 42;   // the weight of the largest logit
@@ -214,8 +218,11 @@ struct Row {
   CountWeight* warp_sum;  // [32]
   float* queue;      // [64] this warp's, and the places
   int* queue_at;
+  CountWeight bins[kBins / kThreads];  // this thread's of the whole cluster's
+  float near_to;     // the first histogram's range
   bool safe;         // how the bins hold their sums, see put()
   bool infinite;     // the largest logit is +inf
+  bool summed_up;    // `bins` are those of the first histogram, if that is there
   int rank, ranks, v0, size, seg;  // seg: logits of a segment, a multiple of 128
   Weights weight;
 
@@ -350,16 +357,18 @@ struct Row {
   // Every CTA sums up all bins for itself: one cluster barrier behind the
   // filling, and none for a second target.
   enum Crossing { kNever, kFound, kFull };
-  __device__ Crossing cross(bool by_weight, u64 target, CountWeight& before, int& bin, int& bin_n) {
+  __device__ Crossing cross(bool by_weight, u64 target, CountWeight& before, int& bin, int& bin_n, bool again = false) {
     constexpr int kPer = kBins / kThreads;
     static_assert(kPer == 4, "a thread reads 16 bytes of a histogram");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    CountWeight sum[kPer], all{0, 0};
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) sum[k] = {0, 0};
+    CountWeight (&sum)[kPer] = bins, all{0, 0};
     int most = 0;
+    if (!again) {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) sum[k] = {0, 0};
+    }
 #pragma unroll 2
-    for (int r = 0; r < ranks; ++r) {
+    for (int r = again ? ranks : 0; r < ranks; ++r) {
       const uint4 n4 = reinterpret_cast<const uint4*>(cluster.map_shared_rank(hn, r))[tid];
       const uint4 l4 = reinterpret_cast<const uint4*>(cluster.map_shared_rank(hlo, r))[tid];
       const uint4 h4 = reinterpret_cast<const uint4*>(cluster.map_shared_rank(hhi, r))[tid];
@@ -506,28 +515,30 @@ struct Row {
   }
 
   // The shortest prefix of the order that has `target` elements, or weight:
-  // its cut and weight.  near: the bins hold the part up to kNear (on return as
+  // its cut and weight.  near: the bins hold the first range (on return as
   // well).  With `sums`, the segments' sums of it (of what has bits least or
   // above) are taken on the way; summed says whether they could be.
   __device__ bool select(bool by_weight, u64 target, uint32_t least, bool sums, Cut& cut, u64& cut_weight,
                          bool& near, bool& summed) {
     CountWeight before{0, 0};
     int bin, bin_n;
-    Range range{0.f, kNear};
+    Range range{0.f, near_to};
     auto refill = [&](bool direct) {
       sync();  // every CTA has read the bins
       fill(range, direct);
       sync();
     };
+    const bool again = near && summed_up;  // the sums of all bins are there from the last target
     if (!near) refill(false), near = true;
-    Crossing got = cross(by_weight, target, before, bin, bin_n);
+    Crossing got = cross(by_weight, target, before, bin, bin_n, again);
+    summed_up = true;
     if (got == kFull) {
       safe = true;
       refill(false);
       got = cross(by_weight, target, before, bin, bin_n);
     }
     if (got == kNever) {  // below it: what is above are all of the first bins
-      range = {kNear, -kLeast};
+      range = {near_to, -kLeast};
       refill(true);  // most logits lie there: they are not collected
       near = false;
       got = cross(by_weight, target, before, bin, bin_n);
@@ -750,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const T* global = reinterpret_cast<const T*>(p.logits) + row * p.stride + v0;
   Row<T> R{cluster, global, nullptr, (reinterpret_cast<uintptr_t>(global) & (4 * sizeof(T) - 1)) == 0,
            hist, hist + kBins, hist + 2 * kBins, few_key, few_at, few_w, seg_sum, &s_shown, s_warp,
-           s_queue[warp], s_queue_at[warp], false, false, rank, ranks, v0, size, 128 * ((p.slice + 128 * kSegments - 1) / (128 * kSegments)), {}};
+           s_queue[warp], s_queue_at[warp], {}, 0.f, false, false, false, rank, ranks, v0, size, 128 * ((p.slice + 128 * kSegments - 1) / (128 * kSegments)), {}};
   // segments of up to 1024 logits, of fewer where a warp would have none
   R.seg = max(R.seg, min(1024, 128 * ((p.slice + 128 * kNumWarps - 1) / (128 * kNumWarps))));
   const float temperature = p.temperature ? p.temperature[row] : p.temperature_all;
@@ -867,8 +878,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   const float top_p = p.top_p ? p.top_p[row] : p.top_p_all;
   const bool use_k = top_k > 0 && top_k < p.vocab, use_p = top_p < 1.f;
   bool summed = false;
+  R.near_to = use_k ? kNearK : kNearP;
   if (use_k || use_p) {
-    u64 total = R.fill({0.f, kNear}, !use_k);
+    u64 total = R.fill({0.f, R.near_to}, !use_k);
     if (use_k)
       R.sync();  // every histogram is complete
     else
@@ -879,8 +891,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     if (use_k && R.select(false, (u64)top_k, least, !use_p, o, w, near, summed)) shorten(o);
     if (use_p) {
       if (use_k && w == 0) {  // fewer than k have a weight: all of it counts
+        R.summed_up = false;
         R.sync();
-        total = R.total_of(R.fill({0.f, kNear}, true));
+        total = R.total_of(R.fill({0.f, R.near_to}, true));
         near = true;
       }
       if (w) total = w;
