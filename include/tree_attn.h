@@ -405,7 +405,8 @@ tree_attn_status tree_attn_append_slots(const void* k_new, const void* v_new, in
  *   prefix_pages, prefix_len   pages of the shared prefix (device) and its
  *                  tokens; 0 for none.
  *   softmax_scale  <= 0 selects 1/sqrt(head_dim).
- *   out            [n_tokens][n_q_heads][head_dim], q's type, contiguous.
+ *   out            [n_tokens][n_q_heads][head_dim], q's type, contiguous; not
+ *                  q's own memory.
  *   lse            fp32 [n_tokens][n_q_heads] (natural log), may be NULL.
  *   workspace      device memory of tree_attn_prefix_workspace() bytes,
  *                  256-byte aligned; two runs that may overlap on the GPU need

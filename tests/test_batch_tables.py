@@ -39,7 +39,7 @@ def _check(lens, n_new, table, free, n_free, max_new, base=0, status=None):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("requests,held,new", [(1, 0, 1), (1, 15, 1), (1, 16, 1), (3, 40, 5), (64, 200, 1), (64, 100, 90),
-                                               (257, 33, 20), (1025, 17, 4), (2500, 30, 3)])
+                                               (257, 33, 20), (1025, 17, 4), (2500, 30, 3), (16384, 20, 2)])
 def test_extend_and_take_back(requests, held, new):
     width = -(-(held + 3 * new) // 16) + 1
     rng, lens, table, free, n_free = _state(requests + held, requests, width, requests * width + 3, held)

@@ -126,6 +126,40 @@ def test_work_cut_into_runs(lens, prefix, heads):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("requests,prefix", [(2049, 20), (5000, 0), (3000, 150)])
+def test_more_requests_than_a_cta_searches_by_itself(requests, prefix):
+    g = np.random.default_rng(requests)
+    lens, new = g.integers(0, 40, requests).tolist(), g.integers(0, 2, requests).tolist()
+    s = make(requests, lens, new, 2, 1, 64, prefix, padding=5)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = attend(to_gpu(s), status=status)
+    assert status.item() == 0
+    check(s, out, lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("prefix", [0, 33, 900])
+def test_captured_and_replayed_with_other_lengths(prefix):
+    """A graph's runs follow the lengths, offsets and tables that lie in memory when it is replayed."""
+    s = make(9, [100, 7, 60], [2, 1, 1], 12, 2, 64, prefix, padding=2, width=9)
+    c = to_gpu(s)
+    attend(c)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = attend(c)
+    for lens, cu in (([100, 7, 60], [0, 2, 3, 4]), ([90, 0, 48], [0, 1, 1, 6]), ([1, 2, 3], [0, 0, 3, 6]), ([0, 0, 0], [0, 0, 0, 0])):
+        out.fill_(7)
+        lse.fill_(7)
+        for name, x in (("lens", lens), ("cu", cu)):
+            s[name] = torch.tensor(x, dtype=torch.int32)
+            c[name].copy_(s[name])
+        s["cu_all"] = np.array(cu)
+        graph.replay()
+        check(s, out, lse)
+
+
+@pytest.mark.gpu
 def test_scale_and_large_scores():
     s = make(3, [100, 64], None, 4, 2, 64, 90, gain=3.0)
     out, lse = attend(to_gpu(s), softmax_scale=0.31)
@@ -235,7 +269,7 @@ def _run(**kw):
     (dict(width=-1), "INVALID_ARG"), (dict(d=96), "UNSUPPORTED"), (dict(hq=5), "UNSUPPORTED"),
     (dict(hq=258), "UNSUPPORTED"), (dict(dtype=2), "UNSUPPORTED"), (dict(b=16385), "UNSUPPORTED"),
     (dict(pages=-1), "UNSUPPORTED"), (dict(width=1 << 27, stride=1 << 27), "UNSUPPORTED"),
-    (dict(t=1 << 29), "UNSUPPORTED"), (dict(q=264), "ALIGNMENT"), (dict(q_stride=516), "ALIGNMENT"),
+    (dict(t=1 << 29), "UNSUPPORTED"), (dict(t=1 << 24, b=9, width=1 << 26, stride=1 << 26), "UNSUPPORTED"), (dict(q=264), "ALIGNMENT"), (dict(q_stride=516), "ALIGNMENT"),
     (dict(lens=258), "ALIGNMENT"), (dict(work=272), "ALIGNMENT"), (dict(bytes=100), "BUFFER_TOO_SMALL")])
 def test_refusals(kw, name):
     assert _abi.STATUS_NAMES[_run(**kw)] == "TA_ERR_" + name

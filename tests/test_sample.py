@@ -129,6 +129,19 @@ def test_large_rows(vocab, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows", [1, 60, 400])
+def test_filters_that_end_far_below_the_largest(rows):
+    """Steep rows, where a filter's end lies past 2^-16 and 2^-24 of the largest weight, and rows of few distinct values, whose
+    bins hold thousands."""
+    x = rows_of(31, rows, 9000, spread=6.0)
+    x[rows // 2] = (x[rows // 2] / 4).round()
+    some = range(0, rows, max(1, rows // 5))
+    for n, kw in enumerate([dict(top_k=7000), dict(top_k=7000, top_p=1 - 2.0 ** -23), dict(top_p=1 - 2.0 ** -24),
+                            dict(top_p=1 - 2.0 ** -20, temperature=2.0), dict(top_k=8999, temperature=0.5), dict(top_p=0.9999, min_p=1e-7)]):
+        check(x, numbers(n, rows, 2), rows=some, **kw)
+
+
+@pytest.mark.gpu
 def test_many_draws_follow_the_weights():
     """All of a row's tokens come, each as often as its share of evenly spread numbers says (to one)."""
     x = rows_of(10, 1, 300, spread=1.0)

@@ -6,7 +6,8 @@ Argument marshalling only: each function checks its tensors, makes the outputs
 that were not given, and calls the C ABI (``include/tree_attn.h``).  The
 functions take no host synchronisation and may be captured in a CUDA graph.
 They run on the tensors' device: on ``stream`` if given, else on that device's
-current stream.
+current stream.  What they allocate belongs to that stream; tensors made on
+another one need the usual care (``wait_stream``, ``record_stream``).
 """
 from __future__ import annotations
 

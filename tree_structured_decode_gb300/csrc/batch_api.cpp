@@ -2,6 +2,7 @@
 // launches.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <string>
@@ -176,6 +177,11 @@ tree_attn_status tree_attn_prefix_run(const void* q, int64_t q_stride, const voi
       return fail(TA_ERR_INVALID_ARG, "table_width is negative or table_stride below it");
     if ((int64_t)table_width * ta::kPage > INT32_MAX || (uint32_t)num_pages > ta::kMaxPages)
       return fail(TA_ERR_UNSUPPORTED, "rows of 2^31 tokens or more, or num_pages out of range");
+    // a warp's, or CTA's, share of the work is counted in 32 bits
+    const int64_t kv_tiles = ((int64_t)n_tokens * p.gqa / 8 + n_requests + 1) * n_kv_heads;
+    const int64_t most = std::max<int64_t>(table_width, prefix_len / ta::kPage + 1);
+    if (kv_tiles > INT64_MAX / most || kv_tiles * most / p.num_sms > INT32_MAX)
+      return fail(TA_ERR_UNSUPPORTED, "too many query rows for tables this wide or a prefix this long");
     if (!cu_new && n_tokens != n_requests)
       return fail(TA_ERR_INVALID_ARG, "without cu_new there is one query a request: n_tokens must be n_requests");
     if (n_tokens == 0) return TA_OK;
