@@ -126,6 +126,19 @@ def test_work_cut_into_runs(lens, prefix, heads):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("requests", [383, 384, 385, 2500])
+@pytest.mark.parametrize("asking,heads,prefix", [(1, (16, 1), 700), (5, (4, 2), 33), (9, (2, 2), 9000), (300, (4, 2), 50)])
+def test_a_few_of_many_requests_ask(requests, asking, heads, prefix):
+    """Up to 16 query rows behind a prefix stand in one line with the requests' own pages; more go apart."""
+    new = [0] * requests
+    for i in range(asking):
+        new[(i + 1) * requests // asking - 1] = 1
+    s = make(requests, [(7 * b) % 40 for b in range(requests)], new, *heads, 128, prefix, padding=2)
+    out, lse = attend(to_gpu(s))
+    check(s, out, lse)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("requests,prefix", [(2049, 20), (5000, 0), (3000, 150)])
 def test_more_requests_than_a_cta_searches_by_itself(requests, prefix):
     g = np.random.default_rng(requests)

@@ -32,12 +32,29 @@ constexpr float kGrowLog2 = 8.f;  // the running maximum is raised when a score 
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr long long kWaitLimitNs = 2000000000ll;
 
-// Batches without a prefix kernel that does it on the side, or with many
-// requests.
+// Batches of more requests than a CTA of the line kernel has threads.
 __global__ void __launch_bounds__(1024) prefix_schedule_kernel(const Args a) {
   __shared__ long long s_warp[32];
+  const PrefixParams& p = a.p;
   asm volatile("griddepcontrol.launch_dependents;");
-  schedule_own(a, threadIdx.x, 1024, 0, s_warp);
+  const int per = (p.n_req + 1023) / 1024;
+  const int b0 = min((int)threadIdx.x * per, p.n_req), b1 = min(b0 + per, p.n_req);
+  int bad = 0;
+  long long mine = 0, total;
+  for (int b = b0; b < b1; ++b) mine += steps_of(a, checked(p, b, bad));
+  const long long base = a.mixed ? prefix_cuts(a).total : 0;
+  long long at = base + scan_block(mine, s_warp, total) - mine;
+  for (int b = b0; b < b1; ++b) {
+    Request r = checked(p, b, bad);
+    r.p0 = at;
+    at += steps_of(a, r);
+    publish(a, b, r);
+  }
+  if (bad && p.status) atomicOr(p.status, bad);
+  if (threadIdx.x == 0) {
+    a.line[0].sizes[0] = base + total;
+    a.line[0].sizes[1] = own_run(a, base + total);
+  }
 }
 
 // ------------------------------------------------------------- attention
@@ -92,17 +109,19 @@ constexpr int kMaxPlaces = 2048;  // requests whose places are searched in share
 // 12 warps an SM hide one another's latencies; each has two pages (four at d =
 // 64) in flight or in use.
 constexpr int kLineWarps = 12;
+constexpr int kMaxSelf = kLineWarps * 32;  // requests that a CTA checks by itself, one a thread
 template <int D>
 struct Ring {
   static constexpr int kWarps = kLineWarps;
   static constexpr int kHead = kPage * D * 2;           // bytes of a page-head
   static constexpr int kStages = 2 * (128 / D);  // K and V of one page each
   static constexpr int kBytes = kWarps * kStages * 2 * kHead;
-  // barriers, the schedule's sum, requests' places in the line
+  // barriers, the scan's sums, the requests (or their places in the line)
   static constexpr int kSum = kBytes + kWarps * kStages * 8;
-  static constexpr int kPlaces = kSum + 16;
+  static constexpr int kPlaces = kSum + kWarps * 8;
   static constexpr int kSmem = kPlaces + kMaxPlaces * 8;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+  static_assert(kMaxSelf * sizeof(Request) <= kMaxPlaces * 8, "the requests fit where places would");
 };
 
 // NT: tiles of 8 query rows.
@@ -114,14 +133,17 @@ struct Ring {
 // and accumulators for the eight or fewer rows of one query.)  The running
 // maximum grows only when a score passes it by 2^8, so most pages need no
 // reduction across lanes.  Bound by reading K and V once.
+// The line is the requests' own pages, with the prefix's before them where it
+// has at most 16 query rows a kv head (b < 0 below).  Every CTA sums up the
+// requests by itself, which costs less than a kernel before this one.
 template <int D, bool kHalf, int NT>
 __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
     prefix_line_kernel(const __grid_constant__ CUtensorMap tmk,
-                       const __grid_constant__ CUtensorMap tmv, const Args a, const int which) {
+                       const __grid_constant__ CUtensorMap tmv, const Args a) {
   using R = Ring<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const PrefixParams& p = a.p;
-  const Line& L = a.line[which];
+  const Line& L = a.line[0];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t ring = ptx::smem_u32(smem_raw) + warp * R::kStages * 2 * R::kHead;
@@ -137,25 +159,45 @@ __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
   __syncwarp();
   // the next kernel may set itself up while this one runs
   asm volatile("griddepcontrol.launch_dependents;");
-  if (which == 0) {
-    // The schedule is the kernel's before this one, which has to end first; or,
-    // early, the one's before that, which has ended (the tensor-core kernel let
-    // this one start only then).
-    if (!a.early) asm volatile("griddepcontrol.wait;" ::: "memory");
-  } else if (a.side_schedule && blockIdx.x == gridDim.x - 1 && warp == R::kWarps - 1) {
-    schedule_own(a, lane, 32, 1, reinterpret_cast<long long*>(smem_raw + R::kSum));
-  }
+  // The schedule, if there is one, is the kernel's before this one, which has to
+  // end first; or, early, the one's before that, which has ended (the
+  // tensor-core kernel let this one start only then).
+  if (!a.early) asm volatile("griddepcontrol.wait;" ::: "memory");
 
+  Request* requests = reinterpret_cast<Request*>(smem_raw + R::kPlaces);
   long long* places = reinterpret_cast<long long*>(smem_raw + R::kPlaces);
-  const bool near = which == 0 && L.n_req <= kMaxPlaces;
-  if (near) {
-    for (int b = threadIdx.x; b < L.n_req; b += R::kWarps * 32) places[b] = __ldcg(&L.req[b].p0);
+  const bool near = p.n_req <= kMaxPlaces;
+  Cuts prefix{};
+  if (a.mixed) prefix = prefix_cuts(a);
+  const long long base = prefix.total;  // the prefix's pages in the line
+  long long total, run;
+  if (a.self) {
+    const int b = threadIdx.x;
+    int bad = 0;
+    Request r{};
+    if (b < p.n_req) r = checked(p, b, bad);
+    const long long mine = b < p.n_req ? steps_of(a, r) : 0;
+    r.p0 = base + scan_block(mine, reinterpret_cast<long long*>(smem_raw + R::kSum), total) - mine;
+    total += base;
+    run = own_run(a, total);
+    if (b < p.n_req) requests[b] = r;
+    if (blockIdx.x == 0) {  // for the merge
+      if (b < p.n_req) publish(a, b, r);
+      if (bad && p.status) atomicOr(p.status, bad);
+      if (b == 0) L.sizes[0] = total, L.sizes[1] = run;
+    }
     __syncthreads();
+  } else {
+    if (near) {
+      for (int b = threadIdx.x; b < p.n_req; b += R::kWarps * 32) places[b] = __ldcg(&L.req[b].p0);
+      __syncthreads();
+    }
+    total = __ldcg(L.sizes);
+    run = __ldcg(L.sizes + 1);
   }
-  const Cuts cuts = which ? prefix_cuts(a) : own_cuts(a);
-  const long long total = cuts.total, run = cuts.run;
   auto request = [&](int b) {  // (past L1: see above)
-    if (which) return cuts.one;
+    if (b < 0) return prefix.one;
+    if (a.self) return requests[b];
     const long long* src = reinterpret_cast<const long long*>(L.req + b);
     Request r;
     const long long w[3] = {__ldcg(src), __ldcg(src + 1), __ldcg(src + 2)};
@@ -171,15 +213,16 @@ __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
   struct Where {
     int b, head, tile, pg, np, page;
   };
-  auto look_up = [&](int base) {
+  auto look_up = [&](int from) {
     Where r{0, 0, 0, 0, 1, 0};
-    const int i = base + lane;
+    const int i = from + lane;
     if (i < count) {
       const long long x = x0 + i;
-      int lo = 0, hi = L.n_req;
+      int lo = 0, hi = p.n_req;
+      if (x < base) lo = -1, hi = 0;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if ((near ? places[mid] : __ldcg(&L.req[mid].p0)) <= x)
+        if ((a.self ? requests[mid].p0 : near ? places[mid] : __ldcg(&L.req[mid].p0)) <= x)
           lo = mid;
         else
           hi = mid;
@@ -193,7 +236,7 @@ __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
       r.tile = (int)(seg - (long long)r.head * tiles);
       r.pg = (int)(in - seg * q.np);
       r.np = q.np;
-      r.page = L.table[(long long)lo * L.table_stride + r.pg];
+      r.page = lo < 0 ? p.prefix_pages[r.pg] : p.table[(long long)lo * p.table_stride + r.pg];
       if ((unsigned)r.page >= (unsigned)p.num_pages) {
         r.page = p.num_pages;  // outside the tensor map: read as zeros
         if (p.status) atomicOr(p.status, kBatchBadSlot);
@@ -256,7 +299,7 @@ __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int r2 = 8 * n + 2 * t + e, j = (tile * 8 * NT + r2) / p.gqa;
-          vis[n][e] = r2 >= rows ? 0 : L.causal ? max(r.len - r.n + j + 1, 0) : r.len;
+          vis[n][e] = r2 >= rows ? 0 : b >= 0 ? max(r.len - r.n + j + 1, 0) : r.len;
           m[n][e] = -INFINITY;
           l[n][e] = 0.f;
         }
@@ -401,20 +444,21 @@ __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
             }
             if (g == 0 && p.lse) p.lse[at_row] = den == 0.f ? -INFINITY : (m[n][e] + log2f(den)) * kLn2;
           } else {
-            float* dst = (whole ? L.row_o + at_row * D : L.piece_o + (slot + r) * D) + g;
+            const Line& M = a.line[b < 0 ? 1 : 0];
+            float* dst = (whole ? M.row_o + at_row * D : L.piece_o + (slot + r) * D) + g;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               dst[16 * k] = o[k][n][e];
               dst[16 * k + 8] = o[k][n][2 + e];
             }
-            if (g == 0) (whole ? L.row_ml[at_row] : L.piece_ml[slot + r]) = make_float2(m[n][e], den);
+            if (g == 0) (whole ? M.row_ml[at_row] : L.piece_ml[slot + r]) = make_float2(m[n][e], den);
           }
         }
       }
     }
   }
   // early: this kernel has ended only when the one before it has, for the merge
-  if (which == 0 && a.early) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (a.early) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ------------------------------------------------------------- merge
@@ -488,7 +532,7 @@ __global__ void __launch_bounds__(256, 3) prefix_merge_kernel(const Args a) {
   if (threadIdx.x == 0) {
     const Cuts cuts = prefix_cuts(a);
     const int tok = first / p.gqa;
-    const Pieces q = pieces_of(a.line[1], cuts.one, cuts.run, p, tok, kvh, first - tok * p.gqa);
+    const Pieces q = pieces_of(a.line[1], cuts.one, prefix_run(a, cuts), p, tok, kvh, first - tok * p.gqa);
     s_w0 = q.w0;
     s_n = q.n;
     s_in = q.in;
@@ -576,7 +620,7 @@ __global__ void __launch_bounds__(256) prefix_merge_row_kernel(const Args a) {
   if (tok >= own.tok0 && tok < own.tok0 + own.n) {
     const int kvh = h / p.gqa;
     if (p.prefix_len > 0 && tok < cuts.one.n)
-      pp = pieces_of(a.line[1], cuts.one, cuts.run, p, tok, kvh, h - kvh * p.gqa);
+      pp = pieces_of(a.line[1], cuts.one, prefix_run(a, cuts), p, tok, kvh, h - kvh * p.gqa);
     po = pieces_of(a.line[0], own, a.line[0].sizes[1], p, tok, kvh, h - kvh * p.gqa);
   }
   const int n = po.n + pp.n;
@@ -628,7 +672,6 @@ size_t up(size_t x) { return (x + 255) / 256 * 256; }
 constexpr int kTileMinRows = 17;
 bool by_tiles(const PrefixParams& p) { return (long long)p.n_tokens * p.gqa >= kTileMinRows; }
 
-constexpr int kMaxSideRequests = 2048;
 // Rows an SM up to which the merge takes a block a row.
 constexpr int kBlockRows = 8;
 
@@ -641,48 +684,52 @@ size_t lay_out(const PrefixParams& p, uint8_t* base, Args* a) {
     return q;
   };
   const size_t rows = (size_t)p.n_tokens * p.hq;
-  for (int i = 0; i < 2; ++i) {
-    Line& L = a->line[i];
-    L = Line{};
-    L.n_req = i ? 1 : p.n_req;
-    L.width = i ? 0 : p.width;
-    L.causal = i ? 0 : 1;
-    L.table = i ? p.prefix_pages : p.table;
-    L.table_stride = i ? 0 : p.table_stride;
-    // query rows of a tile: 8, or 16 where a request has more on average (the
-    // prefix by lines has at most 16).  32 were slower, with the registers they
-    // take: 62 us against 37 at 128 requests of up to four drafts, 16 rows each.
-    const long long queries = i || p.n_req == 0 ? p.n_tokens : (p.n_tokens + p.n_req - 1) / p.n_req;
-    L.tile_rows = queries * p.gqa <= 8 ? 8 : 16;
-    L.step = kPage;
-    L.runs = p.num_sms * kLineWarps;
-    if (i == 1) {
-      if (p.prefix_len == 0) continue;
-      if (by_tiles(p)) L.tile_rows = kTileRows, L.step = kTileTokens, L.runs = p.num_sms;
-    } else {
-      L.req = reinterpret_cast<Request*>(take(sizeof(Request) * (size_t)(L.n_req + 1)));
-      L.sizes = reinterpret_cast<long long*>(take(16));
-    }
+  const bool tiles = p.prefix_len > 0 && by_tiles(p);
+  a->mixed = p.prefix_len > 0 && !tiles;
+  a->early = tiles;
+  a->self = p.n_req <= kMaxSelf;
+  // (Joining a segment with the prefix's pieces as well, in the line kernel's
+  // epilogue, was slower: its warps wait for those loads, 105 to 168 us at 512
+  // requests of 64 heads, against 9 us less in the merge.)
+  a->join = p.prefix_len == 0;
+  a->request_of = reinterpret_cast<int32_t*>(take(sizeof(int32_t) * (size_t)p.n_tokens));
+  auto rows_of = [&](Line& L) {
+    L.row_o = reinterpret_cast<float*>(take(rows * p.d * 4));
+    L.row_ml = reinterpret_cast<float2*>(take(rows * 8));
+  };
+  auto pieces_of_runs = [&](Line& L) {
     for (L.tile_shift = 0; (1 << L.tile_shift) < L.tile_rows;) ++L.tile_shift;
     const size_t pieces = 2 * (size_t)L.runs * L.tile_rows;
     L.piece_o = reinterpret_cast<float*>(take(pieces * p.d * 4));
     L.piece_ml = reinterpret_cast<float2*>(take(pieces * 8));
-    L.row_o = reinterpret_cast<float*>(take(rows * p.d * 4));
-    L.row_ml = reinterpret_cast<float2*>(take(rows * 8));
+  };
+  Line& own = a->line[0];
+  Line& pre = a->line[1];
+  own = Line{};
+  // query rows of a tile: 8, or 16 where a request has more on average (the
+  // prefix by lines has at most 16).  32 were slower, with the registers they
+  // take: 62 us against 37 at 128 requests of up to four drafts, 16 rows each.
+  const long long queries = a->mixed || p.n_req == 0 ? p.n_tokens : (p.n_tokens + p.n_req - 1) / p.n_req;
+  own.tile_rows = queries * p.gqa <= 8 ? 8 : 16;
+  own.step = kPage;
+  own.runs = p.num_sms * kLineWarps;
+  own.req = reinterpret_cast<Request*>(take(sizeof(Request) * (size_t)(p.n_req + 1)));
+  own.sizes = reinterpret_cast<long long*>(take(16));
+  pieces_of_runs(own);
+  rows_of(own);
+  pre = own;  // mixed: the same line, pieces and all
+  if (tiles) {
+    pre.tile_rows = kTileRows;
+    pre.step = kTileTokens;
+    pre.runs = p.num_sms;
+    pieces_of_runs(pre);
   }
-  a->request_of = reinterpret_cast<int32_t*>(take(sizeof(int32_t) * (size_t)p.n_tokens));
-  // (Joining a segment with the prefix's pieces as well, in the line kernel's
-  // epilogue, was slower: eight warps an SM wait for those loads, 105 to 168 us
-  // at 512 requests of 64 heads, against 9 us less in the merge.)
-  a->join = p.prefix_len == 0;
-  a->early = p.prefix_len > 0 && by_tiles(p);
-  a->side_schedule = p.prefix_len > 0 && !a->early && p.n_req <= kMaxSideRequests;
+  if (p.prefix_len > 0) rows_of(pre);
   return at;
 }
 
 template <int D, bool kHalf, int NT>
-cudaError_t launch_line(const Args& a, int which, const CUtensorMap& mk, const CUtensorMap& mv,
-                        cudaStream_t s) {
+cudaError_t launch_line(const Args& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
   using R = Ring<D>;
   cudaError_t e = cudaFuncSetAttribute(prefix_line_kernel<D, kHalf, NT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmem);
@@ -696,14 +743,8 @@ cudaError_t launch_line(const Args& a, int which, const CUtensorMap& mk, const C
   cfg.dynamicSmemBytes = R::kSmem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = which == 0 ? 1 : 0;  // the own tokens': set up while the kernel before ends
-  return cudaLaunchKernelEx(&cfg, prefix_line_kernel<D, kHalf, NT>, mk, mv, a, which);
-}
-template <int D, bool kHalf>
-cudaError_t launch_line(const Args& a, int which, const CUtensorMap& mk, const CUtensorMap& mv,
-                        cudaStream_t s) {
-  return a.line[which].tile_rows == 8 ? launch_line<D, kHalf, 1>(a, which, mk, mv, s)
-                                      : launch_line<D, kHalf, 2>(a, which, mk, mv, s);
+  cfg.numAttrs = a.early || !a.self ? 1 : 0;  // (a kernel of this run comes before it)
+  return cudaLaunchKernelEx(&cfg, prefix_line_kernel<D, kHalf, NT>, mk, mv, a);
 }
 
 template <int D, bool kHalf>
@@ -714,23 +755,19 @@ cudaError_t run(const Args& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = make_page_map(&mv, p.v_pages, D, p.hkv, p.num_pages, true);
   if (e != cudaSuccess) return e;
-  if (!a.side_schedule) {
+  if (!a.self) {
     prefix_schedule_kernel<<<1, 1024, 0, s>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  if (p.prefix_len > 0) {
-    if (by_tiles(p)) {
-      CUtensorMap half;  // one 64-column half of a page-head
-      e = make_page_map(&half, p.k_pages, D, p.hkv, p.num_pages, false);
-      if (e != cudaSuccess) return e;
-      e = launch_prefix_tiles(a, half, mv, s);
-    } else {
-      e = launch_line<D, kHalf>(a, 1, mk, mv, s);
-    }
+  if (a.early) {
+    CUtensorMap half;  // one 64-column half of a page-head
+    e = make_page_map(&half, p.k_pages, D, p.hkv, p.num_pages, false);
+    if (e != cudaSuccess) return e;
+    e = launch_prefix_tiles(a, half, mv, s);
     if (e != cudaSuccess) return e;
   }
-  e = launch_line<D, kHalf>(a, 0, mk, mv, s);
+  e = a.line[0].tile_rows == 8 ? launch_line<D, kHalf, 1>(a, mk, mv, s) : launch_line<D, kHalf, 2>(a, mk, mv, s);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -29,15 +29,14 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 // request's keys), cut into equal runs of steps: the requests' own tokens, or
 // the prefix as a request of its own whose rows are all tokens'.
 struct Line {
-  Request* req;       // null: the prefix, see prefix_of()
-  long long* sizes;   // [0] steps in the line, [1] a run
+  Request* req;       // (own tokens)
+  long long* sizes;   // (own tokens) [0] steps in the line, [1] a run
   float* piece_o;     // [2 * runs][tile_rows][d]
   float2* piece_ml;   // [2 * runs][tile_rows]: {m, l}
   float* row_o;       // [tokens * hq][d]: segments in one run
   float2* row_ml;
-  const int32_t* table;
-  long long table_stride;
-  int n_req, width, causal, tile_rows, tile_shift, step;  // tile_rows = 1 << tile_shift; step: keys
+  int tile_rows, tile_shift;  // tile_rows = 1 << tile_shift
+  int step;           // keys
   int runs;           // warps (or CTAs) that the line is cut for
 };
 
@@ -45,8 +44,9 @@ struct Args {
   PrefixParams p;
   Line line[2];  // own tokens, prefix
   int32_t* request_of;  // [tokens] (of tokens that are some request's)
-  int side_schedule;  // the prefix by lines checks and sums up the requests on the side
-  int early;          // the own tokens' kernel starts while the prefix's still runs
+  int mixed;          // the prefix (of few rows) stands in the own tokens' line, before them
+  int self;           // the line kernel's CTAs check and sum up the requests themselves
+  int early;          // the line kernel starts while the tensor-core one still runs
   int join;           // own segments in one run are final
 };
 
@@ -54,11 +54,11 @@ __device__ __forceinline__ int tiles_of(const Request& r, int gqa, const Line& L
   return (r.n * gqa + L.tile_rows - 1) >> L.tile_shift;
 }
 
-// The prefix's line: one request of all queries.  Tokens of no request (the
-// padding of a batch of fixed size) are not counted.
+// The prefix as one request of all queries.  Tokens of no request (the padding
+// of a batch of fixed size) are not counted.
 struct Cuts {
   Request one;
-  long long total, run;
+  long long total, run;  // run: of its own line (not mixed)
 };
 __device__ __forceinline__ Cuts prefix_cuts(const Args& a) {
   const PrefixParams& p = a.p;
@@ -70,15 +70,17 @@ __device__ __forceinline__ Cuts prefix_cuts(const Args& a) {
   c.one.n = p.cu ? min(max(p.cu[p.n_req], 0), p.n_tokens) : p.n_tokens;
   c.one.np = L.step == kPage ? (p.prefix_len + kPage - 1) / kPage : (p.prefix_len + kTileTokens - 1) / kTileTokens;
   c.total = (long long)tiles_of(c.one, p.gqa, L) * p.hkv * c.one.np;
-  c.run = max(quotient(c.total + L.runs - 1, L.runs), L.step == kPage ? (long long)kMinPages : 1ll);
+  c.run = max(quotient(c.total + L.runs - 1, L.runs), 1ll);
   return c;
 }
-__device__ __forceinline__ Cuts own_cuts(const Args& a) {
-  Cuts c;
-  c.one = Request{};
-  c.total = __ldcg(a.line[0].sizes);
-  c.run = __ldcg(a.line[0].sizes + 1);
-  return c;
+// The own tokens' line (with the prefix before them, if mixed): a run.
+__device__ __forceinline__ long long own_run(const Args& a, long long total) {
+  return max(quotient(total + a.line[0].runs - 1, a.line[0].runs), (long long)kMinPages);
+}
+
+// (after the line kernel)
+__device__ __forceinline__ long long prefix_run(const Args& a, const Cuts& c) {
+  return a.mixed ? a.line[0].sizes[1] : c.run;
 }
 
 // Where a line's pieces of one query row lie: n of them (0: the line has no
@@ -113,37 +115,32 @@ __device__ __forceinline__ Pieces pieces_of(const Line& L, const Request& r, lon
   return q;
 }
 
-// Checks lengths and offsets and sums up the line of the requests' own pages:
-// tid of `threads` (a multiple of 32) threads, which meet at named barrier
-// `bar`; s_warp holds a word per warp.
-__device__ inline void schedule_own(const Args& a, int tid, int threads, int bar, long long* s_warp);
-
-
-
-__device__ inline void schedule_own(const Args& a, int tid, int threads, int bar, long long* s_warp) {
-  const PrefixParams& p = a.p;
-  const int lane = tid & 31, warp = tid >> 5;
-  const int per = (p.n_req + threads - 1) / threads;
-  const int b0 = min(tid * per, p.n_req), b1 = min(b0 + per, p.n_req);
-  int bad = 0;
-  auto request = [&](int b) {
-    Request r;
-    int len = p.lens[b], first = b, last = b + 1;
-    if (p.cu) first = p.cu[b], last = p.cu[b + 1];
-    if (len < 0 || len > p.width * kPage || first < 0 || last < first || last > p.n_tokens)
-      bad |= kBatchBadInput;
-    r.len = min(max(len, 0), p.width * kPage);
-    r.tok0 = min(max(first, 0), p.n_tokens);
-    r.n = min(max(last, r.tok0), p.n_tokens) - r.tok0;
-    r.np = (r.len + kPage - 1) / kPage;
-    r.p0 = 0;
-    return r;
-  };
-  auto work = [&](const Request& r) {
-    return (long long)tiles_of(r, p.gqa, a.line[0]) * r.np * p.hkv;
-  };
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += work(request(b));
+// A request, checked.
+__device__ __forceinline__ Request checked(const PrefixParams& p, int b, int& bad) {
+  Request r;
+  const int len = p.lens[b];
+  int first = b, last = b + 1;
+  if (p.cu) first = p.cu[b], last = p.cu[b + 1];
+  if (len < 0 || len > p.width * kPage || first < 0 || last < first || last > p.n_tokens) bad |= kBatchBadInput;
+  r.len = min(max(len, 0), p.width * kPage);
+  r.tok0 = min(max(first, 0), p.n_tokens);
+  r.n = min(max(last, r.tok0), p.n_tokens) - r.tok0;
+  r.np = (r.len + kPage - 1) / kPage;
+  r.p0 = 0;
+  return r;
+}
+__device__ __forceinline__ long long steps_of(const Args& a, const Request& r) {
+  return (long long)tiles_of(r, a.p.gqa, a.line[0]) * r.np * a.p.hkv;
+}
+// What the merge reads of it.
+__device__ __forceinline__ void publish(const Args& a, int b, const Request& r) {
+  a.line[0].req[b] = r;
+  if (a.p.cu)
+    for (int t = r.tok0; t < r.tok0 + r.n; ++t) a.request_of[t] = b;
+}
+// Inclusive scan over a block; s_warp holds a word per warp, total is the sum.
+__device__ __forceinline__ long long scan_block(long long mine, long long* s_warp, long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long v = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -151,25 +148,13 @@ __device__ inline void schedule_own(const Args& a, int tid, int threads, int bar
     if (lane >= off) v += o;
   }
   if (lane == 31) s_warp[warp] = v;
-  asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
-  long long at = v - mine, total = 0;
-  for (int w = 0; w < threads / 32; ++w) {
-    if (w == warp) at += total;
+  __syncthreads();
+  total = 0;
+  for (int w = 0; w < (int)blockDim.x / 32; ++w) {
+    if (w == warp) v += total;
     total += s_warp[w];
   }
-  for (int b = b0; b < b1; ++b) {
-    Request r = request(b);
-    r.p0 = at;
-    a.line[0].req[b] = r;
-    at += work(r);
-    if (p.cu)
-      for (int t = r.tok0; t < r.tok0 + r.n; ++t) a.request_of[t] = b;
-  }
-  if (bad && p.status) atomicOr(p.status, bad);
-  if (tid == 0) {
-    a.line[0].sizes[0] = total;
-    a.line[0].sizes[1] = max((total + a.line[0].runs - 1) / a.line[0].runs, (long long)kMinPages);
-  }
+  return v;
 }
 
 // Most query rows of a tile of the tensor-core prefix kernel: two of 128.

@@ -150,13 +150,12 @@ __device__ void stream_kv(const CUtensorMap* tmk, const CUtensorMap* tmv, const 
                           const Cta<D>& c, Walk walk) {
   using C = Cfg<D>;
   const PrefixParams& p = a.p;
-  const Line& L = a.line[1];
   const int lane = threadIdx.x & 31;
   const int n_pages = (p.prefix_len + kPage - 1) / kPage;
   auto page_of = [&](int j) {  // lane i < 8: page i of step j
     const int i = j * kStepPages + lane;
     if (lane >= kStepPages || i >= n_pages) return 0;
-    const int id = L.table[i];
+    const int id = p.prefix_pages[i];
     if ((unsigned)id < (unsigned)p.num_pages) return id;
     if (p.status) atomicOr(p.status, kBatchBadSlot);
     return p.num_pages;  // outside the tensor map: read as zeros
@@ -528,8 +527,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     else if (warp == 9)
       issue_products<D, kHalf>(a, c, walk, rows, tmem);
     else if (warp == 10) {
-      // The schedule's kernel has ended and its writes are there; only then may
-      // the own tokens' kernel, which reads them, start beside this one.
+      // The schedule's kernel, if there is one, has ended and its writes are there;
+      // only then may the own tokens' kernel, which reads them, start beside this one.
       asm volatile("griddepcontrol.wait;" ::: "memory");
       asm volatile("griddepcontrol.launch_dependents;");
     }
@@ -553,7 +552,8 @@ cudaError_t launch(const Args& a, const CUtensorMap& mk, const CUtensorMap& mv, 
   const long long blocks = ((long long)p.n_tokens * p.gqa + kTileRows - 1) / kTileRows;
   const long long steps = blocks * p.hkv * ((p.prefix_len + kTileTokens - 1) / kTileTokens);
   const unsigned grid = (unsigned)(steps < p.num_sms ? steps : p.num_sms);
-  // a programmatic dependent of the schedule's kernel, of which it reads nothing
+  // a programmatic dependent of the schedule's kernel (if there is one), of which
+  // it reads nothing
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -563,7 +563,7 @@ cudaError_t launch(const Args& a, const CUtensorMap& mk, const CUtensorMap& mv, 
   cfg.dynamicSmemBytes = Cfg<D>::kSmem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = a.self ? 0 : 1;
   return cudaLaunchKernelEx(&cfg, prefix_tile_kernel<D, kHalf>, mk, mv, a);
 }
 
