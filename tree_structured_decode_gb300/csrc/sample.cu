@@ -15,16 +15,19 @@
 // again, by then from L2.  The passes:
 //   1  the largest logit (and NaNs);
 //   2  with top-k or top-p: the bins, a histogram of counts and weights over the
-//      weight's exponent (2048 bins of 1/128 of a power of two; a second one for
-//      what is below 2^-16 where the first does not suffice), and the row's
-//      weight.  The bin where the kept prefix of the order (logit descending,
+//      weight's exponent (2048 bins down to 2^-16 or 2^-24; a second one for what
+//      is below where the first does not suffice), and the row's weight.  The bin where the kept prefix of the order (logit descending,
 //      index ascending) ends follows by a scan;
 //   3  for each such bin, the sums of what lies above it, segment by segment in
 //      index order, and a list of the bin's values, which one CTA compares all
 //      with all.  (A bin of more values is cut further by the float's bits.)
 // What is kept is then: bits above `key`, or equal and index at most `last`.
 // A draw finds its segment by the segments' running sums and walks through it.
-// Each pass is bound by the ~50 instructions of a weight, not by memory.
+// Bound by instructions: about 145 a logit in all passes, 42 of them a weight's.
+// 256 rows of 128000 fp32 logits with top-p take 247 us (131 MB: 0.53 TB/s); the
+// SMs that have two rows issue in 75 % of all cycles, the others have one.  A
+// histogram without its atomics saves 6 us, two weights at a time in packed
+// arithmetic nothing.  One row is bound by the barriers between its passes.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
@@ -46,7 +49,9 @@ constexpr int kThreads = 512;
 constexpr int kNumWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kSegments = 256;     // of a CTA's part, at most
-constexpr int kHeld = 61440;       // bytes of logits held in shared memory: two CTAs fit an SM
+// Bytes of logits held in shared memory, where two CTAs share an SM and where
+// each has one for itself.
+constexpr int kHeld = 61440, kHeldAlone = 163840;
 constexpr int kFew = 384;          // values of a bin that are compared all with all (at most the threads of a CTA)
 // The first histogram's range of exponents: down to 2^-16 for top-k, which need
 // not look at more than the largest logits, and to 2^-24 for top-p alone, which
@@ -736,8 +741,12 @@ struct Row {
   }
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p) {
+// kAlone: no more CTAs than SMs, and twice the registers, which hold all of a
+// row's state: 28 us for a row of 32000 against 32.  (With more rows two CTAs an
+// SM are as fast: 256 rows of 128000 take 243 us or 247, 256 halves of rows of
+// 50257 71 against 87.)
+template <typename T, bool kAlone>
+__global__ void __launch_bounds__(kThreads, kAlone ? 1 : 2) sample_kernel(const SampleParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Shown s_shown;
   __shared__ CountWeight s_warp[32];
@@ -979,12 +988,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   R.sync();  // this CTA's words may still be read
 }
 
-template <typename T>
+template <typename T, bool kAlone>
 cudaError_t run(SampleParams p, int ranks, cudaStream_t s) {
   p.slice = ((p.vocab + ranks - 1) / ranks + 127) / 128 * 128;
-  p.held = p.slice * sizeof(T) <= kHeld;
+  p.held = p.slice * sizeof(T) <= (kAlone ? kHeldAlone : kHeld);
   const size_t smem = 1024 * 8 + kSegments * 8 + kFew * 24 + 3 * kBins * 4 + (p.held ? p.slice * sizeof(T) : 0);
-  cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(sample_kernel<T, kAlone>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.rows * ranks);
@@ -998,16 +1007,24 @@ cudaError_t run(SampleParams p, int ranks, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = ranks > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, p);
+  return cudaLaunchKernelEx(&cfg, sample_kernel<T, kAlone>, p);
+}
+template <typename T>
+cudaError_t run(const SampleParams& p, int ranks, cudaStream_t s) {
+  return (long long)p.rows * ranks <= p.num_sms ? run<T, true>(p, ranks, s) : run<T, false>(p, ranks, s);
 }
 
 }  // namespace
 
 cudaError_t launch_sample(const SampleParams& p, cudaStream_t s) {
   if (p.rows == 0 || p.draws == 0) return cudaSuccess;
-  // few rows: more CTAs a row while there is room on the SMs (two fit one)
+  // Few rows: more CTAs a row, as long as each has an SM for itself.  (Up to two
+  // an SM was slower: 64 rows of 50257 39 against 44 us, 76 of 32000 33 against
+  // 49, 128 of 50257 70 against 71; faster only where a part is too large for
+  // shared memory, 150 rows of 128000 138 against 130.  A row of 32000 on 2, 4 or
+  // 8 CTAs: 37, 32, 40.)
   int ranks = 1;
-  while (ranks < kMaxRanks && (long long)p.rows * ranks <= p.num_sms && p.vocab / ranks > 4096) ranks *= 2;
+  while (ranks < kMaxRanks && 2ll * p.rows * ranks <= p.num_sms && p.vocab / ranks > 4096) ranks *= 2;
   if (p.dtype == kFp32) return run<float>(p, ranks, s);
   if (p.dtype == kBf16) return run<__nv_bfloat16>(p, ranks, s);
   return run<__half>(p, ranks, s);
