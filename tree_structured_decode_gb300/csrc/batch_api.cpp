@@ -180,7 +180,7 @@ tree_attn_status tree_attn_prefix_run(const void* q, int64_t q_stride, const voi
     // a warp's, or CTA's, share of the work is counted in 32 bits
     const int64_t kv_tiles = ((int64_t)n_tokens * p.gqa / 8 + n_requests + 1) * n_kv_heads;
     const int64_t most = std::max<int64_t>(table_width, prefix_len / ta::kPage + 1);
-    if (kv_tiles > INT64_MAX / most || kv_tiles * most / p.num_sms > INT32_MAX)
+    if (kv_tiles > INT64_MAX / most || kv_tiles * most / p.num_sms > INT32_MAX / 8)
       return fail(TA_ERR_UNSUPPORTED, "too many query rows for tables this wide or a prefix this long");
     if (!cu_new && n_tokens != n_requests)
       return fail(TA_ERR_INVALID_ARG, "without cu_new there is one query a request: n_tokens must be n_requests");

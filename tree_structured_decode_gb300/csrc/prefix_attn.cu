@@ -32,6 +32,12 @@ constexpr float kGrowLog2 = 8.f;  // the running maximum is raised when a score 
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr long long kWaitLimitNs = 2000000000ll;
 
+// (The line kernel's) All SMs without tensor-core tiles.
+__device__ __forceinline__ Split split_for_line(const Args& a, long long total) {
+  if (a.tiles) return split_of(a, prefix_cuts(a), total);
+  return Split{a.p.num_sms, Runs{1, 0, 1}};
+}
+
 // Batches of more requests than a CTA of the line kernel has threads.
 __global__ void __launch_bounds__(1024) prefix_schedule_kernel(const Args a) {
   __shared__ long long s_warp[32];
@@ -51,10 +57,7 @@ __global__ void __launch_bounds__(1024) prefix_schedule_kernel(const Args a) {
     publish(a, b, r);
   }
   if (bad && p.status) atomicOr(p.status, bad);
-  if (threadIdx.x == 0) {
-    a.line[0].sizes[0] = base + total;
-    a.line[0].sizes[1] = own_run(a, base + total);
-  }
+  if (threadIdx.x == 0) publish_sizes(a, base + total, split_for_line(a, base + total));
 }
 
 // ------------------------------------------------------------- attention
@@ -108,7 +111,6 @@ constexpr int kMaxPlaces = 2048;  // requests whose places are searched in share
 
 // 12 warps an SM hide one another's latencies; each has two pages (four at d =
 // 64) in flight or in use.
-constexpr int kLineWarps = 12;
 constexpr int kMaxSelf = kLineWarps * 32;  // requests that a CTA checks by itself, one a thread
 template <int D>
 struct Ring {
@@ -159,10 +161,7 @@ __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
   __syncwarp();
   // the next kernel may set itself up while this one runs
   asm volatile("griddepcontrol.launch_dependents;");
-  // The schedule, if there is one, is the kernel's before this one, which has to
-  // end first; or, early, the one's before that, which has ended (the
-  // tensor-core kernel let this one start only then).
-  if (!a.early) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the schedule, if there is one
 
   Request* requests = reinterpret_cast<Request*>(smem_raw + R::kPlaces);
   long long* places = reinterpret_cast<long long*>(smem_raw + R::kPlaces);
@@ -171,6 +170,7 @@ __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
   if (a.mixed) prefix = prefix_cuts(a);
   const long long base = prefix.total;  // the prefix's pages in the line
   long long total, run;
+  int ctas;  // that have a part of the line
   if (a.self) {
     const int b = threadIdx.x;
     int bad = 0;
@@ -179,12 +179,14 @@ __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
     const long long mine = b < p.n_req ? steps_of(a, r) : 0;
     r.p0 = base + scan_block(mine, reinterpret_cast<long long*>(smem_raw + R::kSum), total) - mine;
     total += base;
-    run = own_run(a, total);
+    const Split split = split_for_line(a, total);
+    ctas = split.line_ctas;
+    run = own_run(a, total, ctas);
     if (b < p.n_req) requests[b] = r;
     if (blockIdx.x == 0) {  // for the merge
       if (b < p.n_req) publish(a, b, r);
       if (bad && p.status) atomicOr(p.status, bad);
-      if (b == 0) L.sizes[0] = total, L.sizes[1] = run;
+      if (b == 0) publish_sizes(a, total, split);
     }
     __syncthreads();
   } else {
@@ -194,6 +196,7 @@ __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
     }
     total = __ldcg(L.sizes);
     run = __ldcg(L.sizes + 1);
+    ctas = split_for_line(a, total).line_ctas;
   }
   auto request = [&](int b) {  // (past L1: see above)
     if (b < 0) return prefix.one;
@@ -204,7 +207,8 @@ __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
     memcpy(&r, w, sizeof r);
     return r;
   };
-  const int w = warp * gridDim.x + blockIdx.x;
+  if ((int)blockIdx.x >= ctas) return;
+  const int w = warp * ctas + blockIdx.x;
   const long long x0 = min((long long)w * run, total);
   const int count = (int)(min(x0 + run, total) - x0);
 
@@ -457,8 +461,6 @@ __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
       }
     }
   }
-  // early: this kernel has ended only when the one before it has, for the merge
-  if (a.early) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ------------------------------------------------------------- merge
@@ -532,7 +534,7 @@ __global__ void __launch_bounds__(256, 3) prefix_merge_kernel(const Args a) {
   if (threadIdx.x == 0) {
     const Cuts cuts = prefix_cuts(a);
     const int tok = first / p.gqa;
-    const Pieces q = pieces_of(a.line[1], cuts.one, prefix_run(a, cuts), p, tok, kvh, first - tok * p.gqa);
+    const Pieces q = pieces_of(a.line[1], cuts.one, prefix_runs(a), p, tok, kvh, first - tok * p.gqa);
     s_w0 = q.w0;
     s_n = q.n;
     s_in = q.in;
@@ -540,7 +542,7 @@ __global__ void __launch_bounds__(256, 3) prefix_merge_kernel(const Args a) {
   }
   const int tok = row / p.gqa, in_head = row - tok * p.gqa;
   const long long at_row = (long long)tok * p.hq + kvh * p.gqa + in_head;
-  const long long run = p.n_req > 0 ? a.line[0].sizes[1] : 1;
+  const Runs runs = own_runs(a);
   __syncthreads();
   if (row >= rows) return;
   int b = tok;
@@ -550,7 +552,7 @@ __global__ void __launch_bounds__(256, 3) prefix_merge_kernel(const Args a) {
   Pieces po{&a.line[0], 0, at_row, 0, 0}, pp{&a.line[1], 0, at_row, 0, 0};
   if (tok >= own.tok0 && tok < own.tok0 + own.n) {
     if (tok < s_queries) pp = Pieces{&a.line[1], s_w0, at_row, s_n, s_in + half};  // else cu is broken
-    po = pieces_of(a.line[0], own, run, p, tok, kvh, in_head);
+    po = pieces_of(a.line[0], own, runs, p, tok, kvh, in_head);
   }
   if (a.join && po.n == 1) return;  // done by the line kernel
   const int n = po.n + pp.n;
@@ -620,8 +622,8 @@ __global__ void __launch_bounds__(256) prefix_merge_row_kernel(const Args a) {
   if (tok >= own.tok0 && tok < own.tok0 + own.n) {
     const int kvh = h / p.gqa;
     if (p.prefix_len > 0 && tok < cuts.one.n)
-      pp = pieces_of(a.line[1], cuts.one, prefix_run(a, cuts), p, tok, kvh, h - kvh * p.gqa);
-    po = pieces_of(a.line[0], own, a.line[0].sizes[1], p, tok, kvh, h - kvh * p.gqa);
+      pp = pieces_of(a.line[1], cuts.one, prefix_runs(a), p, tok, kvh, h - kvh * p.gqa);
+    po = pieces_of(a.line[0], own, own_runs(a), p, tok, kvh, h - kvh * p.gqa);
   }
   const int n = po.n + pp.n;
   if (a.join && po.n == 1) return;  // done by the line kernel (the whole block)
@@ -684,9 +686,8 @@ size_t lay_out(const PrefixParams& p, uint8_t* base, Args* a) {
     return q;
   };
   const size_t rows = (size_t)p.n_tokens * p.hq;
-  const bool tiles = p.prefix_len > 0 && by_tiles(p);
-  a->mixed = p.prefix_len > 0 && !tiles;
-  a->early = tiles;
+  a->tiles = p.prefix_len > 0 && by_tiles(p);
+  a->mixed = p.prefix_len > 0 && !a->tiles;
   a->self = p.n_req <= kMaxSelf;
   // (Joining a segment with the prefix's pieces as well, in the line kernel's
   // epilogue, was slower: its warps wait for those loads, 105 to 168 us at 512
@@ -714,11 +715,11 @@ size_t lay_out(const PrefixParams& p, uint8_t* base, Args* a) {
   own.step = kPage;
   own.runs = p.num_sms * kLineWarps;
   own.req = reinterpret_cast<Request*>(take(sizeof(Request) * (size_t)(p.n_req + 1)));
-  own.sizes = reinterpret_cast<long long*>(take(16));
+  own.sizes = reinterpret_cast<long long*>(take(5 * sizeof(long long)));
   pieces_of_runs(own);
   rows_of(own);
   pre = own;  // mixed: the same line, pieces and all
-  if (tiles) {
+  if (a->tiles) {
     pre.tile_rows = kTileRows;
     pre.step = kTileTokens;
     pre.runs = p.num_sms;
@@ -743,7 +744,7 @@ cudaError_t launch_line(const Args& a, const CUtensorMap& mk, const CUtensorMap&
   cfg.dynamicSmemBytes = R::kSmem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = a.early || !a.self ? 1 : 0;  // (a kernel of this run comes before it)
+  cfg.numAttrs = a.self ? 0 : 1;  // (the schedule comes before it)
   return cudaLaunchKernelEx(&cfg, prefix_line_kernel<D, kHalf, NT>, mk, mv, a);
 }
 
@@ -760,15 +761,15 @@ cudaError_t run(const Args& a, cudaStream_t s) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  if (a.early) {
+  e = a.line[0].tile_rows == 8 ? launch_line<D, kHalf, 1>(a, mk, mv, s) : launch_line<D, kHalf, 2>(a, mk, mv, s);
+  if (e != cudaSuccess) return e;
+  if (a.tiles) {
     CUtensorMap half;  // one 64-column half of a page-head
     e = make_page_map(&half, p.k_pages, D, p.hkv, p.num_pages, false);
     if (e != cudaSuccess) return e;
     e = launch_prefix_tiles(a, half, mv, s);
     if (e != cudaSuccess) return e;
   }
-  e = a.line[0].tile_rows == 8 ? launch_line<D, kHalf, 1>(a, mk, mv, s) : launch_line<D, kHalf, 2>(a, mk, mv, s);
-  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

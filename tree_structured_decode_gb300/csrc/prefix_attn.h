@@ -10,7 +10,8 @@
 namespace ta {
 
 constexpr int kTileTokens = 128;  // keys of a step of the tensor-core tiles
-constexpr int kMinPages = 4;    // shortest run of a warp of the line kernel
+constexpr int kMinPages = 4;      // shortest run of a warp of the line kernel
+constexpr int kLineWarps = 12;    // of a CTA of the line kernel
 
 // What the kernels know of a request, checked: its first token and row count
 // lie in the batch, its pages in the table.
@@ -30,7 +31,7 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 // the prefix as a request of its own whose rows are all tokens'.
 struct Line {
   Request* req;       // (own tokens)
-  long long* sizes;   // (own tokens) [0] steps in the line, [1] a run
+  long long* sizes;   // (own tokens) [0] steps in the line, [1] a run; the prefix's Runs: [2] longer, [3] shorter, [4] n_longer
   float* piece_o;     // [2 * runs][tile_rows][d]
   float2* piece_ml;   // [2 * runs][tile_rows]: {m, l}
   float* row_o;       // [tokens * hq][d]: segments in one run
@@ -46,7 +47,7 @@ struct Args {
   int32_t* request_of;  // [tokens] (of tokens that are some request's)
   int mixed;          // the prefix (of few rows) stands in the own tokens' line, before them
   int self;           // the line kernel's CTAs check and sum up the requests themselves
-  int early;          // the line kernel starts while the tensor-core one still runs
+  int tiles;          // the prefix goes to the tensor cores
   int join;           // own segments in one run are final
 };
 
@@ -54,11 +55,23 @@ __device__ __forceinline__ int tiles_of(const Request& r, int gqa, const Line& L
   return (r.n * gqa + L.tile_rows - 1) >> L.tile_shift;
 }
 
+// A line's runs: n_longer of one length, then those of another.
+struct Runs {
+  long long longer, shorter, n_longer;
+  __device__ __forceinline__ long long start(long long w) const {
+    return w <= n_longer ? w * longer : n_longer * longer + (w - n_longer) * shorter;
+  }
+  __device__ __forceinline__ long long of(long long x) const {
+    const long long in = x - n_longer * longer;
+    return in < 0 || shorter == 0 ? quotient(x, longer) : n_longer + quotient(in, shorter);
+  }
+};
+
 // The prefix as one request of all queries.  Tokens of no request (the padding
 // of a batch of fixed size) are not counted.
 struct Cuts {
   Request one;
-  long long total, run;  // run: of its own line (not mixed)
+  long long total;
 };
 __device__ __forceinline__ Cuts prefix_cuts(const Args& a) {
   const PrefixParams& p = a.p;
@@ -70,17 +83,64 @@ __device__ __forceinline__ Cuts prefix_cuts(const Args& a) {
   c.one.n = p.cu ? min(max(p.cu[p.n_req], 0), p.n_tokens) : p.n_tokens;
   c.one.np = L.step == kPage ? (p.prefix_len + kPage - 1) / kPage : (p.prefix_len + kTileTokens - 1) / kTileTokens;
   c.total = (long long)tiles_of(c.one, p.gqa, L) * p.hkv * c.one.np;
-  c.run = max(quotient(c.total + L.runs - 1, L.runs), 1ll);
   return c;
 }
-// The own tokens' line (with the prefix before them, if mixed): a run.
-__device__ __forceinline__ long long own_run(const Args& a, long long total) {
-  return max(quotient(total + a.line[0].runs - 1, a.line[0].runs), (long long)kMinPages);
-}
 
-// (after the line kernel)
-__device__ __forceinline__ long long prefix_run(const Args& a, const Cuts& c) {
-  return a.mixed ? a.line[0].sizes[1] : c.run;
+// How the SMs are shared.  The tiles are bound by arithmetic, the line kernel by
+// memory, so that half the SMs take the line nearly as fast (512 requests of 64
+// heads, 240 tokens each: 114 us on 76, 103 on 152).  The others go to the tiles
+// alone; those of the line take shorter runs of tiles behind it: 458 us instead
+// of 483 in all.  (A quarter, 478: 203 us for the line next to the tiles.)  A
+// step of the tiles lasts as long as kStepCost pages of the line there.
+// All SMs take the line first where it has much more to do than the tiles, and
+// where its rows are in tiles of 16, so that it is not bound by memory alone (128
+// requests of four drafts: 39 us on 152, 59 on 76, the whole 91 against 100).
+constexpr int kStepCost = 13;
+constexpr int kLateSteps = 2;  // what a CTA that starts behind the line loses
+struct Split {
+  int line_ctas;
+  Runs runs;  // of tiles
+};
+__device__ __forceinline__ Split split_of(const Args& a, const Cuts& prefix, long long pages) {
+  const int sms = a.line[1].runs;
+  const long long steps = prefix.total;
+  const int behind = a.line[0].tile_rows == 8 && pages <= 4 * kStepCost * steps ? sms / 2 : 0;
+  const int alone = sms - behind;
+  Split s{sms, Runs{0, 0, alone}};
+  if (behind > 0) {
+    s.line_ctas = behind;
+    const long long each = quotient(kStepCost * steps + pages, sms) - quotient(pages, behind);
+    s.runs.shorter = max(quotient(max(each, 0ll), kStepCost) - kLateSteps, 0ll);
+  }
+  long long run = max(quotient(steps - s.runs.shorter * behind + alone - 1, alone), 1ll);
+  if (s.runs.shorter == 0 && run < prefix.one.np) {
+    // a few steps more where no run has two segments then: one costs about 5
+    const int n = prefix.one.np, k = (int)quotient(n, run), even = n / k;
+    if (even * k == n && even - run <= 4) run = even;
+  }
+  s.runs.longer = run;
+  return s;
+}
+// The own tokens' line (with the prefix before them, if mixed) on so many CTAs.
+__device__ __forceinline__ long long own_run(const Args& a, long long total, int ctas) {
+  const long long warps = (long long)ctas * kLineWarps;
+  return max(quotient(total + warps - 1, warps), (long long)kMinPages);
+}
+// What the kernels after it need.
+__device__ __forceinline__ void publish_sizes(const Args& a, long long total, const Split& s) {
+  long long* to = a.line[0].sizes;
+  to[0] = total;
+  to[1] = own_run(a, total, s.line_ctas);
+  to[2] = s.runs.longer;
+  to[3] = s.runs.shorter;
+  to[4] = s.runs.n_longer;
+}
+__device__ __forceinline__ Runs own_runs(const Args& a) {
+  return Runs{a.line[0].sizes[1], 0, a.line[0].runs};
+}
+__device__ __forceinline__ Runs prefix_runs(const Args& a) {
+  const long long* from = a.line[0].sizes;
+  return a.mixed ? own_runs(a) : Runs{from[2], from[3], from[4]};
 }
 
 // Where a line's pieces of one query row lie: n of them (0: the line has no
@@ -101,16 +161,16 @@ struct Pieces {
 };
 // Pieces of token tok's q head h (of kv head kvh, its in-th) in line L, whose
 // request there is r.
-__device__ __forceinline__ Pieces pieces_of(const Line& L, const Request& r, long long run,
+__device__ __forceinline__ Pieces pieces_of(const Line& L, const Request& r, const Runs& runs,
                                             const PrefixParams& p, int tok, int kvh, int in_head) {
   Pieces q{&L, 0, (long long)tok * p.hq + kvh * p.gqa + in_head, 0, 0};
   if (r.np == 0) return q;
   const int in = (tok - r.tok0) * p.gqa + in_head;
   const long long seg = (long long)kvh * tiles_of(r, p.gqa, L) + (in >> L.tile_shift);
   const long long first = r.p0 + seg * r.np;
-  q.w0 = quotient(first, run);
-  const long long past = first - q.w0 * run + r.np - 1;  // the last step, from the first run's start
-  q.n = past < run ? 1 : (int)quotient(past, run) + 1;
+  q.w0 = runs.of(first);
+  const long long last = first + r.np - 1;
+  q.n = last < runs.start(q.w0 + 1) ? 1 : (int)(runs.of(last) - q.w0) + 1;
   q.in = in & (L.tile_rows - 1);
   return q;
 }

@@ -18,9 +18,10 @@
 // S of the next step may be issued right behind the P V that still reads P from
 // the same columns.
 //
-// Steps of all (kv head, row block) segments stand in one line; a CTA takes an
-// equal, contiguous run of it.  What it has of a segment goes out as {m, l} and
-// the unnormalised O in 32 bits.
+// Steps of all (kv head, row block) segments stand in one line; a CTA takes a
+// contiguous run of it.  What it has of a segment goes out as {m, l} and the
+// unnormalised O in 32 bits.  This kernel starts while the line kernel runs on
+// some of the SMs; CTAs that start behind it there have shorter runs.
 //
 // Every wait has a limit.  One that runs out sets the status word's timeout bit
 // and the CTA's abort flag; every role then stops issuing, waits (with a limit)
@@ -131,12 +132,12 @@ struct Walk {
     return true;
   }
 };
-__device__ __forceinline__ Walk walk_of(const Cuts& cuts, int rows) {
+__device__ __forceinline__ Walk walk_of(const Cuts& cuts, const Runs& runs, int rows) {
   Walk w;
   w.n = cuts.one.np;
   w.blocks = (rows + kTileRows - 1) / kTileRows;
-  const long long x = min((long long)blockIdx.x * cuts.run, cuts.total);
-  w.left = (int)(min(x + cuts.run, cuts.total) - x);
+  const long long x = min(runs.start(blockIdx.x), cuts.total);
+  w.left = (int)(min(runs.start(blockIdx.x + 1ll), cuts.total) - x);
   const long long u = quotient(x, max(w.n, 1));
   w.j = (int)(x - u * w.n);
   w.head = (int)quotient(u, max(w.blocks, 1));
@@ -485,8 +486,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int s_rows;
   if (c.base & 1023) {  // the swizzled layouts need it
     if (threadIdx.x == 0 && c.status) atomicOr(c.status, kBatchTimeout);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
+  // the merge may set itself up where there is room
+  asm volatile("griddepcontrol.launch_dependents;");
+  // pages in the own tokens' line, of which this kernel waits for no sum
+  __shared__ long long s_sums[kThreads / 32];
+  long long pages = 0, all_pages;
+  for (int b = threadIdx.x; b < a.p.n_req; b += kThreads) {
+    int bad = 0;
+    pages += steps_of(a, checked(a.p, b, bad));
+  }
+  scan_block(pages, s_sums, all_pages);
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       ptx::mbar_init(c.full(s), 1);
@@ -503,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_init(c.drain(), 1);
     const Cuts cuts = prefix_cuts(a);
     s_rows = cuts.one.n * a.p.gqa;
-    s_walk = walk_of(cuts, s_rows);
+    s_walk = walk_of(cuts, split_of(a, cuts, all_pages).runs, s_rows);
     *c.abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -527,10 +539,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     else if (warp == 9)
       issue_products<D, kHalf>(a, c, walk, rows, tmem);
     else if (warp == 10) {
-      // The schedule's kernel, if there is one, has ended and its writes are there;
-      // only then may the own tokens' kernel, which reads them, start beside this one.
+      // This kernel has ended only when the line kernel has: the merge waits for this one.
       asm volatile("griddepcontrol.wait;" ::: "memory");
-      asm volatile("griddepcontrol.launch_dependents;");
     }
     __syncwarp();
   }
@@ -552,8 +562,7 @@ cudaError_t launch(const Args& a, const CUtensorMap& mk, const CUtensorMap& mv, 
   const long long blocks = ((long long)p.n_tokens * p.gqa + kTileRows - 1) / kTileRows;
   const long long steps = blocks * p.hkv * ((p.prefix_len + kTileTokens - 1) / kTileTokens);
   const unsigned grid = (unsigned)(steps < p.num_sms ? steps : p.num_sms);
-  // a programmatic dependent of the schedule's kernel (if there is one), of which
-  // it reads nothing
+  // a programmatic dependent of the line kernel, of which it reads nothing
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -563,7 +572,7 @@ cudaError_t launch(const Args& a, const CUtensorMap& mk, const CUtensorMap& mv, 
   cfg.dynamicSmemBytes = Cfg<D>::kSmem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = a.self ? 0 : 1;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, prefix_tile_kernel<D, kHalf>, mk, mv, a);
 }
 
