@@ -126,6 +126,20 @@ def test_work_cut_into_runs(lens, prefix, heads):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lens,new,heads,prefix", [
+    ([100] * 40, None, (16, 4), 40001),                  # tiles beside the own pages, and behind them
+    ([700] * 9, None, (32, 8), 12000),
+    ([30] * 64, [3] * 64, (16, 2), 10000),               # own tiles of 16 rows
+    ([2000] * 60, [2] * 60, (24, 4), 500),               # own pages first, on all SMs
+    ([3000] * 40, None, (4, 2), 140),
+    ([0] * 50, None, (8, 2), 3000)])                     # no own pages at all
+def test_sms_shared_by_tiles_and_own_pages(lens, new, heads, prefix):
+    s = make(prefix, lens, new, *heads, 128, prefix)
+    out, lse = attend(to_gpu(s))
+    check(s, out, lse)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("requests", [383, 384, 385, 2500])
 @pytest.mark.parametrize("asking,heads,prefix", [(1, (16, 1), 700), (5, (4, 2), 33), (9, (2, 2), 9000), (300, (4, 2), 50)])
 def test_a_few_of_many_requests_ask(requests, asking, heads, prefix):

@@ -134,7 +134,10 @@ struct Ring {
 // with P^T turned by movmatrix.  (Rows as M want 16 of them: twice the products
 // and accumulators for the eight or fewer rows of one query.)  The running
 // maximum grows only when a score passes it by 2^8, so most pages need no
-// reduction across lanes.  Bound by reading K and V once.
+// reduction across lanes.  Bound by reading K and V once: 64000 page-heads of 16
+// x 128 (527 MB) in 103 us, 5.1 TB/s; while its SMs are busy 6.4 TB/s, but runs of
+// equal length do not end together.  (The pages by cp.async instead of TMA: 6 %
+// slower.  A CTA that joins its warps' pieces: three times as slow.)
 // The line is the requests' own pages, with the prefix's before them where it
 // has at most 16 query rows a kv head (b < 0 below).  Every CTA sums up the
 // requests by itself, which costs less than a kernel before this one.
@@ -514,54 +517,56 @@ __device__ __forceinline__ float inverse(float den) {
 }
 
 // Joins a row's (token, q head) pieces of both lines, where the line kernel has
-// not: half a warp a row, a block 16 rows of a kv head (which share their pieces
-// of the prefix).  What bounds it is the chain of loads (request, then {m, l} and
-// O at once), so up to four pieces are read together.
+// not: half a warp a row, a block 16 rows of a kv head, whose pieces one warp
+// looks up, a row a lane.  What bounds it is the chain of loads: request, then
+// {m, l} and O of two pieces at once (four, with the registers for three blocks an
+// SM instead of four, is as fast; four with four blocks 8 us slower at 32768 rows).
 constexpr int kMergeRows = 16;
+constexpr int kAtOnce = 2;  // pieces
 template <int D, bool kHalf>
-__global__ void __launch_bounds__(256, 3) prefix_merge_kernel(const Args a) {
+__global__ void __launch_bounds__(256, 4) prefix_merge_kernel(const Args a) {
   const PrefixParams& p = a.p;
   constexpr int E = D / 16;  // columns of a lane
   const int in = threadIdx.x & 15, half = threadIdx.x >> 4;
   const int rows = p.n_tokens * p.gqa;  // of a kv head
   const int chunks = (rows + kMergeRows - 1) / kMergeRows;
   const int kvh = blockIdx.x / chunks, first = (blockIdx.x - kvh * chunks) * kMergeRows;
-  const int row = first + half;
-  // the prefix's pieces of the block's first row; the tokens of some request
-  __shared__ long long s_w0;
-  __shared__ int s_n, s_in, s_queries;
+  struct Place {
+    long long w0, row;
+    int n, in;
+  };
+  __shared__ Place s_own[kMergeRows], s_prefix[kMergeRows];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (threadIdx.x == 0) {
+  if (threadIdx.x < kMergeRows) {
+    const int row = min(first + (int)threadIdx.x, rows - 1);
+    const int tok = row / p.gqa, in_head = row - tok * p.gqa;
+    const long long at_row = (long long)tok * p.hq + kvh * p.gqa + in_head;
     const Cuts cuts = prefix_cuts(a);
-    const int tok = first / p.gqa;
-    const Pieces q = pieces_of(a.line[1], cuts.one, prefix_runs(a), p, tok, kvh, first - tok * p.gqa);
-    s_w0 = q.w0;
-    s_n = q.n;
-    s_in = q.in;
-    s_queries = cuts.one.n;
+    int b = tok;
+    if (p.cu) b = tok < cuts.one.n ? a.request_of[tok] : -1;
+    Request own{};
+    if ((unsigned)b < (unsigned)p.n_req) own = a.line[0].req[b];
+    Pieces po{&a.line[0], 0, at_row, 0, 0}, pp{&a.line[1], 0, at_row, 0, 0};
+    if (tok >= own.tok0 && tok < own.tok0 + own.n) {
+      if (tok < cuts.one.n) pp = pieces_of(a.line[1], cuts.one, prefix_runs(a), p, tok, kvh, in_head);  // else cu is broken
+      po = pieces_of(a.line[0], own, own_runs(a), p, tok, kvh, in_head);
+    }
+    s_own[threadIdx.x] = Place{po.w0, po.row, po.n, po.in};
+    s_prefix[threadIdx.x] = Place{pp.w0, pp.row, pp.n, pp.in};
   }
-  const int tok = row / p.gqa, in_head = row - tok * p.gqa;
-  const long long at_row = (long long)tok * p.hq + kvh * p.gqa + in_head;
-  const Runs runs = own_runs(a);
   __syncthreads();
-  if (row >= rows) return;
-  int b = tok;
-  if (p.cu) b = tok < s_queries ? a.request_of[tok] : -1;
-  Request own{};
-  if ((unsigned)b < (unsigned)p.n_req) own = a.line[0].req[b];
-  Pieces po{&a.line[0], 0, at_row, 0, 0}, pp{&a.line[1], 0, at_row, 0, 0};
-  if (tok >= own.tok0 && tok < own.tok0 + own.n) {
-    if (tok < s_queries) pp = Pieces{&a.line[1], s_w0, at_row, s_n, s_in + half};  // else cu is broken
-    po = pieces_of(a.line[0], own, runs, p, tok, kvh, in_head);
-  }
+  if (first + half >= rows) return;
+  const Place own = s_own[half], pre = s_prefix[half];
+  const long long at_row = own.row;
+  const Pieces po{&a.line[0], own.w0, at_row, own.n, own.in}, pp{&a.line[1], pre.w0, at_row, pre.n, pre.in};
   if (a.join && po.n == 1) return;  // done by the line kernel
   const int n = po.n + pp.n;
   float M = -INFINITY, den = 0.f, acc[E] = {};
-  for (int k0 = 0; k0 < n; k0 += 4) {
-    float2 ml[4];
-    float4 v[4][E / 4];
+  for (int k0 = 0; k0 < n; k0 += kAtOnce) {
+    float2 ml[kAtOnce];
+    float4 v[kAtOnce][E / 4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kAtOnce; ++i) {
       const int k = k0 + i;
       ml[i] = make_float2(-INFINITY, 0.f);
 #pragma unroll
@@ -574,7 +579,9 @@ __global__ void __launch_bounds__(256, 3) prefix_merge_kernel(const Args a) {
         for (int e = 0; e < E / 4; ++e) v[i][e] = __ldcg(src + 16 * e + in);
       }
     }
-    const float m_new = fmaxf(fmaxf(M, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
+    float m_new = M;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) m_new = fmaxf(m_new, ml[i].x);
     const float base = m_new == -INFINITY ? 0.f : m_new;
     const float a0 = ptx::ex2(M - base);
     M = m_new;
@@ -582,7 +589,7 @@ __global__ void __launch_bounds__(256, 3) prefix_merge_kernel(const Args a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] *= a0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kAtOnce; ++i) {
       const float w = ptx::ex2(ml[i].x - base);
       den = fmaf(w, ml[i].y, den);
 #pragma unroll
@@ -670,12 +677,16 @@ __global__ void __launch_bounds__(256) prefix_merge_row_kernel(const Args a) {
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
-// Query rows from which the prefix goes to the tensor-core tiles.
+// Query rows (of a kv head) from which the prefix goes to the tensor-core tiles.
+// The line's tiles have up to 16, and read the prefix once each: 24 rows behind
+// 4000 tokens take 19 us by tensor-core tiles, 52 by the line; 16 rows 19 and 16
+// (64 rows behind 200 tokens 15 and 20, 16 rows 13 and 14).
 constexpr int kTileMinRows = 17;
 bool by_tiles(const PrefixParams& p) { return (long long)p.n_tokens * p.gqa >= kTileMinRows; }
 
-// Rows an SM up to which the merge takes a block a row.
-constexpr int kBlockRows = 8;
+// Rows an SM up to which the merge takes a block a row: 512 rows with prefixes
+// of 8000 24 us (half a warp a row: 47), 1216 rows 33 (32), of 500 26 (22).
+constexpr int kBlockRows = 4;
 
 // Lays the workspace out; returns its size.
 size_t lay_out(const PrefixParams& p, uint8_t* base, Args* a) {

@@ -10,7 +10,6 @@
 namespace ta {
 
 constexpr int kTileTokens = 128;  // keys of a step of the tensor-core tiles
-constexpr int kMinPages = 4;      // shortest run of a warp of the line kernel
 constexpr int kLineWarps = 12;    // of a CTA of the line kernel
 
 // What the kernels know of a request, checked: its first token and row count
@@ -92,10 +91,13 @@ __device__ __forceinline__ Cuts prefix_cuts(const Args& a) {
 // alone; those of the line take shorter runs of tiles behind it: 458 us instead
 // of 483 in all.  (A quarter, 478: 203 us for the line next to the tiles.)  A
 // step of the tiles lasts as long as kStepCost pages of the line there.
-// All SMs take the line first where it has much more to do than the tiles, and
-// where its rows are in tiles of 16, so that it is not bound by memory alone (128
-// requests of four drafts: 39 us on 152, 59 on 76, the whole 91 against 100).
+// All SMs take the line first where it has much more to do than the tiles (256
+// requests of 300 tokens behind 200: 69 us, on half the SMs 74), and from fewer
+// pages on where its rows are in tiles of 16, so that it is not bound by memory
+// alone (128 requests of four drafts: 39 us on 152, 59 on 76, the whole 91 against
+// 100; 64 requests of 300 tokens, four drafts, behind 500: 43 against 34).
 constexpr int kStepCost = 13;
+constexpr int kFewPages = 12;  // of a warp
 constexpr int kLateSteps = 2;  // what a CTA that starts behind the line loses
 struct Split {
   int line_ctas;
@@ -104,7 +106,9 @@ struct Split {
 __device__ __forceinline__ Split split_of(const Args& a, const Cuts& prefix, long long pages) {
   const int sms = a.line[1].runs;
   const long long steps = prefix.total;
-  const int behind = a.line[0].tile_rows == 8 && pages <= 4 * kStepCost * steps ? sms / 2 : 0;
+  const int warps = sms / 2 * kLineWarps;
+  const bool half = pages <= warps * kFewPages + (a.line[0].tile_rows == 8 ? 4 * kStepCost * steps : 0);
+  const int behind = half ? sms / 2 : 0;
   const int alone = sms - behind;
   Split s{sms, Runs{0, 0, alone}};
   if (behind > 0) {
@@ -124,7 +128,7 @@ __device__ __forceinline__ Split split_of(const Args& a, const Cuts& prefix, lon
 // The own tokens' line (with the prefix before them, if mixed) on so many CTAs.
 __device__ __forceinline__ long long own_run(const Args& a, long long total, int ctas) {
   const long long warps = (long long)ctas * kLineWarps;
-  return max(quotient(total + warps - 1, warps), (long long)kMinPages);
+  return max(quotient(total + warps - 1, warps), 1ll);
 }
 // What the kernels after it need.
 __device__ __forceinline__ void publish_sizes(const Args& a, long long total, const Split& s) {

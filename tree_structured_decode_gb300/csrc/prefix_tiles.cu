@@ -9,8 +9,12 @@
 //   pairs over S, O += P V.
 // The two tiles alternate: while one's softmax runs, the other's products do.
 // A step's products are 4 * 256 * 128 * d operations, its exponentials 256 * 128:
-// at d = 128 tensor cores and exponential units have about the same to do, and
-// what binds is the softmax warps' instructions.
+// at d = 128 tensor cores and exponential units have about the same to do.  A step
+// takes 1.66 us at d = 128 (1.54 PFLOP/s on 152 SMs); the products would take 1.05:
+// what binds is the chain S, softmax, P V of a tile, which the other tile's only
+// half covers.  (P handed over in two parts was slower, 434 against 371 us for 512
+// queries of 64 heads behind 32768 tokens.)  A segment costs another 8 us for its
+// queries, first S and output.
 //
 // Roles: warps 0-3 and 4-7 are the softmax of tile 0 and 1 (thread = row =
 // TMEM lane), warp 8 streams K and V by TMA (and zeroes V's rows past the
