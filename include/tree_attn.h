@@ -414,7 +414,8 @@ tree_attn_status tree_attn_append_slots(const void* k_new, const void* v_new, in
  * A row that sees no key, and every token at or past cu_new[n_requests], gets
  * out = 0 and lse = -inf.  Slots past a request's end may hold anything; those
  * of its tokens that a query does not see (later drafts) must be finite.  A
- * page id out of range reads as zeros and sets the status word.
+ * page id out of range reads as zeros and sets the status word.  With offsets
+ * that fall or leave the tokens, which set it too, no token has a request.
  * Errors: TA_ERR_INVALID_ARG, TA_ERR_ALIGNMENT, TA_ERR_UNSUPPORTED,
  * TA_ERR_BUFFER_TOO_SMALL (workspace), TA_ERR_CUDA. */
 tree_attn_status tree_attn_prefix_run(const void* q, int64_t q_stride, const void* k_pages,

@@ -254,6 +254,20 @@ def test_bad_values_on_the_device_are_said_and_stay_in_bounds():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("requests", [40, 600])
+@pytest.mark.parametrize("prefix", [0, 5, 500])
+def test_offsets_out_of_order_give_no_token_a_request(requests, prefix):
+    """Offsets that give all tokens to every second request, over and over: no such work is done."""
+    s = make(requests, [90] * requests, [1] * 4 + [0] * (requests - 4), 16 if prefix == 500 else 4, 2, 64, prefix)
+    c = to_gpu(s)
+    c["cu"] = torch.tensor(([0, 4] * requests)[: requests + 1], dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = attend(c, status=status)
+    assert status.item() == _abi.BATCH_BAD_INPUT
+    assert not out.any() and torch.isneginf(lse).all()
+
+
+@pytest.mark.gpu
 def test_no_request_no_token():
     s = to_gpu(make(7, [4], None, 4, 2, 64, 10))
     z = torch.zeros(0, dtype=torch.int32, device="cuda")

@@ -48,15 +48,18 @@ __global__ void __launch_bounds__(1024) prefix_schedule_kernel(const Args a) {
   int bad = 0;
   long long mine = 0, total;
   for (int b = b0; b < b1; ++b) mine += steps_of(a, checked(p, b, bad));
+  const bool broken = __syncthreads_or(bad & kBadOffsets);
+  if (broken) mine = 0;
   const long long base = a.mixed ? prefix_cuts(a).total : 0;
   long long at = base + scan_block(mine, s_warp, total) - mine;
   for (int b = b0; b < b1; ++b) {
     Request r = checked(p, b, bad);
+    if (broken) r.n = 0;
     r.p0 = at;
     at += steps_of(a, r);
     publish(a, b, r);
   }
-  if (bad && p.status) atomicOr(p.status, bad);
+  if (bad && p.status) atomicOr(p.status, bad & ~kBadOffsets);
   if (threadIdx.x == 0) publish_sizes(a, base + total, split_for_line(a, base + total));
 }
 
@@ -179,6 +182,7 @@ __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
     int bad = 0;
     Request r{};
     if (b < p.n_req) r = checked(p, b, bad);
+    if (__syncthreads_or(bad & kBadOffsets)) r.n = 0;
     const long long mine = b < p.n_req ? steps_of(a, r) : 0;
     r.p0 = base + scan_block(mine, reinterpret_cast<long long*>(smem_raw + R::kSum), total) - mine;
     total += base;
@@ -188,7 +192,7 @@ __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
     if (b < p.n_req) requests[b] = r;
     if (blockIdx.x == 0) {  // for the merge
       if (b < p.n_req) publish(a, b, r);
-      if (bad && p.status) atomicOr(p.status, bad);
+      if (bad && p.status) atomicOr(p.status, bad & ~kBadOffsets);
       if (b == 0) publish_sizes(a, total, split);
     }
     __syncthreads();

@@ -179,13 +179,17 @@ __device__ __forceinline__ Pieces pieces_of(const Line& L, const Request& r, con
   return q;
 }
 
-// A request, checked.
+// A request, checked.  Offsets out of order (kBadOffsets, beside the status bit)
+// could give tokens to many requests and make the line any length: then no
+// request has queries.
+constexpr int kBadOffsets = 256;
 __device__ __forceinline__ Request checked(const PrefixParams& p, int b, int& bad) {
   Request r;
   const int len = p.lens[b];
   int first = b, last = b + 1;
   if (p.cu) first = p.cu[b], last = p.cu[b + 1];
-  if (len < 0 || len > p.width * kPage || first < 0 || last < first || last > p.n_tokens) bad |= kBatchBadInput;
+  if (len < 0 || len > p.width * kPage) bad |= kBatchBadInput;
+  if (first < 0 || last < first || last > p.n_tokens) bad |= kBatchBadInput | kBadOffsets;
   r.len = min(max(len, 0), p.width * kPage);
   r.tok0 = min(max(first, 0), p.n_tokens);
   r.n = min(max(last, r.tok0), p.n_tokens) - r.tok0;

@@ -498,10 +498,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // pages in the own tokens' line, of which this kernel waits for no sum
   __shared__ long long s_sums[kThreads / 32];
   long long pages = 0, all_pages;
-  for (int b = threadIdx.x; b < a.p.n_req; b += kThreads) {
-    int bad = 0;
-    pages += steps_of(a, checked(a.p, b, bad));
-  }
+  int bad = 0;
+  for (int b = threadIdx.x; b < a.p.n_req; b += kThreads) pages += steps_of(a, checked(a.p, b, bad));
+  if (__syncthreads_or(bad & kBadOffsets)) pages = 0;
   scan_block(pages, s_sums, all_pages);
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
