@@ -9,6 +9,10 @@ the binding's entry points raises.
     plan = Plan(parent, node_kv_len, node_page_offsets, node_pages, num_pages,
                 query_node, query_kv_end, n_q_heads, n_kv_heads, head_dim)
     out, lse = plan.run(q, k_pages, v_pages)
+
+A decode loop whose lengths live on the GPU, so that one captured step serves
+all steps, has ``extend_tables``, ``append_slots``, ``prefix_attention`` and
+``sample``; they hold no state.
 """
 from ._abi import (  # noqa: F401
     LIB_PATH,
