@@ -9,23 +9,23 @@
 // does not depend on the order or the grid, and agrees with 64-bit arithmetic
 // except where u lies within about 2^-42 of a border.
 //
-// A row belongs to one CTA, or to a cluster of two or four where rows are few;
+// A row belongs to one CTA, or to a cluster of two or four where rows are few or long;
 // what the CTAs of a cluster have to tell one another goes through distributed
 // shared memory.  A part that fits lies in shared memory; a larger one is read
 // again, by then from L2.  The passes:
 //   1  the largest logit (and NaNs);
 //   2  with top-k or top-p: the bins, a histogram of counts and weights over the
 //      weight's exponent (2048 bins down to 2^-16 or 2^-24; a second one for what
-//      is below where the first does not suffice), and the row's weight.  The bin where the kept prefix of the order (logit descending,
-//      index ascending) ends follows by a scan;
+//      is below where the first does not suffice), and the row's weight.  The
+//      bin where the kept prefix of the order (logit descending, index ascending)
+//      ends follows by a scan;
 //   3  for each such bin, the sums of what lies above it, segment by segment in
 //      index order, and a list of the bin's values, which one CTA compares all
 //      with all.  (A bin of more values is cut further by the float's bits.)
 // What is kept is then: bits above `key`, or equal and index at most `last`.
 // A draw finds its segment by the segments' running sums and walks through it.
 // Bound by instructions: about 145 a logit in all passes, 42 of them a weight's.
-// 256 rows of 128000 fp32 logits with top-p take 247 us (131 MB: 0.53 TB/s); the
-// SMs that have two rows issue in 75 % of all cycles, the others have one.  A
+// 256 rows of 128000 fp32 logits with top-p take 224 us (131 MB: 0.59 TB/s).  A
 // histogram without its atomics saves 6 us, two weights at a time in packed
 // arithmetic nothing.  One row is bound by the barriers between its passes.
 #include <cooperative_groups.h>
@@ -1025,6 +1025,11 @@ cudaError_t launch_sample(const SampleParams& p, cudaStream_t s) {
   // 8 CTAs: 37, 32, 40.)
   int ranks = 1;
   while (ranks < kMaxRanks && 2ll * p.rows * ranks <= p.num_sms && p.vocab / ranks > 4096) ranks *= 2;
+  // Many rows: two a row where it is long, which evens out what the SMs have (160
+  // rows of 128000 fp32 150 against 186 us, 256 217 against 231, 1000 653 against
+  // 668; of 50257 bf16 160 84 against 92, 256 112 against 110; of 32000 fp32 300 88
+  // against 68; four a row were slower, 256 of 128000 233).
+  if (p.rows > p.num_sms && p.vocab > 65536) ranks = 2;
   if (p.dtype == kFp32) return run<float>(p, ranks, s);
   if (p.dtype == kBf16) return run<__nv_bfloat16>(p, ranks, s);
   return run<__half>(p, ranks, s);
