@@ -25,7 +25,7 @@
 // What is kept is then: bits above `key`, or equal and index at most `last`.
 // A draw finds its segment by the segments' running sums and walks through it.
 // Bound by instructions: about 145 a logit in all passes, 42 of them a weight's.
-// 256 rows of 128000 fp32 logits with top-p take 224 us (131 MB: 0.59 TB/s).  A
+// 256 rows of 128000 fp32 logits with top-p take 220 us (131 MB: 0.6 TB/s).  A
 // histogram without its atomics saves 6 us, two weights at a time in packed
 // arithmetic nothing.  One row is bound by the barriers between its passes.
 #include <cooperative_groups.h>
@@ -271,7 +271,7 @@ struct Row {
 
   // f(i, four logits) over the CTA's part by whole warps, end(s) after each
   // segment: a warp takes every 16th segment, a lane four logits of 128, kAhead
-  // loads in flight.
+  // loads in flight (one where each logit has much to do: two took 6 % longer).
   template <int kAhead, class F, class End>
   __device__ __forceinline__ void each(F f, End end) const {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -436,7 +436,7 @@ struct Row {
     long long all_hi = 0, all_lo = 0;
     int seg_hi = 0, seg_lo = 0;  // at most 32 of 2^20 and 2^21
     if (sum) {
-      each<2>(
+      each<1>(
           [&](int, const float (&v)[4]) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -456,7 +456,7 @@ struct Row {
         const float th = weight.parts(v, hi, lo);
         if (range.has(th)) put(range.bin(th), hi, lo);
       };
-      each<2>(
+      each<1>(
           [&](int i, const float (&v)[4]) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) q.push(v[k] >= low, v[k], i + k, bin);
@@ -502,7 +502,7 @@ struct Row {
       lo_sum += lo;
     };
     if (cut.key == 0) {  // all: no need to collect them
-      each<2>(
+      each<1>(
           [&](int, const float (&v)[4]) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) add(v[k], 0);
@@ -511,7 +511,7 @@ struct Row {
       return;
     }
     Queue q{queue, queue_at, 0};
-    each<2>(
+    each<1>(
         [&](int i, const float (&v)[4]) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) q.push(cut.has(key_of(v[k]), v0 + i + k), v[k], i + k, add);
@@ -587,7 +587,7 @@ struct Row {
     };
     // the bin's lower end, or the logit of bits least where that is higher
     const float low = below(-(range.from + (bin + 1) * ((range.to - range.from) / kBins)));
-    each<2>(
+    each<1>(
         [&](int i, const float (&v)[4]) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) q.push(v[k] >= low, v[k], i + k, sort);
@@ -660,7 +660,7 @@ struct Row {
       clear();
       near = false;
       safe = true;
-      each<2>(
+      each<1>(
           [&](int, const float (&v)[4]) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -686,7 +686,7 @@ struct Row {
   // The index of the n-th logit (from 1) of these bits.
   __device__ int index_of(uint32_t key, int n) {
     int count = 0;
-    each<2>(
+    each<1>(
         [&](int, const float (&v)[4]) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) count += key_of(v[k]) == key;
@@ -771,8 +771,8 @@ __global__ void __launch_bounds__(kThreads, kAlone ? 1 : 2) sample_kernel(const 
   Row<T> R{cluster, global, nullptr, (reinterpret_cast<uintptr_t>(global) & (4 * sizeof(T) - 1)) == 0,
            hist, hist + kBins, hist + 2 * kBins, few_key, few_at, few_w, seg_sum, &s_shown, s_warp,
            s_queue[warp], s_queue_at[warp], {}, 0.f, false, false, false, rank, ranks, v0, size, 128 * ((p.slice + 128 * kSegments - 1) / (128 * kSegments)), {}};
-  // segments of up to 1024 logits, of fewer where a warp would have none
-  R.seg = max(R.seg, min(1024, 128 * ((p.slice + 128 * kNumWarps - 1) / (128 * kNumWarps))));
+  // segments of up to 512 logits, of fewer where a warp would have none
+  R.seg = max(R.seg, min(512, 128 * ((p.slice + 128 * kNumWarps - 1) / (128 * kNumWarps))));
   const float temperature = p.temperature ? p.temperature[row] : p.temperature_all;
   const float min_p = p.min_p ? p.min_p[row] : p.min_p_all;
   if (tid == 0) {  // 64-bit arithmetic is slow here: once a CTA
