@@ -52,6 +52,8 @@ constexpr int kSegments = 256;     // of a CTA's part, at most
 // Bytes of logits held in shared memory, where two CTAs share an SM and where
 // each has one for itself.
 constexpr int kHeld = 61440, kHeldAlone = 163840;
+template <bool kAlone>
+constexpr int held_most = kAlone ? kHeldAlone : kHeld;
 constexpr int kFew = 384;          // values of a bin that are compared all with all (at most the threads of a CTA)
 // The first histogram's range of exponents: down to 2^-16 for top-k, which need
 // not look at more than the largest logits, and to 2^-24 for top-p alone, which
@@ -990,10 +992,14 @@ __global__ void __launch_bounds__(kThreads, kAlone ? 1 : 2) sample_kernel(const 
 
 template <typename T, bool kAlone>
 cudaError_t run(SampleParams p, int ranks, cudaStream_t s) {
+  constexpr int kTables = 1024 * 8 + kSegments * 8 + kFew * 24 + 3 * kBins * 4;
   p.slice = ((p.vocab + ranks - 1) / ranks + 127) / 128 * 128;
-  p.held = p.slice * sizeof(T) <= (kAlone ? kHeldAlone : kHeld);
-  const size_t smem = 1024 * 8 + kSegments * 8 + kFew * 24 + 3 * kBins * 4 + (p.held ? p.slice * sizeof(T) : 0);
-  cudaError_t e = cudaFuncSetAttribute(sample_kernel<T, kAlone>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  p.held = p.slice * sizeof(T) <= held_most<kAlone>;
+  const size_t smem = kTables + (p.held ? p.slice * sizeof(T) : 0);
+  // The limit is the kernel's, for all threads of the process: always the most
+  // that any call asks for, not this call's, which would fail another's launch.
+  cudaError_t e = cudaFuncSetAttribute(sample_kernel<T, kAlone>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kTables + held_most<kAlone>);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.rows * ranks);
