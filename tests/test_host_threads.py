@@ -56,3 +56,25 @@ def test_vocabularies_of_two_sizes(rows, small, large, temperature):
         return work
 
     together(work_of(small), work_of(large), work_of(small))
+
+
+def test_batches_of_two_sizes():
+    def work_of(requests):
+        lens = torch.arange(requests, device="cuda", dtype=torch.int32) % 32
+        table = torch.arange(3 * requests, device="cuda", dtype=torch.int32).reshape(requests, 3)
+        free = torch.arange(3 * requests, 4 * requests, device="cuda", dtype=torch.int32)
+        n_free = torch.tensor([requests], device="cuda", dtype=torch.int32)
+        new = torch.ones_like(lens)
+        before = [x.clone() for x in (lens, free, n_free)]
+        want = ta.extend_tables(lens, new, table, free, n_free, requests)
+        ta.extend_tables(lens, -new, table, free, n_free, 0)
+
+        def work(i):
+            got = ta.extend_tables(lens, new, table, free, n_free, requests)
+            ta.extend_tables(lens, back, table, free, n_free, 0)
+            if i % 200 == 199:
+                assert all(torch.equal(a, b) for a, b in zip((*want, *before), (*got, lens, free, n_free)))
+        back = -new
+        return work
+
+    together(work_of(4000), work_of(16384), calls=2000)

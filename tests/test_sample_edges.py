@@ -1,0 +1,33 @@
+"""Rows of logits at the edges of what sampling promises, against the
+definition in float64 (`oracle.batch.sample`)."""
+import pytest
+import torch
+
+from test_sample import check, numbers
+
+ta = pytest.importorskip("tree_structured_decode_gb300")
+
+INF = float("inf")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("vocab", [60, 9000])
+def test_infinity_is_above_the_largest_number(vocab):
+    """+inf shares the row among its like, not with the largest finite number: its weight is exp(-inf)."""
+    x = torch.randn((4, vocab), generator=torch.Generator().manual_seed(vocab)).cuda()
+    most = torch.finfo(torch.float32).max
+    x[0, 3], x[0, 40] = most, INF
+    x[1, ::2], x[1, [5, 51]] = most, INF
+    x[2, 7], x[2, 8:] = INF, most
+    x[3, 2], x[3, 50] = most, -INF  # no infinity: the largest number has the row for itself
+    for kw in (dict(temperature=0.0), {}, dict(top_k=3), dict(top_p=0.9), dict(min_p=0.3), dict(temperature=1e30, top_k=20, top_p=0.8)):
+        check(x, numbers(6, 4, 7), **kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("top_k", [2 ** 31 - 1, 2 ** 31, 2 ** 32 + 1, 2 ** 40, -2 ** 32 + 1])
+def test_a_top_k_of_any_size(top_k):
+    """At or above the vocabulary, or not above 0: off, whatever its size."""
+    x = torch.randn((3, 50), generator=torch.Generator().manual_seed(1)).cuda()
+    want = ta.sample(x, numbers(2, 3, 40))
+    assert all(torch.equal(a, b) for a, b in zip(want, ta.sample(x, numbers(2, 3, 40), top_k=top_k)))

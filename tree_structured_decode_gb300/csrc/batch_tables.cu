@@ -233,9 +233,13 @@ __global__ void __launch_bounds__(256) append_slots_kernel(const AppendSlotsPara
 
 cudaError_t launch_extend_tables(const ExtendParams& p, cudaStream_t s) {
   const size_t smem = 3 * sizeof(int32_t) * ((size_t)p.n_req + 1);
+  constexpr size_t kMost = 3 * sizeof(int32_t) * (kMaxRequests + 1);
+  static_assert(kMost + 2048 <= 227 * 1024, "the scans of the largest batch fit a CTA");
   if (smem > 40 * 1024) {  // more than any kernel may have unasked
+    // The limit is the kernel's, for all threads of the process: always the
+    // largest batch's, not this call's, which would fail another's launch.
     const cudaError_t e = cudaFuncSetAttribute(
-        extend_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        extend_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
