@@ -1,0 +1,26 @@
+"""Rows of logits at the edges of what sampling promises, against the
+definition in float64 (`oracle.batch.sample`)."""
+import pytest
+import torch
+
+from test_sample import check, numbers
+
+ta = pytest.importorskip("tree_structured_decode_gb300")
+
+INF = float("inf")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,vocab", [(3, 4000), (60, 8000), (3, 8000), (30, 30000), (3, 130000), (160, 70000)])
+@pytest.mark.parametrize("masked", [True, False])
+def test_top_k_ends_at_the_last_of_many_equal_logits(rows, vocab, masked):
+    """1000 equal logits, top-k 1000, and a top-p that ends among them; rows of one, two and four CTAs."""
+    g = torch.Generator().manual_seed(vocab)
+    x = torch.full((rows, vocab), -INF) if masked else torch.randn((rows, vocab), generator=g) - 9
+    for i in range(rows):
+        x[i, torch.randperm(vocab, generator=g)[:1000]] = 0.5
+    x = x.cuda()
+    some = range(0, rows, max(1, rows // 3))
+    for n, kw in enumerate([dict(top_p=0.75), dict(top_p=0.375), dict(top_p=1 - 2.0 ** -9, min_p=0.5), dict(top_p=0.0), {}]):
+        for _ in range(3):
+            check(x, numbers(n, rows, 5), rows=some, top_k=1000, **kw)

@@ -188,7 +188,7 @@ struct Cut {
 struct Shown {
   float top;         // its largest logit, and (greedy) the first index that has it
   int first, bad;
-  uint32_t kmin, kmax;
+  uint32_t kmin[2], kmax[2];  // bits of a bin's values: for top-k and for top-p
   CountWeight before;
   int bin, bin_n;
   int ties;
@@ -641,19 +641,21 @@ struct Row {
       }
       return true;
     }
-    // many values: cut the range of bits until one is left
+    // many values: cut the range of bits until one is left.  (Bounds of their own,
+    // as the lists: where the bin's values are all equal and top-k ends at the last
+    // of them, no barrier stands between the reads here and top-p's.)
     kmin = __reduce_min_sync(0xffffffffu, kmin);
     kmax = __reduce_max_sync(0xffffffffu, kmax);
-    if (threadIdx.x == 0) shown->kmin = 0xffffffffu, shown->kmax = 0;
+    if (threadIdx.x == 0) shown->kmin[which] = 0xffffffffu, shown->kmax[which] = 0;
     __syncthreads();
     if ((threadIdx.x & 31) == 0) {
-      atomicMin(&shown->kmin, kmin);
-      atomicMax(&shown->kmax, kmax);
+      atomicMin(&shown->kmin[which], kmin);
+      atomicMax(&shown->kmax[which], kmax);
     }
     sync();
     for (int r = 0; r < ranks; ++r) {
-      kmin = min(kmin, peer(r).kmin);
-      kmax = max(kmax, peer(r).kmax);
+      kmin = min(kmin, peer(r).kmin[which]);
+      kmax = max(kmax, peer(r).kmax[which]);
     }
     while (kmin != kmax) {
       const uint32_t span = kmax - kmin;
