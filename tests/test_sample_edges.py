@@ -24,3 +24,17 @@ def test_top_k_ends_at_the_last_of_many_equal_logits(rows, vocab, masked):
     for n, kw in enumerate([dict(top_p=0.75), dict(top_p=0.375), dict(top_p=1 - 2.0 ** -9, min_p=0.5), dict(top_p=0.0), {}]):
         for _ in range(3):
             check(x, numbers(n, rows, 5), rows=some, top_k=1000, **kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("vocab", [60, 9000])
+def test_infinity_is_above_the_largest_number(vocab):
+    """+inf shares the row among its like, not with the largest finite number: its weight is exp(-inf)."""
+    x = torch.randn((4, vocab), generator=torch.Generator().manual_seed(vocab)).cuda()
+    most = torch.finfo(torch.float32).max
+    x[0, 3], x[0, 40] = most, INF
+    x[1, ::2], x[1, [5, 51]] = most, INF
+    x[2, 7], x[2, 8:] = INF, most
+    x[3, 2], x[3, 50] = most, -INF  # no infinity: the largest number has the row for itself
+    for kw in (dict(temperature=0.0), {}, dict(top_k=3), dict(top_p=0.9), dict(min_p=0.3), dict(temperature=1e30, top_k=20, top_p=0.8)):
+        check(x, numbers(6, 4, 7), **kw)

@@ -242,7 +242,8 @@ struct Row {
   }
 
   // Logits i .. i + 3 (i a multiple of 4), -inf past the part's end; all: there
-  // are four.  Past pass 1 +inf counts as the largest finite number.
+  // are four.  Past pass 1, in a row that has +inf, it counts as the largest
+  // finite number and all else as -inf: its weight is exp(-inf).
   __device__ __forceinline__ void load4(int i, float (&v)[4], bool all) const {
     T y[4];
     if (held) {
@@ -267,7 +268,7 @@ struct Row {
     }
     if (infinite) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = fminf(v[k], kMostFinite);
+      for (int k = 0; k < 4; ++k) v[k] = v[k] == INFINITY ? kMostFinite : -INFINITY;
     }
   }
 
