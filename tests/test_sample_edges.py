@@ -38,3 +38,12 @@ def test_infinity_is_above_the_largest_number(vocab):
     x[3, 2], x[3, 50] = most, -INF  # no infinity: the largest number has the row for itself
     for kw in (dict(temperature=0.0), {}, dict(top_k=3), dict(top_p=0.9), dict(min_p=0.3), dict(temperature=1e30, top_k=20, top_p=0.8)):
         check(x, numbers(6, 4, 7), **kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("top_k", [2 ** 31 - 1, 2 ** 31, 2 ** 32 + 1, 2 ** 40, -2 ** 32 + 1])
+def test_a_top_k_of_any_size(top_k):
+    """At or above the vocabulary, or not above 0: off, whatever its size."""
+    x = torch.randn((3, 50), generator=torch.Generator().manual_seed(1)).cuda()
+    want = ta.sample(x, numbers(2, 3, 40))
+    assert all(torch.equal(a, b) for a, b in zip(want, ta.sample(x, numbers(2, 3, 40), top_k=top_k)))

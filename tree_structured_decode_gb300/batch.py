@@ -28,6 +28,13 @@ def _codes():
     return {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
+def _int32(name, x):
+    """A number as the C ABI takes it: refused where ctypes would cut it to its low 32 bits."""
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} = {x} does not fit 32 bits")
+    return x
+
+
 def _index(name, t):
     """The CUDA device's index of a tensor."""
     index = t.get_device()
@@ -63,6 +70,7 @@ def _table(t, rows, index, kind):
     if t.dtype is not kind or t.get_device() != index or t.dim() != 2:
         raise ValueError(f"block_table must be a 2-d {kind} tensor on cuda:{index}")
     n, width = t.shape
+    _int32("block_table's width", width)
     stride = t.stride(0)
     if n != rows:
         raise ValueError(f"block_table has {n} rows for {rows} requests")
@@ -101,8 +109,9 @@ def extend_tables(lens, n_new, block_table, free_pages, n_free, max_new, positio
     ``status`` (int32 ``[1]``, OR-ed) and ``include/tree_attn.h``."""
     import torch
 
+    _int32("max_new", max_new), _int32("position_base", position_base)
+    b, cap = _int32("lens' length", lens.numel()), _int32("free_pages' length", free_pages.numel())
     index, kind = _index("lens", lens), torch.int32
-    b, cap = lens.numel(), free_pages.numel()
     table, stride, width = _table(block_table, b, index, kind)
     lens_at, new_at = _vector("lens", lens, b, index, kind), _vector("n_new", n_new, b, index, kind)
     free_at, n_free_at = _vector("free_pages", free_pages, cap, index, kind), _vector("n_free", n_free, 1, index, kind)
@@ -159,12 +168,13 @@ def prefix_attention(q, k_pages, v_pages, block_table, lens, cu_new=None, prefix
     fp32 ``[tokens, q heads]`` (None without ``want_lse``)."""
     import torch
 
+    _int32("prefix_len", prefix_len)
     index, kind, dtype = _index("q", q), torch.int32, q.dtype
     pages, hkv, _, d = _pools(k_pages, v_pages, index)
     if dtype is not k_pages.dtype:
         raise ValueError(f"q must be of the pools' type {k_pages.dtype}")
     (t, hq, _), q_stride = _rows("q", q, dtype, d, index)
-    b = lens.numel()
+    b = _int32("lens' length", lens.numel())
     table, stride, width = _table(block_table, b, index, kind)
     lens_at = _vector("lens", lens, b, index, kind)
     cu_at = None if cu_new is None else _vector("cu_new", cu_new, b + 1, index, kind)
@@ -205,6 +215,8 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=Non
     nothing to draw."""
     import torch
 
+    for n in (*logits.shape, *u.shape):
+        _int32("a size of logits or u", n)
     index, real = _index("logits", logits), torch.float32
     code = _codes().get(logits.dtype)
     if code is None or logits.dim() != 2:
@@ -225,7 +237,9 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=Non
         elif isinstance(x, torch.Tensor):
             args += (_vector(name, x, rows, index, kind), off)
         else:
-            args += (None, type(off)(x))
+            x = type(off)(x)
+            # at or above the vocabulary, or not above 0, top_k is off: no number is cut to 32 bits
+            args += (None, min(max(x, 0), vocab) if kind is torch.int32 else x)
     context, handle = _launch_on(index, stream)
     with context:
         device = logits.device
