@@ -261,11 +261,14 @@ cudaError_t launch_append_kv(const uint16_t* k_new, const uint16_t* v_new, const
   const int chunks = d * 2 / 16;
   const long long n = 2LL * nq * hkv * chunks;
   const int blocks = (int)((n + 255) / 256 < 152 * 8 ? (n + 255) / 256 : 152 * 8);
-  append_kv_kernel<<<blocks, 256, 0, s>>>(reinterpret_cast<const uint4*>(k_new),
-                                          reinterpret_cast<const uint4*>(v_new), dst, nq, hkv,
-                                          chunks, reinterpret_cast<uint4*>(k_pages),
-                                          reinterpret_cast<uint4*>(v_pages));
-  return cudaGetLastError();
+  // The launch's own error: cudaGetLastError() would give one that another call left.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  return cudaLaunchKernelEx(&cfg, append_kv_kernel, reinterpret_cast<const uint4*>(k_new),
+                            reinterpret_cast<const uint4*>(v_new), dst, nq, hkv, chunks,
+                            reinterpret_cast<uint4*>(k_pages), reinterpret_cast<uint4*>(v_pages));
 }
 
 cudaError_t launch_lse_merge(const MergeParams& params, int d, cudaStream_t s) {

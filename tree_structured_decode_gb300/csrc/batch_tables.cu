@@ -264,12 +264,13 @@ cudaError_t launch_append_slots(const AppendSlotsParams& p, cudaStream_t s) {
   if (p.n_tokens == 0) return cudaSuccess;
   const int parts = (p.hkv * (p.d / 8) + 127) / 128;
   const long long warps = (long long)p.n_tokens * parts;
-  const unsigned blocks = (unsigned)((warps + 7) / 8);
-  if (p.d == 128)
-    append_slots_kernel<4><<<blocks, 256, 0, s>>>(p, parts);
-  else
-    append_slots_kernel<3><<<blocks, 256, 0, s>>>(p, parts);
-  return cudaGetLastError();
+  // The launch's own error: cudaGetLastError() would give one that another call left.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((warps + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  return p.d == 128 ? cudaLaunchKernelEx(&cfg, append_slots_kernel<4>, p, parts)
+                    : cudaLaunchKernelEx(&cfg, append_slots_kernel<3>, p, parts);
 }
 
 }  // namespace ta

@@ -772,8 +772,11 @@ cudaError_t run(const Args& a, cudaStream_t s) {
   e = make_page_map(&mv, p.v_pages, D, p.hkv, p.num_pages, true);
   if (e != cudaSuccess) return e;
   if (!a.self) {
-    prefix_schedule_kernel<<<1, 1024, 0, s>>>(a);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t one = {};  // (not by cudaGetLastError(), which gives what another call left)
+    one.gridDim = dim3(1);
+    one.blockDim = dim3(1024);
+    one.stream = s;
+    e = cudaLaunchKernelEx(&one, prefix_schedule_kernel, a);
     if (e != cudaSuccess) return e;
   }
   e = a.line[0].tile_rows == 8 ? launch_line<D, kHalf, 1>(a, mk, mv, s) : launch_line<D, kHalf, 2>(a, mk, mv, s);
