@@ -405,6 +405,9 @@ tree_attn_status tree_attn_append_slots(const void* k_new, const void* v_new, in
  *   prefix_pages, prefix_len   pages of the shared prefix (device) and its
  *                  tokens; 0 for none.
  *   softmax_scale  <= 0 selects 1/sqrt(head_dim).
+ *                  Scores, maxima, sums and accumulators are held in 32 bits;
+ *                  weights are rounded to q's type for the product with V (in
+ *                  fp16 below 2^-21 of the largest to a multiple of 2^-31).
  *   out            [n_tokens][n_q_heads][head_dim], q's type, contiguous; not
  *                  q's own memory.
  *   lse            fp32 [n_tokens][n_q_heads] (natural log), may be NULL.

@@ -134,7 +134,7 @@ struct Ring {
 // stages (K and V of one page, by TMA) and never waits for another warp.  Query
 // rows are the N of mma.m16n8k16, a page's 16 tokens its M and then its K:
 //   S^T = K Q^T (16 x 8 NT),  O^T += V^T P^T (d x 8 NT),
-// with P^T turned by movmatrix.  (Rows as M want 16 of them: twice the products
+// with P^T turned by movmatrix, in the queries' type (see kFp16Base).  (Rows as M want 16 of them: twice the products
 // and accumulators for the eight or fewer rows of one query.)  The running
 // maximum grows only when a score passes it by 2^8, so most pages need no
 // reduction across lanes.  Bound by reading K and V once: 64000 page-heads of 16
@@ -149,6 +149,7 @@ __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
     prefix_line_kernel(const __grid_constant__ CUtensorMap tmk,
                        const __grid_constant__ CUtensorMap tmv, const Args a) {
   using R = Ring<D>;
+  constexpr float kBase = kHalf ? kFp16Base : 0.f;  // m is that much below the largest score
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const PrefixParams& p = a.p;
   const Line& L = a.line[0];
@@ -361,7 +362,7 @@ __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
           if (tk0 + g + 8 >= vis[n][e]) sc[n][2 + e] = -INFINITY;
         }
         mx[n][e] = fmaxf(sc[n][e], sc[n][2 + e]) * p.scale_log2;
-        grow |= mx[n][e] > m[n][e] + kGrowLog2;
+        grow |= mx[n][e] > m[n][e] + (kBase + kGrowLog2);
       }
     }
     if (__any_sync(0xffffffffu, grow)) {
@@ -374,7 +375,7 @@ __global__ void __launch_bounds__(Ring<D>::kWarps * 32, 1)
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          x = fmaxf(x, m[n][e]);
+          x = fmaxf(x - kBase, m[n][e]);
           alpha[e] = x == m[n][e] ? 1.f : ptx::ex2(m[n][e] - x);
           m[n][e] = x;
           l[n][e] *= alpha[e];

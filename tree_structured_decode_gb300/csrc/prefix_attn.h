@@ -225,6 +225,18 @@ __device__ __forceinline__ long long scan_block(long long mine, long long* s_war
   return v;
 }
 
+// Weights P = 2^(s - m) are rounded to the queries' type for the product with V,
+// whose operands are of one type; the sums l add them before that.  Half a step
+// of the type each (2^-8 or 2^-11 of the weight), of either sign: the output's
+// error grows by 40 %, root mean square 0.0023 of the output's in bf16 and 0.00029
+// in fp16 behind 32768 tokens, where its own rounding alone gives 0.0017 and
+// 0.00021.  P as a pair of 16-bit parts would double P V.
+// fp16 ends at 2^-24, so m is held kFp16Base below the largest score there and P
+// goes up to 2^(8 + 7): a weight loses at most 2^-32 of the largest.  (With P up to
+// 2^8 it was 2^-25, and thousands of small weights together were lost by more than
+// the output's rounding.)
+constexpr float kFp16Base = 7.f;
+
 // Most query rows of a tile of the tensor-core prefix kernel: two of 128.
 constexpr int kTileRows = 256;
 // The prefix's pieces by tcgen05 (a.line[1] cut in steps of kTileTokens keys).

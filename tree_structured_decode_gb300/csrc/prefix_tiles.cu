@@ -6,7 +6,7 @@
 // both, 128 tokens a step, so each byte read from L2 serves 256 rows.  Per step
 // and tile, on tcgen05 with the accumulators in TMEM:
 //   S = Q K^T (128 x 128), online softmax on one row per thread, P as 16-bit
-//   pairs over S, O += P V.
+//   pairs over S (see kFp16Base), O += P V.
 // The two tiles alternate: while one's softmax runs, the other's products do.
 // A step's products are 4 * 256 * 128 * d operations, its exponentials 256 * 128:
 // at d = 128 tensor cores and exponential units have about the same to do.  A step
@@ -358,6 +358,7 @@ template <int D, bool kHalf>
 __device__ void softmax_rows(const Args& a, const Cta<D>& c, Walk walk, int rows,
                              uint32_t tmem, int t) {
   using C = Cfg<D>;
+  constexpr float kBase = kHalf ? kFp16Base : 0.f;  // m is that much below the largest score
   const PrefixParams& p = a.p;
   const Line& L = a.line[1];
   const int tid = threadIdx.x & 127, warp = tid >> 5;
@@ -405,9 +406,9 @@ __device__ void softmax_rows(const Args& a, const Cta<D>& c, Walk walk, int rows
         for (int k = 0; k < 128; k += 2) m4[(k >> 1) & 3] = ptx::max3(m4[(k >> 1) & 3], v[k], v[k + 1]);
         const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
         float alpha = 1.f;
-        if (mx > m + kRescaleLog2 || j == 0) {
-          alpha = j == 0 ? 1.f : ptx::ex2(m - mx);
-          m = mx;
+        if (mx > m + (kBase + kRescaleLog2) || j == 0) {
+          alpha = j == 0 ? 1.f : ptx::ex2(m - (mx - kBase));
+          m = mx - kBase;
         }
         l *= alpha;
         // the S that was waited for was issued behind the last P V: O holds it
