@@ -456,11 +456,16 @@ tree_attn_status tree_attn_prefix_workspace(int32_t n_requests, int32_t n_tokens
  * passes u times the total.
  *   - temperature not above 0: the largest logit (the first of equal ones).
  *     top_k <= 0 or >= vocab, top_p >= 1 (or NaN), min_p <= 0 (or NaN): off.
- *   - Weights are whole multiples of 2^-42 of the largest, summed exactly:
- *     results do not depend on the GPU's timing.
+ *   - Weights are whole multiples of 2^-42 of the largest, each off by at most
+ *     0.67 of these (over 4 million samples), and summed exactly: results do
+ *     not depend on the GPU's timing, and are those of exact weights except
+ *     where a filter's or u's border lies within vocab * 0.67 * 2^-42 (at most
+ *     4e-8) of the largest weight.  Tokens below about 2^-43 of it have weight
+ *     0 and are never drawn.
  *   - -inf is never drawn; a row with a NaN, or with nothing above -inf, gives
  *     token -1 and logprob NaN.  +inf shares the row among its like.
- *   - u below 0 (or NaN) counts as 0, 1 and above as the last kept token.
+ *   - u below 0 (or NaN) counts as 0; 1 and above gives the last kept token
+ *     of a weight above 0.
  * Errors: TA_ERR_INVALID_ARG, TA_ERR_ALIGNMENT, TA_ERR_UNSUPPORTED (vocab
  * above TREE_ATTN_MAX_VOCAB), TA_ERR_CUDA. */
 #define TREE_ATTN_MAX_VOCAB 262144

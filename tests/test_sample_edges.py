@@ -1,5 +1,7 @@
 """Rows of logits at the edges of what sampling promises, against the
 definition in float64 (`oracle.batch.sample`)."""
+import math
+
 import pytest
 import torch
 
@@ -47,3 +49,29 @@ def test_a_top_k_of_any_size(top_k):
     x = torch.randn((3, 50), generator=torch.Generator().manual_seed(1)).cuda()
     want = ta.sample(x, numbers(2, 3, 40))
     assert all(torch.equal(a, b) for a, b in zip(want, ta.sample(x, numbers(2, 3, 40), top_k=top_k)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("units", [0.3, 0.34, 0.66, 0.75, 1.4, 1.5, 2.3])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_flat_tail_of_tiny_weights(units, dtype):
+    """262143 equal weights of so many 2^-42: all rounded in one direction, by up to 0.67 units.  The token is right for a
+    number within 262144 * 0.67 * 2^-42 of u's place (and one unit: the place is a whole number); below half a unit the tail
+    is never drawn."""
+    n = 262144
+    x = torch.full((1, n), math.log(units * 2.0 ** -42))
+    first = 1000
+    x[0, first] = 0
+    x = x.to(dtype).cuda()
+    w = math.exp(x[0, 0].item())  # of the rounded logit
+    u = 1 - torch.cat([2.0 ** -torch.arange(12, 25).float(), torch.arange(1, 90) * 2.0 ** -24])
+    tokens, logprobs = ta.sample(x, u.reshape(1, -1).cuda())
+    total, off = 1 + (n - 1) * w, (n * 0.67 + 1) * 2.0 ** -42
+    before = lambda i: i * w if i <= first else 1 + (i - 1) * w  # noqa: E731
+    for t, lp, place in zip(tokens[0].tolist(), logprobs[0].tolist(), (u.double() * total).tolist()):
+        assert before(t) - off <= place <= before(t + 1) + off
+        assert t == first or w * 2.0 ** 42 >= 0.5
+        assert abs(lp - math.log((1 if t == first else w) / total)) <= 1e-5
+    for kw in (dict(top_p=1 - 2.0 ** -22), dict(top_k=1), dict(top_k=5), dict(min_p=0.5)):
+        got, _ = ta.sample(x, u.reshape(1, -1).cuda(), **kw)
+        assert (got == first).all()

@@ -5,9 +5,10 @@
 // so a sum that is off in its last bits gives another token.  The weights are
 // therefore whole numbers,
 //   w_i = round(2^42 exp((l_i - max) / T)),
-// computed to about that last unit, and every sum of them is exact: the result
-// does not depend on the order or the grid, and agrees with 64-bit arithmetic
-// except where u lies within about 2^-42 of a border.
+// off by at most 0.67 units (below exp(kLeast) they are 0), and every sum of them
+// is exact: the result does not depend on the order or the grid, and is that of
+// exact weights except where a border lies within vocab * 0.67 * 2^-42 (4e-8 at
+// 262144 logits, all off in one direction) of the largest weight.
 //
 // A row belongs to one CTA, or to a cluster of two or four where rows are few or long;
 // what the CTAs of a cluster have to tell one another goes through distributed
