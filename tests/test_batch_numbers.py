@@ -1,9 +1,12 @@
 """Numbers that do not fit the C ABI's 32 bits are refused, not cut."""
+import os
+import re
+
 import pytest
 import torch
 
 ta = pytest.importorskip("tree_structured_decode_gb300")
-from tree_structured_decode_gb300 import batch  # noqa: E402
+from tree_structured_decode_gb300 import _abi, batch  # noqa: E402
 
 TOO_LARGE = [2 ** 31, 2 ** 32 + 5, 2 ** 63, -2 ** 31 - 1, -2 ** 32 + 5]
 
@@ -37,3 +40,12 @@ def test_tensors_of_too_many_entries():
         ta.extend_tables(wide[0], wide[0], z.reshape(1, 1), z, z, 1)
     with pytest.raises(ValueError, match="32 bits"):
         ta.sample(torch.empty((2 ** 32 + 1, 1), device="meta"), torch.empty((2 ** 32 + 1,), device="meta"))
+
+
+def test_limits_and_bits_are_the_header_s():
+    path = os.path.join(os.path.dirname(__file__), "..", "include", "tree_attn.h")
+    with open(path) as f:
+        said = dict(re.findall(r"TREE_ATTN_(MAX_\w+|BATCH_\w+) =? ?(\d+)", f.read()))
+    assert len(said) == 7
+    for name, value in said.items():
+        assert getattr(_abi, name) == int(value), name

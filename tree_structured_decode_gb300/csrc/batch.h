@@ -61,7 +61,7 @@ struct PrefixParams {
 size_t prefix_workspace(const PrefixParams& p);
 cudaError_t launch_prefix_attention(const PrefixParams& p, void* workspace, cudaStream_t s);
 
-constexpr int kMaxVocab = 262144;  // segments of 1024 logits in one CTA
+constexpr int kMaxVocab = 262144;
 struct SampleParams {
   const void* logits;            // [rows][vocab], rows `stride` elements apart
   long long stride;

@@ -11,6 +11,16 @@
 #include "batch.h"
 #include "plan_state.h"
 
+// The limits that the kernels rest on, and the codes, are those of the ABI.
+static_assert(ta::kMaxRequests == TREE_ATTN_MAX_REQUESTS && ta::kMaxVocab == TREE_ATTN_MAX_VOCAB, "limits");
+static_assert((int)ta::kBf16 == TA_BF16 && (int)ta::kFp16 == TA_FP16 && (int)ta::kFp32 == TA_FP32, "types");
+static_assert((int)ta::kBatchNoPages == TREE_ATTN_BATCH_NO_PAGES &&
+                  (int)ta::kBatchTableFull == TREE_ATTN_BATCH_TABLE_FULL &&
+                  (int)ta::kBatchBadInput == TREE_ATTN_BATCH_BAD_INPUT &&
+                  (int)ta::kBatchBadSlot == TREE_ATTN_BATCH_BAD_SLOT &&
+                  (int)ta::kBatchTimeout == TREE_ATTN_BATCH_TIMEOUT,
+              "status bits");
+
 namespace {
 
 tree_attn_status fail(tree_attn_status s, const std::string& msg) {

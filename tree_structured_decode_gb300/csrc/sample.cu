@@ -50,6 +50,9 @@ constexpr int kThreads = 512;
 constexpr int kNumWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kSegments = 256;     // of a CTA's part, at most
+// A segment of the longest part has 1024 logits, 32 a lane, whose two sums (of up
+// to 2^20 and 2^21 each) stay in 32 bits.
+static_assert(kMaxVocab <= kSegments * 1024, "a lane's sums of a segment");
 // Bytes of logits held in shared memory, where two CTAs share an SM and where
 // each has one for itself.
 constexpr int kHeld = 61440, kHeldAlone = 163840;
