@@ -215,8 +215,9 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=Non
     nothing to draw."""
     import torch
 
-    for n in (*logits.shape, *u.shape):
-        _int32("a size of logits or u", n)
+    if logits.numel() >= 2 ** 31 or u.numel() >= 2 ** 31:  # else no size of them is
+        for n in (*logits.shape, *u.shape):
+            _int32("a size of logits or u", n)
     index, real = _index("logits", logits), torch.float32
     code = _codes().get(logits.dtype)
     if code is None or logits.dim() != 2:
@@ -238,8 +239,9 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=Non
             args += (_vector(name, x, rows, index, kind), off)
         else:
             x = type(off)(x)
-            # at or above the vocabulary, or not above 0, top_k is off: no number is cut to 32 bits
-            args += (None, min(max(x, 0), vocab) if kind is torch.int32 else x)
+            if kind is not real and not 0 <= x < vocab:
+                x = 0  # such a top_k is off, and need not fit 32 bits
+            args += (None, x)
     context, handle = _launch_on(index, stream)
     with context:
         device = logits.device
