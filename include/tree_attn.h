@@ -456,6 +456,7 @@ tree_attn_status tree_attn_prefix_workspace(int32_t n_requests, int32_t n_tokens
  * passes u times the total.
  *   - temperature not above 0: the largest logit (the first of equal ones).
  *     top_k <= 0 or >= vocab, top_p >= 1 (or NaN), min_p <= 0 (or NaN): off.
+ *     min_p above 1 counts as 1: the logits equal to the largest.
  *   - Weights are whole multiples of 2^-42 of the largest, each off by at most
  *     0.67 of these (over 4 million samples), and summed exactly: results do
  *     not depend on the GPU's timing, and are those of exact weights except

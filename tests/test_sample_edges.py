@@ -75,3 +75,20 @@ def test_a_flat_tail_of_tiny_weights(units, dtype):
     for kw in (dict(top_p=1 - 2.0 ** -22), dict(top_k=1), dict(top_k=5), dict(min_p=0.5)):
         got, _ = ta.sample(x, u.reshape(1, -1).cuda(), **kw)
         assert (got == first).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("temperature", [0.3, 1.0, 1e30])
+def test_min_p_of_one_and_above(temperature):
+    """Leaves the logits equal to the largest, all of them: any other weighs less than 1, at whatever temperature."""
+    x = torch.randn((5, 700), generator=torch.Generator().manual_seed(3))
+    for i in range(1, 5):
+        x[i, torch.randperm(700, generator=torch.Generator().manual_seed(i))[: 3 ** i]] = x[i].max()
+    x, u = x.cuda(), numbers(4, 5, 60)
+    want, _ = check(x, u, 1.0, min_p=1.0)
+    assert (x.gather(1, torch.from_numpy(want).long().cuda()) == x.amax(1, keepdim=True)).all()
+    ties = (x == x.amax(1, keepdim=True)).sum(1, keepdim=True)
+    for min_p in (1.0, 1.5, float("inf"), torch.full((5,), 3.0, device="cuda")):
+        tokens, logprobs = ta.sample(x, u, temperature, min_p=min_p)
+        assert (tokens.cpu().numpy() == want).all()
+        assert (logprobs + ties.log()).abs().max() <= 1e-5
