@@ -313,11 +313,12 @@ tree_attn_status tree_attn_plan_get_stats(tree_attn_plan_t plan,
 /* ------------------------------------------------------------------------
  * Operators of a decode loop whose lengths live on the GPU.
  *
- * A plan fixes lengths and pages when it is made.  The calls below take them
- * from device memory instead, so that one captured CUDA graph serves every
- * step of a batch: page tables grow on the GPU, new keys and values go to
- * their slots, the batch attends to a shared prefix and its own tokens, and
- * the next tokens are drawn.
+ * A plan fixes lengths and pages when it is made.  The calls below take the
+ * requests' from device memory instead, so that one captured CUDA graph serves
+ * every step of a batch: page tables grow on the GPU, new keys and values go
+ * to their slots, the batch attends to a shared prefix and its own tokens, and
+ * the next tokens are drawn.  What the host gives is fixed in such a graph: the
+ * sizes of the batch (requests, tokens, table width) and prefix_len.
  *
  *   - They hold no state: every buffer is the caller's, on the current
  *     device, 16-byte aligned where it holds keys, values or queries, 4-byte
@@ -382,7 +383,8 @@ tree_attn_status tree_attn_extend_tables(int32_t* lens, const int32_t* n_new, in
  *                  of a joint projection needs no copy).
  *   slots          per token; -1 is skipped, and so is a slot outside the
  *                  pools (which also sets the status word).
- * Two tokens with one slot leave either's values.  Errors:
+ * Two tokens with one slot leave either's values, each 16 bytes by themselves
+ * (and K and V).  Errors:
  * TA_ERR_INVALID_ARG, TA_ERR_ALIGNMENT, TA_ERR_UNSUPPORTED, TA_ERR_CUDA. */
 tree_attn_status tree_attn_append_slots(const void* k_new, const void* v_new, int64_t k_stride,
                                         int64_t v_stride, const int32_t* slots, int32_t n_tokens,
@@ -414,6 +416,10 @@ tree_attn_status tree_attn_append_slots(const void* k_new, const void* v_new, in
  *   workspace      device memory of tree_attn_prefix_workspace() bytes,
  *                  256-byte aligned; two runs that may overlap on the GPU need
  *                  two.
+ * Made for the few queries that a request has in a decode step.  A chunk of a
+ * prompt is accepted, and its prefix is as fast; its own keys are read once
+ * for every 16 query rows of a kv head, and the workspace holds its output
+ * twice in 32 bits.
  * A row that sees no key, and every token at or past cu_new[n_requests], gets
  * out = 0 and lse = -inf.  Slots past a request's end may hold anything; those
  * of its tokens that a query does not see (later drafts) must be finite.  A

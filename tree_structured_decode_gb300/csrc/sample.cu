@@ -751,9 +751,10 @@ struct Row {
 };
 
 // kAlone: no more CTAs than SMs, and twice the registers, which hold all of a
-// row's state: 28 us for a row of 32000 against 32.  (With more rows two CTAs an
-// SM are as fast: 256 rows of 128000 take 243 us or 247, 256 halves of rows of
-// 50257 71 against 87.)
+// row's state.  (L2 flushed, launch included: a row of 32000 fp32 on four CTAs 42 us
+// against 49 with the registers for two an SM, 100 rows of 50257 bf16 on one each 77
+// against 91.  With more CTAs than SMs two an SM are as fast or faster: 256 rows of
+// 50257 122 against 122, of 128000 on two each 238 against 274.)
 template <typename T, bool kAlone>
 __global__ void __launch_bounds__(kThreads, kAlone ? 1 : 2) sample_kernel(const SampleParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -1031,17 +1032,25 @@ cudaError_t run(const SampleParams& p, int ranks, cudaStream_t s) {
 
 cudaError_t launch_sample(const SampleParams& p, cudaStream_t s) {
   if (p.rows == 0 || p.draws == 0) return cudaSuccess;
-  // Few rows: more CTAs a row, as long as each has an SM for itself.  (Up to two
-  // an SM was slower: 64 rows of 50257 39 against 44 us, 76 of 32000 33 against
-  // 49, 128 of 50257 70 against 71; faster only where a part is too large for
-  // shared memory, 150 rows of 128000 138 against 130.  A row of 32000 on 2, 4 or
-  // 8 CTAs: 37, 32, 40.)
+  // Few rows: more CTAs a row, as long as each has an SM for itself.  (us on 1, 2, 4,
+  // L2 flushed and launch included: a row of 32000 52, 45, 42; 8 of 128000 143, 85, 54;
+  // 32 of 50257 76, 50, 42.  Two an SM: 64 of 50257 on four each 51 against 50, 76 of
+  // 32000 71 against 48, 128 of 50257 on two each 74 against 74; faster where a part
+  // does not fit shared memory, which this rule leaves: 150 of 128000 136 against 180.
+  // So do 38 rows of 32000, whose clusters of four do not find all 152 SMs free: 60
+  // against 49 on two each.)
   int ranks = 1;
   while (ranks < kMaxRanks && 2ll * p.rows * ranks <= p.num_sms && p.vocab / ranks > 4096) ranks *= 2;
-  // Many rows: two a row where it is long, which evens out what the SMs have (160
-  // rows of 128000 fp32 150 against 186 us, 256 217 against 231, 1000 653 against
-  // 668; of 50257 bf16 160 84 against 92, 256 112 against 110; of 32000 fp32 300 88
-  // against 68; four a row were slower, 256 of 128000 233).
+  // Many rows: two a row where it is long, which evens out what the SMs have.  (On 1
+  // and 2 each, fp32 with top-p / bf16 with all filters:
+  //              160 rows              256 rows              1000 rows
+  //    50257     106, 106 / 114, 106   121, 129 / 121, 121   317, 384 / 338, 363
+  //    60000     129, 112 / 108, 100   135, 131 / 139, 121   352, 391 / 375, 375
+  //    65537     138, 118 / 126, 122   148, 146 / 141, 151   392, 427 / 391, 451
+  //    80000     161, 134 / 152, 136   174, 162 / 168, 164   450, 462 / 446, 495
+  //   100000     189, 147 / 175, 157   215, 199 / 201, 205   589, 581 / 549, 599
+  //   128000     204, 169 / 195, 174   272, 239 / 247, 233   716, 676 / 655, 670
+  // The border follows the few hundred rows; it costs a thousand up to 18 %.)
   if (p.rows > p.num_sms && p.vocab > 65536) ranks = 2;
   if (p.dtype == kFp32) return run<float>(p, ranks, s);
   if (p.dtype == kBf16) return run<__nv_bfloat16>(p, ranks, s);
