@@ -483,6 +483,136 @@ tree_attn_status tree_attn_sample(const void* logits, int64_t stride, int32_t dt
                                   float top_p_all, const float* min_p, float min_p_all,
                                   int32_t* tokens, float* logprobs, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Prompts taken in, and trees of drafted tokens verified, with lengths on the
+ * GPU: the same conventions (page pools, tables, status word, capture) as
+ * above.  A step of a batch that verifies drafts:
+ *   tree_attn_extend_tables()   room for every node of the trees
+ *   tree_attn_append_slots()    their keys and values, layer by layer
+ *   tree_attn_chunk_run()       their attention, layer by layer
+ *   tree_attn_sample()          a token drawn at every node
+ *   tree_attn_accept_drafts()   the path that agrees with them
+ *   tree_attn_keep_drafts()     its keys and values moved together
+ *   tree_attn_extend_tables()   the other nodes taken back
+ * ------------------------------------------------------------------------ */
+
+/* Most nodes of a request's tree in a step. */
+#define TREE_ATTN_NODES_MAX 128
+
+/* Attention of several new tokens of each request, whose keys and values are in
+ * its pages already: a prompt or a chunk of one, or a tree of drafted tokens.
+ *   q, q_stride, k_pages, v_pages, num_pages, block_table, table_stride,
+ *   table_width, dtype, softmax_scale, out, lse
+ *                  as in tree_attn_prefix_run().
+ *   lens           tokens of each request, this step's among them.
+ *   cu_new[n_requests+1]   request b's n new tokens are [cu_new[b],
+ *                  cu_new[b+1]), its last n; NULL: one each, n_tokens ==
+ *                  n_requests.
+ *   parents[n_tokens]   NULL: new token i sees the request's first lens[b] - n +
+ *                  i + 1 tokens.  Else it sees the first lens[b] - n, itself, and
+ *                  the new tokens above it: parents[cu_new[b] + i] is the one
+ *                  right above (counted within the request, below i), -1 where
+ *                  there is none.  At most TREE_ATTN_NODES_MAX a request.
+ *   workspace      device memory of tree_attn_chunk_workspace() bytes, 256-byte
+ *                  aligned; two runs that may overlap on the GPU need two.
+ * Scores, maxima, sums and accumulators are held in 32 bits; weights are rounded
+ * to q's type for the product with V, as in tree_attn_prefix_run().
+ * A row that sees no key, and every token at or past cu_new[n_requests], gets
+ * out = 0 and lse = -inf.  Slots past a request's end may hold anything; those
+ * of its tokens that a query does not see must be finite.  A page id out of range
+ * reads as zeros; offsets that fall or leave the tokens leave every token without
+ * a request, and a tree of too many nodes its request without queries; a parent
+ * that is not below its node counts as -1; each sets the status word.
+ * Errors: TA_ERR_INVALID_ARG, TA_ERR_ALIGNMENT, TA_ERR_UNSUPPORTED,
+ * TA_ERR_BUFFER_TOO_SMALL (workspace), TA_ERR_CUDA. */
+tree_attn_status tree_attn_chunk_run(const void* q, int64_t q_stride, const void* k_pages,
+                                     const void* v_pages, int32_t num_pages,
+                                     const int32_t* block_table, int64_t table_stride,
+                                     int32_t table_width, const int32_t* lens,
+                                     const int32_t* cu_new, const int32_t* parents,
+                                     int32_t n_requests, int32_t n_tokens, int32_t n_q_heads,
+                                     int32_t n_kv_heads, int32_t head_dim, int32_t dtype,
+                                     float softmax_scale, void* out, float* lse, int32_t* status,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that tree_attn_chunk_run() needs for these sizes on the
+ * current device.  Errors: TA_ERR_INVALID_ARG, TA_ERR_UNSUPPORTED. */
+tree_attn_status tree_attn_chunk_workspace(int32_t n_requests, int32_t n_tokens, int32_t n_q_heads,
+                                           int32_t n_kv_heads, int32_t head_dim, size_t* bytes);
+
+/* The drafts that stand.  A request's node 0 is its last token, the others are
+ * drafted; sampled[] is the token that the model drew at each node.  Node 0 is
+ * kept, and of a kept node's children the first whose drafted token is what was
+ * drawn at that node, down to a node with no such child.  (Tokens drawn by
+ * tree_attn_sample() keep the model's own distribution.)
+ *   drafted, parents, sampled [n_tokens], cu_new [n_requests+1] (NULL: one node
+ *   each)          parents as in tree_attn_chunk_run().  A token below 0 matches
+ *                  nothing.
+ *   path[n_tokens] the kept nodes of request b, in order, from cu_new[b] on;
+ *                  -1 behind them.
+ *   n_kept[n_requests]      how many.
+ *   next_tokens[n_requests] the token drawn at the last kept one; -1 where a
+ *                  request has no nodes.
+ *   n_back[n_requests]      n_kept - nodes, for tree_attn_extend_tables().
+ *                  May be NULL.
+ * A request of more than TREE_ATTN_NODES_MAX nodes keeps none; with offsets that
+ * fall or leave the tokens no request has nodes; both, and a parent that is not
+ * below its node (which counts as -1), set the status word.
+ * Errors: TA_ERR_INVALID_ARG, TA_ERR_ALIGNMENT, TA_ERR_UNSUPPORTED, TA_ERR_CUDA. */
+tree_attn_status tree_attn_accept_drafts(const int32_t* drafted, const int32_t* parents,
+                                         const int32_t* cu_new, const int32_t* sampled,
+                                         int32_t n_requests, int32_t n_tokens, int32_t* path,
+                                         int32_t* n_kept, int32_t* next_tokens, int32_t* n_back,
+                                         int32_t* status, void* stream);
+
+/* Move the kept nodes' keys and values together, in place, every kv head of every
+ * layer: of request b with n nodes, what lies at position lens[b] - n + path[i]
+ * goes to lens[b] - n + i.  lens still counts all nodes.
+ *   path, cu_new   as tree_attn_accept_drafts() gives them: rising node numbers
+ *                  up to the first -1.
+ *   k_pages, v_pages   n_layers page pools, layer_stride elements apart (a
+ *                  multiple of 8; 0 counts as one pool's size).
+ * Only the positions that a kept node moves to are written.  A path that does not
+ * rise, and positions or pages out of range, end the request's moves there and
+ * set the status word.  Errors: TA_ERR_INVALID_ARG, TA_ERR_ALIGNMENT,
+ * TA_ERR_UNSUPPORTED, TA_ERR_CUDA. */
+tree_attn_status tree_attn_keep_drafts(const int32_t* path, const int32_t* cu_new,
+                                       const int32_t* lens, const int32_t* block_table,
+                                       int64_t table_stride, int32_t table_width,
+                                       int32_t n_requests, int32_t n_tokens, void* k_pages,
+                                       void* v_pages, int64_t layer_stride, int32_t n_layers,
+                                       int32_t num_pages, int32_t n_kv_heads, int32_t head_dim,
+                                       int32_t* status, void* stream);
+
+/* Log probabilities of given tokens, the entropy, and the likeliest tokens, of
+ * rows of logits.
+ *   logits, stride, dtype, n_rows, vocab   as in tree_attn_sample().
+ *   given          int32 [n_rows][n_given]: tokens asked for.
+ *   temperature    per row [n_rows] in device memory, or NULL: temperature_all.
+ *   given_logprobs fp32 [n_rows][n_given].
+ *   entropy        fp32 [n_rows], in nats; may be NULL.
+ *   top_tokens     int32 [n_rows][top], by falling logit, equal ones by index;
+ *   top_logprobs   fp32 [n_rows][top].
+ * With S = sum_j exp((l_j - max) / T): ln p_i = (l_i - max) / T - ln S, and the
+ * entropy is ln S + sum_j p_j (max - l_j) / T.  One pass over the logits; sums in
+ * 32 bits.
+ *   - A given token outside [0, vocab) has log probability NaN.
+ *   - -inf has log probability -inf and is never among the top tokens: where
+ *     there are fewer, -1 and -inf follow.
+ *   - A row with a NaN, or with nothing above -inf, gives NaN, and tokens -1.
+ *     +inf shares the row among its like.
+ *   - temperature not above 0: the largest logit (the first of equal ones) has
+ *     probability 1.
+ * Errors: TA_ERR_INVALID_ARG, TA_ERR_ALIGNMENT, TA_ERR_UNSUPPORTED (vocab above
+ * TREE_ATTN_MAX_VOCAB, top above TREE_ATTN_TOP_MAX), TA_ERR_CUDA. */
+#define TREE_ATTN_TOP_MAX 64
+tree_attn_status tree_attn_token_logprobs(const void* logits, int64_t stride, int32_t dtype,
+                                          int32_t n_rows, int32_t vocab, const int32_t* given,
+                                          int32_t n_given, const float* temperature,
+                                          float temperature_all, int32_t top,
+                                          float* given_logprobs, float* entropy,
+                                          int32_t* top_tokens, float* top_logprobs, void* stream);
+
 /* Release a plan and its device memory (NULL is ignored).  The caller must
  * make sure no run() of the plan is still executing on the GPU. */
 void tree_attn_plan_destroy(tree_attn_plan_t plan);

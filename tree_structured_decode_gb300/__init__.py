@@ -12,7 +12,9 @@ the binding's entry points raises.
 
 A decode loop whose lengths live on the GPU, so that one captured step serves
 all steps, has ``extend_tables``, ``append_slots``, ``prefix_attention`` and
-``sample``; they hold no state.
+``sample``; they hold no state.  Beside them: ``prompt_attention`` takes prompts
+in, ``draft_attention``, ``accept_drafts`` and ``keep_drafts`` verify trees of
+drafted tokens, ``token_logprobs`` scores tokens.
 """
 from ._abi import (  # noqa: F401
     LIB_PATH,
@@ -24,7 +26,9 @@ from ._abi import (  # noqa: F401
 )
 from .api import Plan, plan, run  # noqa: F401
 from .batch import append_slots, extend_tables, prefix_attention, sample  # noqa: F401
+from .drafts import accept_drafts, draft_attention, keep_drafts, prompt_attention, token_logprobs  # noqa: F401
 
 __all__ = ["Plan", "plan", "run", "extend_tables", "append_slots", "prefix_attention", "sample",
+           "prompt_attention", "draft_attention", "accept_drafts", "keep_drafts", "token_logprobs",
            "Options", "PlanStats", "TreeAttnError",
            "load_library", "status_string", "LIB_PATH"]

@@ -22,10 +22,12 @@ EXPORTS = (
     "tree_attn_profile_read", "tree_attn_run_static", "tree_attn_append_kv",
     "tree_attn_plan_describe_schedule", "tree_attn_extend_tables", "tree_attn_append_slots",
     "tree_attn_prefix_run", "tree_attn_prefix_workspace",
-    "tree_attn_sample",
+    "tree_attn_sample", "tree_attn_chunk_run", "tree_attn_chunk_workspace",
+    "tree_attn_accept_drafts", "tree_attn_keep_drafts", "tree_attn_token_logprobs",
 )
 MAX_REQUESTS = 16384
 MAX_VOCAB = 262144
+NODES_MAX, TOP_MAX = 128, 64  # nodes of a request's tree, alternatives of a row
 # Bits of the status word of the operators whose lengths live on the GPU.
 BATCH_NO_PAGES, BATCH_TABLE_FULL, BATCH_BAD_INPUT, BATCH_BAD_SLOT, BATCH_TIMEOUT = 1, 2, 4, 8, 16
 STATIC_SCRATCH_BYTES = 32 << 20
@@ -118,6 +120,17 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     f = ctypes.c_float
     lib.tree_attn_sample.argtypes = [p, n, i, i, i, p, i, p, f, p, i, p, f, p, f, p, p, p]
     lib.tree_attn_sample.restype = ctypes.c_int
+    lib.tree_attn_chunk_run.argtypes = [p, n, p, p, i, p, n, i, p, p, p, i, i, i, i, i, i, f, p, p, p, p,
+                                        ctypes.c_size_t, p]
+    lib.tree_attn_chunk_run.restype = ctypes.c_int
+    lib.tree_attn_chunk_workspace.argtypes = [i, i, i, i, i, ctypes.POINTER(ctypes.c_size_t)]
+    lib.tree_attn_chunk_workspace.restype = ctypes.c_int
+    lib.tree_attn_accept_drafts.argtypes = [p, p, p, p, i, i, p, p, p, p, p, p]
+    lib.tree_attn_accept_drafts.restype = ctypes.c_int
+    lib.tree_attn_keep_drafts.argtypes = [p, p, p, p, n, i, i, i, p, p, n, i, i, i, i, p, p]
+    lib.tree_attn_keep_drafts.restype = ctypes.c_int
+    lib.tree_attn_token_logprobs.argtypes = [p, n, i, i, i, p, i, p, f, i, p, p, p, p, p]
+    lib.tree_attn_token_logprobs.restype = ctypes.c_int
     lib.tree_attn_device_status.argtypes = [ctypes.c_void_p, ctypes.c_void_p, _I32P]
     lib.tree_attn_device_status.restype = ctypes.c_int
     lib.tree_attn_profile_enable.argtypes = [ctypes.c_void_p, ctypes.c_int32]

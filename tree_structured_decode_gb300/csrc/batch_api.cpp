@@ -8,8 +8,8 @@
 #include <string>
 
 #include "../../include/tree_attn.h"
+#include "api_checks.h"
 #include "batch.h"
-#include "plan_state.h"
 
 // The limits that the kernels rest on, and the codes, are those of the ABI.
 static_assert(ta::kMaxRequests == TREE_ATTN_MAX_REQUESTS && ta::kMaxVocab == TREE_ATTN_MAX_VOCAB, "limits");
@@ -23,35 +23,11 @@ static_assert((int)ta::kBatchNoPages == TREE_ATTN_BATCH_NO_PAGES &&
 
 namespace {
 
-tree_attn_status fail(tree_attn_status s, const std::string& msg) {
-  ta::set_last_error(msg);
-  return s;
-}
-tree_attn_status launched(cudaError_t e, const char* what) {
-  if (e == cudaSuccess) return TA_OK;
-  return fail(TA_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
-}
-bool off(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
-
-// Nothing is thrown across the ABI.
-template <class F>
-tree_attn_status guarded(F&& f) {
-  try {
-    ta::set_last_error("");
-    return f();
-  } catch (...) {
-    return TA_ERR_OOM;
-  }
-}
-
-// SMs of the current device (152 where there is none).
-int device_sms() {
-  int device = 0, sms = 0;
-  if (cudaGetDevice(&device) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || sms <= 0)
-    return 152;
-  return sms;
-}
+using ta::api::device_sms;
+using ta::api::fail;
+using ta::api::guarded;
+using ta::api::launched;
+using ta::api::off;
 
 // The sizes that decide the workspace of a prefix run.
 tree_attn_status prefix_sizes(int32_t n_requests, int32_t n_tokens, int32_t prefix_len,
