@@ -1,6 +1,23 @@
 // Log probabilities of given tokens, entropy and the likeliest tokens of rows of
-// logits (sm_103a): the plain form.  A CTA a row; a pass for the largest logit,
-// one for the sums, and one for each alternative.
+// logits (sm_103a), in one pass over them.
+//
+// With c = log2(e) / T, a thread's logits x, its largest so far m and t = (x - m) c:
+//   S = sum 2^t,  H' = sum 2^t (-t),
+// and where m grows by g / c, S becomes 2^-g S and H' 2^-g (H' + g S).  Threads
+// are joined by the same rule, and
+//   ln p_i = (x_i - max) / T - ln 2 log2 S,  entropy = ln 2 (log2 S + H' / S):
+// no term is negative, so nothing cancels.  Sums are in 32 bits, a thread's of its
+// own 1/128 or less of a row, then a tree.
+//
+// The likeliest k: a list in shared memory takes every logit above a threshold,
+// which rises to the list's k-th whenever the list has grown long (all compared
+// with all).  Where a round's logits would overflow it (the first round's always
+// do), the k-th largest of the threads' largest is a threshold that lets at most
+// k times a thread's part through.  Order is by (logit, index), one 64-bit key.
+//
+// A row belongs to a CTA, or to a cluster of up to eight where rows are few; their
+// sums and lists meet in the first one's shared memory.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -8,117 +25,365 @@
 #include <cstdint>
 
 #include "drafts.h"
+#include "ptx.cuh"
 
 namespace ta {
 namespace {
 
-constexpr int kThreads = 256;
+namespace cg = cooperative_groups;
 typedef unsigned long long u64;
 
-template <class T>
-__device__ __forceinline__ float value(const T* row, int i) { return (float)row[i]; }
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLowest = -3.402823466e38f, kLargest = 3.402823466e38f;
+constexpr float kNone = -200.f;  // 2^t of this or less counts as 0
+constexpr int kMaxCluster = 8;
 
+// Order-preserving bits of a float (no NaN); -0 and 0 have the same.
 __device__ __forceinline__ uint32_t key_of(float x) {
   const uint32_t b = __float_as_uint(x + 0.f);
   return b ^ (b >> 31 ? 0xffffffffu : 0x80000000u);
 }
-
-template <class F>
-__device__ __forceinline__ u64 block_max(u64 x, u64* s, F) {
-  for (int o = 16; o; o >>= 1) {
-    const u64 y = __shfl_xor_sync(0xffffffffu, x, o);
-    x = y > x ? y : x;
-  }
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = s[0];
-  for (int w = 1; w < kThreads / 32; ++w) x = s[w] > x ? s[w] : x;
-  __syncthreads();
-  return x;
+__device__ __forceinline__ float of_key(uint32_t k) {
+  return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xffffffffu));
 }
+__device__ __forceinline__ u64 key_at(float x, int i) { return (u64)key_of(x) << 32 | (uint32_t)~i; }
 
-__device__ __forceinline__ float block_sum(float x, float* s) {
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = 0;
-  for (int w = 0; w < kThreads / 32; ++w) x += s[w];
-  __syncthreads();
-  return x;
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
 template <class T>
+struct Type;
+template <>
+struct Type<float> {
+  static constexpr int kVec = 4, kVectors = 4;  // elements of a 16-byte load, loads of a thread and round
+  static constexpr uint32_t kNothing = 0xff800000u;  // -inf
+  static __device__ __forceinline__ void split(uint32_t w, float* v) { v[0] = __uint_as_float(w); }
+};
+template <>
+struct Type<__nv_bfloat16> {
+  static constexpr int kVec = 8, kVectors = 2;
+  static constexpr uint32_t kNothing = 0xff80ff80u;
+  static __device__ __forceinline__ void split(uint32_t w, float* v) {
+    v[0] = __uint_as_float(w << 16);
+    v[1] = __uint_as_float(w & 0xffff0000u);
+  }
+};
+template <>
+struct Type<__half> {
+  static constexpr int kVec = 8, kVectors = 2;
+  static constexpr uint32_t kNothing = 0xfc00fc00u;
+  static __device__ __forceinline__ void split(uint32_t w, float* v) {
+    const float2 f = ptx::unpack_f16(w);
+    v[0] = f.x, v[1] = f.y;
+  }
+};
+
+struct Sums {
+  float m, s, h;
+};
+// b's logits counted with a's.
+__device__ __forceinline__ Sums joined(const Sums& a, const Sums& b, float c) {
+  const float m = fmaxf(a.m, b.m);
+  const float ga = fminf((m - a.m) * c, -kNone), gb = fminf((m - b.m) * c, -kNone);
+  const float fa = ptx::ex2(-ga), fb = ptx::ex2(-gb);
+  return Sums{m, fmaf(a.s, fa, b.s * fb), fmaf(fmaf(ga, a.s, a.h), fa, fmaf(gb, b.s, b.h) * fb)};
+}
+__device__ __forceinline__ Sums joined_warp(Sums x, float c) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+    x = joined(x, Sums{__shfl_xor_sync(0xffffffffu, x.m, o), __shfl_xor_sync(0xffffffffu, x.s, o),
+                       __shfl_xor_sync(0xffffffffu, x.h, o)}, c);
+  return x;
+}
+
+// A list of at most kRoom keys.
+template <int kThreads, int kGroup>
+struct List {
+  // what is kept of it, and the logits of the threads that a threshold lets through
+  static constexpr int kRoom = kMaxTop + kMaxTop * kGroup;
+  u64 key[kRoom];
+  u64 best[kThreads > kMaxCluster * kMaxTop ? kThreads : kMaxCluster * kMaxTop];
+  u64 threshold;  // keys up to it are left out
+  int n, before;
+};
+
+// The k largest of from[0..n) to to[0..k), in order (0 where there are fewer).
+template <int kThreads>
+__device__ __forceinline__ void select_largest(const u64* from, int n, u64* to, int k) {
+  for (int i = threadIdx.x; i < k; i += kThreads)
+    if (i >= n) to[i] = 0;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const u64 mine = from[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += from[j] > mine;
+    if (rank < k) to[rank] = mine;
+  }
+}
+
+template <class T, int kThreads, bool kTop>
 __global__ void __launch_bounds__(kThreads) scores_kernel(const ScoreParams p) {
-  __shared__ u64 s_max[32];
-  __shared__ float s_sum[32];
-  const T* row = static_cast<const T*>(p.logits) + blockIdx.x * p.stride;
-  const int tid = threadIdx.x, r = blockIdx.x;
-  auto id = [] {};
-  u64 best = 0;
-  bool nan = false;
-  for (int i = tid; i < p.vocab; i += kThreads) {
-    const float x = value(row, i);
-    nan |= x != x;
-    const u64 k = ((u64)key_of(x) << 32) | (uint32_t)~i;
-    best = k > best ? k : best;
-  }
-  nan = __syncthreads_or(nan);
-  best = block_max(best, s_max, id);
-  const int at = (int)~(uint32_t)best;
-  const float top = value(row, at);
-  const bool broken = nan || top == -INFINITY;
-  const float T0 = p.temperature ? p.temperature[r] : p.temperature_all;
-  const bool greedy = !(T0 > 0);
-  const float inv = greedy ? 1.f : 1.f / T0;
-  // (max - x) / T of a logit: 0 for the largest, also where it is infinite
-  auto below = [&](float x, int i) -> float {
-    if (greedy) return i == at ? 0.f : INFINITY;
-    return x == top ? 0.f : (top - x) * inv;
+  constexpr int kVec = Type<T>::kVec, kVectors = Type<T>::kVectors, kGroup = kVectors * kVec;
+  constexpr int kWarps = kThreads / 32;
+  using Keys = List<kThreads, kGroup>;
+  __shared__ Keys s_list;
+  __shared__ Sums s_sums[kWarps], s_rank[kMaxCluster];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r = blockIdx.x / ranks;
+  const T* row = static_cast<const T*>(p.logits) + r * p.stride;
+  const float heat = p.temperature ? p.temperature[r] : p.temperature_all;
+  const bool greedy = !(heat > 0.f);
+  const float inv = greedy ? 1.f : 1.f / heat;
+  // (finite, and not 0: -inf stays below everything)
+  const float c = fminf(fmaxf(inv * kLog2e, 1.17549435e-38f), kLargest);
+  const int k = kTop ? (greedy ? max(p.top, 1) : p.top) : 0;
+
+  // the row as 16-byte vectors; `shift` elements of the first lie before it
+  const int shift = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+  const T* base = row - shift;
+  const int vectors = (shift + p.vocab + kVec - 1) / kVec, per = (vectors + ranks - 1) / ranks;
+  const int v0 = min(rank * per, vectors), v1 = min(v0 + per, vectors);
+  auto load = [&](int at, uint4 (&x)[kVectors]) {
+#pragma unroll
+    for (int u = 0; u < kVectors; ++u) {
+      const int v = at + u * kThreads + tid;
+      const int i0 = v * kVec - shift;
+      if (v < v1 && i0 >= 0 && i0 + kVec <= p.vocab) {
+        x[u] = load16(base + (long long)v * kVec);
+      } else {
+        uint32_t w[4] = {Type<T>::kNothing, Type<T>::kNothing, Type<T>::kNothing, Type<T>::kNothing};
+        if (v < v1) {
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) {
+            if (i0 + e < 0 || i0 + e >= p.vocab) continue;
+            if constexpr (sizeof(T) == 4) {
+              w[e] = reinterpret_cast<const uint32_t*>(row)[i0 + e];
+            } else {
+              const uint32_t h = reinterpret_cast<const uint16_t*>(row)[i0 + e];
+              w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | h << 16 : (w[e / 2] & 0xffff0000u) | h;
+            }
+          }
+        }
+        x[u] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
   };
-  float sum = 0, dot = 0;
-  for (int i = tid; i < p.vocab; i += kThreads) {
-    const float y = below(value(row, i), i), w = expf(-y);
-    sum += w;
-    if (w > 0) dot += w * y;
+
+  if (kTop) {
+    if (tid == 0) s_list.n = 0, s_list.threshold = 0, s_list.before = INT32_MAX;
+    __syncthreads();
   }
-  sum = block_sum(sum, s_sum);
-  dot = block_sum(dot, s_sum);
-  const float ln = logf(sum);
-  if (tid == 0 && p.entropy) p.entropy[r] = broken ? NAN : ln + dot / sum;
+  Sums sum{kLowest, 0.f, 0.f};
+  const uint64_t c2 = ptx::f2(c, c);
+  uint4 ahead[kVectors];
+  load(v0, ahead);
+  for (int at = v0; at < v1; at += kVectors * kThreads) {
+    float x[kGroup];
+#pragma unroll
+    for (int u = 0; u < kVectors; ++u) {
+      const uint32_t w[4] = {ahead[u].x, ahead[u].y, ahead[u].z, ahead[u].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) Type<T>::split(w[e], x + u * kVec + e * (kVec / 4));
+    }
+    if (at + kVectors * kThreads < v1) load(at + kVectors * kThreads, ahead);
+    float most = x[0];
+#pragma unroll
+    for (int e = 1; e + 1 < kGroup; e += 2) most = ptx::max3(most, x[e], x[e + 1]);
+    most = fmaxf(most, x[kGroup - 1]);
+    if (most > sum.m) {
+      const float g = fminf((most - sum.m) * c, -kNone), f = ptx::ex2(-g);
+      sum.h = fmaf(g, sum.s, sum.h) * f;
+      sum.s *= f;
+      sum.m = most;
+    }
+    {
+      const uint64_t low = ptx::f2(-sum.m, -sum.m);
+      uint64_t s2[2] = {0ull, 0ull}, h2[2] = {0ull, 0ull};
+#pragma unroll
+      for (int e = 0; e < kGroup; e += 2) {
+        float t0, t1;
+        ptx::f2_split(ptx::fma_f32x2(ptx::add_f32x2(ptx::f2(x[e], x[e + 1]), low), c2, 0ull), t0, t1);
+        t0 = max_nan(t0, kNone), t1 = max_nan(t1, kNone);
+        const uint64_t w = ptx::f2(ptx::ex2(t0), ptx::ex2(t1));
+        s2[e / 2 & 1] = ptx::add_f32x2(s2[e / 2 & 1], w);
+        h2[e / 2 & 1] = ptx::fma_f32x2(w, ptx::f2(t0, t1), h2[e / 2 & 1]);
+      }
+      float a, b;
+      ptx::f2_split(ptx::add_f32x2(s2[0], s2[1]), a, b);
+      sum.s += a + b;
+      ptx::f2_split(ptx::add_f32x2(h2[0], h2[1]), a, b);
+      sum.h -= a + b;
+    }
+    if (kTop && k > 0) {
+      const int tighten = 4 * k + 64;  // long enough to be worth a pass
+      const auto index = [&](int e) { return (at + (e / kVec) * kThreads + tid) * kVec - shift + e % kVec; };
+      u64 low = s_list.threshold;
+      const auto push = [&]() {  // true where the list has become long
+        if (!(most > -INFINITY) || (low && most < of_key((uint32_t)(low >> 32)))) return false;
+        int hits = 0;
+#pragma unroll
+        for (int e = 0; e < kGroup; ++e) hits += x[e] > -INFINITY && key_at(x[e], index(e)) > low;
+        if (hits == 0) return false;
+        int to = atomicAdd(&s_list.n, hits);
+        if (to + hits > Keys::kRoom) return true;
+#pragma unroll
+        for (int e = 0; e < kGroup; ++e)
+          if (x[e] > -INFINITY && key_at(x[e], index(e)) > low) s_list.key[to++] = key_at(x[e], index(e));
+        return to > tighten;
+      };
+      const int before = s_list.n;  // with what others have pushed in this round: the least of all is before it
+      if (__syncthreads_or(push())) {
+        const bool over = s_list.n > Keys::kRoom;
+        if (over) atomicMin(&s_list.before, before);
+        __syncthreads();
+        const int n = over ? s_list.before : s_list.n;
+        if (n > k) {
+          select_largest<kThreads>(s_list.key, n, s_list.best, k);
+          __syncthreads();
+          for (int i = tid; i < k; i += kThreads) s_list.key[i] = s_list.best[i];
+          if (tid == 0) s_list.n = k, s_list.threshold = s_list.best[k - 1];
+        } else {
+          __syncthreads();
+          if (tid == 0) s_list.n = n;
+        }
+        __syncthreads();
+        if (over) {  // this round's go again, with a threshold that they fit behind
+          u64 mine = 0;
+#pragma unroll
+          for (int e = 0; e < kGroup; ++e) {
+            const u64 key = x[e] > -INFINITY ? key_at(x[e], index(e)) : 0;
+            mine = key > mine ? key : mine;
+          }
+          s_list.best[tid] = mine;
+          __syncthreads();
+          int above = 0;
+          for (int j = 0; j < kThreads; ++j) above += s_list.best[j] > mine;
+          if (above == k - 1 && mine && mine - 1 > s_list.threshold) s_list.threshold = mine - 1;
+          if (tid == 0) s_list.before = INT32_MAX;
+          __syncthreads();
+          low = s_list.threshold;
+          push();
+          __syncthreads();
+        }
+      }
+    }
+  }
+
+  // ---- the row's sums and list
+  sum = joined_warp(sum, c);
+  if (lane == 0) s_sums[warp] = sum;
+  __syncthreads();
+  if (warp == 0) {
+    Sums x = lane < kWarps ? s_sums[lane] : Sums{kLowest, 0.f, 0.f};
+    x = joined_warp(x, c);
+    if (lane == 0) *cluster.map_shared_rank(&s_rank[rank], 0) = x;
+  }
+  if (kTop) {
+    __syncthreads();
+    select_largest<kThreads>(s_list.key, s_list.n, s_list.best, k);
+    __syncthreads();
+    if (ranks > 1) {  // (the first one's keys are its own list's until all have been ranked)
+      u64* to = cluster.map_shared_rank(s_list.key, 0);
+      cluster.sync();
+      for (int i = tid; i < k; i += kThreads) to[rank * k + i] = s_list.best[i];
+    }
+  }
+  if (ranks > 1)
+    cluster.sync();
+  else
+    __syncthreads();
+  if (rank) return;
+  if (kTop && ranks > 1) {
+    select_largest<kThreads>(s_list.key, ranks * k, s_list.best, k);
+  }
+  Sums all = s_rank[0];
+  for (int i = 1; i < ranks; ++i) all = joined(all, s_rank[i], c);
+  int broken = !(all.s > 0.f);  // nothing above -inf
+  int infinite = 0;             // +inf shares the row
+  if (all.s != all.s) {
+    int nan = 0;
+    for (int i = tid; i < p.vocab; i += kThreads) {
+      const float x = (float)row[i];
+      nan |= x != x;
+      infinite += x == INFINITY;
+    }
+    broken = __syncthreads_or(nan);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) infinite += __shfl_xor_sync(0xffffffffu, infinite, o);
+    if (lane == 0) s_sums[warp].s = (float)infinite;
+    __syncthreads();
+    infinite = 0;
+    for (int w = 0; w < kWarps; ++w) infinite += (int)s_sums[w].s;
+  }
+  __syncthreads();
+  if (infinite) all = Sums{INFINITY, (float)infinite, 0.f};
+  const int first = kTop ? (int)~(uint32_t)s_list.best[0] : 0;
+  const float log_s = greedy ? 0.f : log2f(all.s) * kLn2;
+  const auto logprob = [&](float x, int i) {
+    if (broken) return NAN;
+    if (greedy) return i == first ? 0.f : -INFINITY;
+    return (x == all.m ? 0.f : (x - all.m) * inv) - log_s;
+  };
+  if (tid == 0 && p.entropy) p.entropy[r] = broken ? NAN : greedy ? 0.f : fmaf(all.h / all.s, kLn2, log_s);
   for (int g = tid; g < p.n_given; g += kThreads) {
     const int i = p.given[(long long)r * p.n_given + g];
-    const bool in = i >= 0 && i < p.vocab;
-    p.given_logprobs[(long long)r * p.n_given + g] = broken || !in ? NAN : -below(value(row, i), i) - ln;
+    p.given_logprobs[(long long)r * p.n_given + g] = i >= 0 && i < p.vocab ? logprob((float)row[i], i) : NAN;
   }
-  u64 last = ~0ull;
-  for (int k = 0; k < p.top; ++k) {
-    u64 most = 0;
-    for (int i = tid; !broken && i < p.vocab; i += kThreads) {
-      const float x = value(row, i);
-      const u64 key = ((u64)key_of(x) << 32) | (uint32_t)~i;
-      if (x > -INFINITY && key < last && key > most) most = key;
+  if (kTop)
+    for (int e = tid; e < p.top; e += kThreads) {
+      const u64 key = s_list.best[e];
+      const long long to = (long long)r * p.top + e;
+      p.top_tokens[to] = broken || !key ? -1 : (int)~(uint32_t)key;
+      p.top_logprobs[to] = broken ? NAN : key ? logprob(of_key((uint32_t)(key >> 32)), (int)~(uint32_t)key) : -INFINITY;
     }
-    most = block_max(most, s_max, id);
-    last = most;
-    if (tid == 0) {
-      const int i = (int)~(uint32_t)most;
-      const long long to = (long long)r * p.top + k;
-      p.top_tokens[to] = most ? i : -1;
-      p.top_logprobs[to] = broken ? NAN : most ? -below(value(row, i), i) - ln : -INFINITY;
-    }
-  }
+}
+
+template <class T, int kThreads>
+cudaError_t run(const ScoreParams& p, bool top, int ranks, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.rows * ranks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = ranks > 1 ? 1 : 0;
+  return top ? cudaLaunchKernelEx(&cfg, scores_kernel<T, kThreads, true>, p)
+             : cudaLaunchKernelEx(&cfg, scores_kernel<T, kThreads, false>, p);
+}
+
+template <class T>
+cudaError_t pick(const ScoreParams& p, cudaStream_t s) {
+  // a row whose temperature is not above 0 needs its largest logit's place
+  const bool top = p.top > 0 || p.temperature || !(p.temperature_all > 0.f);
+  const long long bytes = (long long)p.vocab * sizeof(T);
+  if (bytes <= 8192) return run<T, 128>(p, top, 1, s);
+  int ranks = 1;
+  while (ranks < kMaxCluster && (long long)p.rows * ranks * 2 <= 2 * p.num_sms && bytes / ranks > 16384) ranks *= 2;
+  return run<T, 256>(p, top, ranks, s);
 }
 
 }  // namespace
 
 cudaError_t launch_token_logprobs(const ScoreParams& p, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.rows);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
-  if (p.dtype == kFp32) return cudaLaunchKernelEx(&cfg, scores_kernel<float>, p);
-  return p.dtype == kFp16 ? cudaLaunchKernelEx(&cfg, scores_kernel<__half>, p)
-                          : cudaLaunchKernelEx(&cfg, scores_kernel<__nv_bfloat16>, p);
+  if (p.dtype == kFp32) return pick<float>(p, s);
+  return p.dtype == kFp16 ? pick<__half>(p, s) : pick<__nv_bfloat16>(p, s);
 }
 
 }  // namespace ta
