@@ -133,12 +133,13 @@ __device__ __forceinline__ void select_largest(const u64* from, int n, u64* to, 
 }
 
 template <class T, int kThreads, bool kTop>
-__global__ void __launch_bounds__(kThreads) scores_kernel(const ScoreParams p) {
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) scores_kernel(const ScoreParams p) {
   constexpr int kVec = Type<T>::kVec, kVectors = Type<T>::kVectors, kGroup = kVectors * kVec;
   constexpr int kWarps = kThreads / 32;
   using Keys = List<kThreads, kGroup>;
   __shared__ Keys s_list;
   __shared__ Sums s_sums[kWarps], s_rank[kMaxCluster];
+  __shared__ uint32_t s_mth[kWarps];
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -181,6 +182,14 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const ScoreParams p) {
       }
     }
   };
+
+  // a given token's logit, asked for now
+  const auto given_at = [&](int g) {
+    const int i = p.given[(long long)r * p.n_given + g];
+    return i >= 0 && i < p.vocab ? i : -1;
+  };
+  const int given_i = rank == 0 && tid < p.n_given ? given_at(tid) : -1;
+  const float given_x = given_i >= 0 ? (float)row[given_i] : 0.f;
 
   if (kTop) {
     if (tid == 0) s_list.n = 0, s_list.threshold = 0, s_list.before = INT32_MAX;
@@ -228,21 +237,45 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const ScoreParams p) {
       sum.h -= a + b;
     }
     if (kTop && k > 0) {
-      const int tighten = 4 * k + 64;  // long enough to be worth a pass
       const auto index = [&](int e) { return (at + (e / kVec) * kThreads + tid) * kVec - shift + e % kVec; };
       u64 low = s_list.threshold;
+      int room = 2 * k + 32;  // a longer list is worth a pass
+      if (!low) {  // none yet: of each warp's lanes the m-th largest, of these the least, has k logits at or above it
+        uint32_t left = key_of(most), mth = 0;
+        for (int m = (k + kWarps - 1) / kWarps; m > 0; --m) {
+          mth = __reduce_max_sync(0xffffffffu, left);
+          if (lane == __ffs(__ballot_sync(0xffffffffu, left == mth)) - 1) left = 0;
+        }
+        if (lane == 0) s_mth[warp] = mth;
+        __syncthreads();
+        mth = s_mth[0];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) mth = min(mth, s_mth[w]);
+        if (of_key(mth) > -INFINITY) {
+          low = ((u64)mth << 32) - 1;
+          if (tid == 0) s_list.threshold = low;  // (read again behind a barrier)
+          room = k;
+        }
+      }
       const auto push = [&]() {  // true where the list has become long
-        if (!(most > -INFINITY) || (low && most < of_key((uint32_t)(low >> 32)))) return false;
-        int hits = 0;
+        const float least = low ? of_key((uint32_t)((low + 1) >> 32)) : kLowest;
+        bool longer = false;
+        if (most >= least) {
+          uint32_t hits = 0;
 #pragma unroll
-        for (int e = 0; e < kGroup; ++e) hits += x[e] > -INFINITY && key_at(x[e], index(e)) > low;
-        if (hits == 0) return false;
-        int to = atomicAdd(&s_list.n, hits);
-        if (to + hits > Keys::kRoom) return true;
+          for (int e = 0; e < kGroup; ++e) hits |= (uint32_t)(x[e] >= least) << e;
 #pragma unroll
-        for (int e = 0; e < kGroup; ++e)
-          if (x[e] > -INFINITY && key_at(x[e], index(e)) > low) s_list.key[to++] = key_at(x[e], index(e));
-        return to > tighten;
+          for (int e = 0; e < kGroup; ++e)
+            if (hits >> e & 1) {
+              const u64 key = key_at(x[e], index(e));
+              if (key > low) {
+                const int to = atomicAdd(&s_list.n, 1);
+                if (to < Keys::kRoom) s_list.key[to] = key;
+                longer |= to >= room;
+              }
+            }
+        }
+        return longer;
       };
       const int before = s_list.n;  // with what others have pushed in this round: the least of all is before it
       if (__syncthreads_or(push())) {
@@ -339,8 +372,8 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const ScoreParams p) {
   };
   if (tid == 0 && p.entropy) p.entropy[r] = broken ? NAN : greedy ? 0.f : fmaf(all.h / all.s, kLn2, log_s);
   for (int g = tid; g < p.n_given; g += kThreads) {
-    const int i = p.given[(long long)r * p.n_given + g];
-    p.given_logprobs[(long long)r * p.n_given + g] = i >= 0 && i < p.vocab ? logprob((float)row[i], i) : NAN;
+    const int i = g == tid ? given_i : given_at(g);
+    p.given_logprobs[(long long)r * p.n_given + g] = i < 0 ? NAN : logprob(g == tid ? given_x : (float)row[i], i);
   }
   if (kTop)
     for (int e = tid; e < p.top; e += kThreads) {
