@@ -1,35 +1,39 @@
 // Attention of several new tokens of each request over its pages, prompts and
 // trees of drafts alike, on tcgen05 (sm_103a).
 //
-// Query rows are (token, q head of a kv head's group); a block of a request's
-// new tokens gives up to 256 rows that share a kv head's keys.  A CTA (one per SM)
-// streams K and V past them, 128 keys a step, with the products' accumulators in
-// TMEM:
+// Query rows are (token, q head of a kv head's group); a block of a request's new
+// tokens gives two tiles of up to 128 rows that share a kv head's keys.  A CTA (one
+// per SM) streams K and V past them, 128 keys a step, with the products'
+// accumulators in TMEM:
 //   S = Q K^T (128 x 128), online softmax on one row per thread, P as 16-bit
 //   pairs over S, O += P V.
-// Two tiles alternate: while one's softmax runs, the other's products do.  With
-// more than 128 rows the tiles are the block's two halves and share each step's
-// keys (a prompt: bound by the products and the softmax between them).  With fewer
-// they are the same rows and take the steps in turn (drafts: bound by reading K
-// and V once); their sums are joined where the segment ends.
+// A tile's step is a task.  Tasks stand in one row, segment behind segment, and go
+// to the two halves of TMEM and of the softmax warps in turn: while one task's
+// softmax runs, the products of its neighbours do, also across segments.  With two
+// tiles in the block (a prompt: bound by the products and the softmax between
+// them) each step is two tasks.  With one (drafts: bound by reading K and V once)
+// a step is one task, the halves take the steps in turn, and their sums are joined
+// where the segment ends.
 //
 // Steps of all (request, kv head, block) segments stand in one line, and a CTA
-// takes an equal, contiguous run of it, whatever the lengths are.  A segment
-// within one run is final; pieces of one that lies in several go out as {m, l} and
-// the unnormalised O in 32 bits and are joined by the merge,
+// takes a contiguous run of it, whatever the lengths are.  Runs are equal in cost:
+// a segment's steps and kSegmentCost more.  A segment within one run is final;
+// pieces of one that lies in several go out as {m, l} and the unnormalised O in 32
+// bits and are joined by the merge,
 //   m = max m_i, out = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i.
 // A CTA has at most one piece that began before its run and one that goes on
 // behind it.
 //
 // Which keys a row sees is a mask of 128 bits a step, made only in steps that hold
 // a key that some row does not see: from the row's end for a prompt, and for a
-// tree from the nodes above the row's, which its thread collects along parents.
+// tree from the nodes above the row's, collected along parents once a block.
 //
-// Roles: warps 0-3 and 4-7 are the softmax of tile 0 and 1 (thread = row = TMEM
+// Roles: warps 0-3 and 4-7 are the softmax of the two halves (thread = row = TMEM
 // lane), warp 8 streams K and V by TMA (and zeroes V's rows past a request's end),
-// warp 9 issues the products, warps 10 and 11 fill rows that see nothing.
-// Products run in the order of issue, so S of a tile's next step may be issued
-// right behind the P V that still reads P from the same columns.
+// warps 9 and 11 issue the products of a half each, warp 10 (one thread) lists the
+// run's segments for the others and brings their queries.  A half's products run
+// in the order of issue, so S of its next task may be issued right behind the P V
+// that still reads P from the same columns.
 //
 // Every wait has a limit.  One that runs out sets the status word's timeout bit
 // and the CTA's abort flag; every role then stops issuing, waits (with a limit)
@@ -50,22 +54,26 @@ namespace ta {
 namespace {
 
 using tiles::drain_wait;
-using tiles::load_q;
 using tiles::pack2;
 using tiles::rescale_o;
 using tiles::wait;
+using tiles::wait_one;
 
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kThreads = 384;
-constexpr int kSoftmaxRegs = 224, kIssueRegs = 56;
+constexpr int kSoftmaxRegs = 216, kIssueRegs = 72;
 static_assert(256 * kSoftmaxRegs + 128 * kIssueRegs <= kThreads * 168, "register split too large");
 constexpr float kRescaleLog2 = 8.f;  // O is rescaled when a row's maximum grows by more than 2^8
 constexpr uint32_t kTmemCols = 512;  // S of both tiles (128 columns each), O of both (128 each)
-constexpr int kBlockRows = 256;      // query rows of a segment, at most
+constexpr int kTile = 128;           // query rows of a tile, at most
+constexpr long long kIdleLimitNs = 20000000000ll;  // without a segment to list or queries to bring
+constexpr int kSegmentCost = 2;      // what a segment costs beside its steps, in steps
 constexpr int kStepPages = kTileTokens / kPage;
 
 struct Cut {  // a segment that lies in several runs, told by the run where it ends
-  int pieces, first, tok, rows, head, pad[3];
+  int pieces, first, tok, tokens, head;
+  int broken;  // (the first one's) no token has a request
+  int pad[2];
 };
 
 struct ChunkArgs {
@@ -73,7 +81,9 @@ struct ChunkArgs {
   Cut* cuts;         // [grid]
   float2* piece_ml;  // [2 * grid][piece_rows]: {m, l}
   float* piece_o;    // [2 * grid][piece_rows][d]
-  int piece_rows, block_tokens, grid;
+  int piece_rows, grid;
+  int tile_tokens, block_tokens;  // of a tile (its rows are whole tokens), of two
+  int block_shift;                // log2(block_tokens), or -1
 };
 
 // A request's lengths, checked: its tokens lie in the batch, its pages in the
@@ -128,50 +138,68 @@ __device__ __forceinline__ int blocks_of(const ChunkArgs& a, const Chunk& r) {
 __device__ __forceinline__ int end_of(const ChunkArgs& a, const Chunk& r, int k) {
   return max(r.len - r.n + min((k + 1) * a.block_tokens, r.n), 0);
 }
-__device__ __forceinline__ int steps_of_block(const ChunkArgs& a, const Chunk& r, int k) {
-  return (end_of(a, r, k) + kTileTokens - 1) / kTileTokens;
+// sum over i < n of floor((i + c) / 2^s)
+__device__ __forceinline__ long long shifted_sum(long long n, long long c, int s) {
+  const auto below = [&](long long x) {  // over i < x of floor(i / 2^s)
+    const long long q = x >> s, r = x & ((1ll << s) - 1);
+    return (q * (q - 1) / 2 << s) + q * r;
+  };
+  return below(c + n) - below(c);
 }
-// Steps of the first k blocks, one kv head.
-__device__ __forceinline__ long long steps_before(const ChunkArgs& a, const Chunk& r, int k) {
+// Blocks of a request that see nothing (all before the first token of the cache).
+__device__ __forceinline__ int blind_blocks(const ChunkArgs& a, const Chunk& r) {
+  return r.len < r.n ? (r.n - r.len) / a.block_tokens : 0;
+}
+// What the first k blocks cost, one kv head: their steps, and kSegmentCost for each
+// that has some.
+__device__ __forceinline__ long long cost_before(const ChunkArgs& a, const Chunk& r, int k) {
   const int blocks = blocks_of(a, r), base = r.len - r.n, t = a.block_tokens;
-  long long sum = 0;
-  if (k == blocks && k > 0) sum = (r.len + kTileTokens - 1) / kTileTokens, --k;
-  const int k0 = base < 0 ? min(-base / t, k) : 0;  // blocks that see nothing
-  return sum + floor_sum(k - k0, kTileTokens, t, base + (long long)(k0 + 1) * t + kTileTokens - 1);
+  const int k0 = min(blind_blocks(a, r), k);
+  long long sum = (long long)kSegmentCost * (k - k0);
+  if (k == blocks && k > 0) sum += (r.len + kTileTokens - 1) / kTileTokens, --k;
+  const long long n = k - k0, first = base + (long long)(k0 + 1) * t + kTileTokens - 1;
+  if (n <= 0) return sum;
+  // of floor((first + i t) / 128)
+  if (a.block_shift >= 7) return sum + (n * (n - 1) / 2 << (a.block_shift - 7)) + n * (first >> 7);
+  if (a.block_shift >= 0) return sum + shifted_sum(n, first >> a.block_shift, 7 - a.block_shift);
+  return sum + floor_sum(n, kTileTokens, t, first);
 }
-__device__ __forceinline__ long long steps_of_request(const ChunkArgs& a, const Chunk& r) {
-  if (r.n <= a.block_tokens) return r.n ? (long long)a.p.hkv * ((r.len + kTileTokens - 1) / kTileTokens) : 0;
-  return a.p.hkv * steps_before(a, r, blocks_of(a, r));
+__device__ __forceinline__ long long cost_of_request(const ChunkArgs& a, const Chunk& r) {
+  if (r.n == 0 || r.len == 0) return 0;
+  if (r.n <= a.block_tokens) return (long long)a.p.hkv * ((r.len + kTileTokens - 1) / kTileTokens + kSegmentCost);
+  return a.p.hkv * cost_before(a, r, blocks_of(a, r));
 }
 
-struct Segment {
+struct alignas(16) Segment {
   int b, head;
-  int tok, first, rows;  // the block's first token, its number among the request's new ones, query rows
-  int len, base, end;    // tokens of the request, those before its new ones, keys of the block
-  int np, j0, j1;        // steps in all, this run's
-  int buf;               // (one tile's rows) which query buffer
-  __device__ __forceinline__ bool pair() const { return rows > 128; }
+  int tok, first, tokens;  // the block's first token, its number among the request's new ones, how many
+  int len, base, end;      // tokens of the request, those before its new ones, keys of the block
+  int np, j0, j1;          // steps in all, this run's (none: there are no more segments)
+  int buf;                 // which query buffer; 2: two tiles, a buffer each
+  __device__ __forceinline__ bool pair() const { return buf == 2; }
   __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == np; }
+  __device__ __forceinline__ int tasks() const { return (j1 - j0) << (int)pair(); }
 };
 
 // The CTA's run, segment by segment.
 struct Walk {
-  int b, head, block, j, left;  // the next step's place, steps left
+  int b, head, block, j, lead, left;  // the next step's place, cost units before it, cost units left
   Chunk r;
-  Raw ahead;                    // the next request's
-  int buf;                      // of the last segment: -1 after two tiles' rows
+  Raw ahead;                          // the next request's
+  int buf;                            // of the last segment
 
   __device__ __forceinline__ void look_ahead(const ChunkParams& p) {
     if (b + 1 < p.n_req) ahead = raw_of(p, b + 1);
   }
   __device__ __forceinline__ bool next(const ChunkArgs& a, Segment& s) {
-    if (left <= 0) return false;
-    const int t = a.block_tokens, count = min(r.n - block * t, t);
+    if (left <= lead) return false;
+    left -= lead;
+    const int t = a.block_tokens;
     s.b = b;
     s.head = head;
     s.first = block * t;
     s.tok = r.tok0 + s.first;
-    s.rows = count * a.p.gqa;
+    s.tokens = min(r.n - s.first, t);
     s.len = r.len;
     s.base = r.len - r.n;
     s.end = end_of(a, r, block);
@@ -179,10 +207,12 @@ struct Walk {
     s.j0 = j;
     s.j1 = min(s.np, j + left);
     left -= s.j1 - s.j0;
-    buf = s.pair() ? -1 : buf < 0 ? 0 : buf ^ 1;
+    // one tile's queries: not into the buffer of the ones before
+    buf = s.tokens > a.tile_tokens ? 2 : buf == 0;
     s.buf = buf;
     j = 0;
-    if (left > 0 && (++block) * t >= r.n) {
+    lead = kSegmentCost;
+    if (left > lead && (++block) * t >= r.n) {
       if (++head == a.p.hkv) {
         head = 0;
         int bad = 0;
@@ -192,7 +222,7 @@ struct Walk {
           look_ahead(a.p);
         } while ((r.n == 0 || r.len == 0) && b + 1 < a.p.n_req);
       }
-      block = r.len < r.n ? (r.n - r.len) / t : 0;  // blocks before it see nothing
+      block = blind_blocks(a, r);
     }
     return true;
   }
@@ -208,8 +238,12 @@ struct Cfg {
   static constexpr int kOffStage = 2 * kQBytes;
   static constexpr int kOffMl = kOffStage + kStages * kStageBytes;  // {m, l} of both tiles' rows
   static constexpr int kOffBar = kOffMl + 2 * 128 * 8;
-  static constexpr int kBars = 3 * kStages + 12;
-  static constexpr int kOffWalk = kOffBar + kBars * 8 + 8;  // behind the TMEM address and the abort flag
+  static constexpr int kListed = 8;  // segments that the roles may be apart
+  static constexpr int kBars = 3 * kStages + 15 + 2 * kListed;
+  // the TMEM address, the abort flag, copies issued: ring entries, of each query buffer
+  static constexpr int kOffWords = kOffBar + kBars * 8;
+  static constexpr int kOffList = (kOffWords + 20 + 15) / 16 * 16;
+  static constexpr int kOffWalk = kOffList + kListed * sizeof(Segment);
   static constexpr int kSmem = kOffWalk + sizeof(Walk);
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
@@ -231,16 +265,63 @@ struct Cta {
   __device__ uint32_t p_full(int t) const { return bar(3 * C::kStages + 4 + t); }
   __device__ uint32_t o_full(int t) const { return bar(3 * C::kStages + 6 + t); }
   __device__ uint32_t o_empty(int t) const { return bar(3 * C::kStages + 8 + t); }
-  __device__ uint32_t joined() const { return bar(3 * C::kStages + 10); }
-  __device__ uint32_t drain() const { return bar(3 * C::kStages + 11); }
+  __device__ uint32_t q_empty(int t) const { return bar(3 * C::kStages + 10 + t); }
+  __device__ uint32_t joined() const { return bar(3 * C::kStages + 12); }
+  __device__ uint32_t drain(int t) const { return bar(3 * C::kStages + 13 + t); }
+  __device__ uint32_t listed(uint32_t i) const { return bar(3 * C::kStages + 15 + i % C::kListed); }
+  __device__ uint32_t unlisted(uint32_t i) const { return bar(3 * C::kStages + 15 + C::kListed + i % C::kListed); }
+  __device__ Segment* segment(uint32_t i) const {
+    return reinterpret_cast<Segment*>(ptr + C::kOffList) + i % C::kListed;
+  }
+  static __device__ uint32_t round(uint32_t i) { return i / C::kListed & 1; }
+  __device__ uint32_t kv_issued() const { return base + C::kOffWords + 8; }
+  __device__ uint32_t q_issued(int buf) const { return base + C::kOffWords + 12 + 4 * buf; }
   __device__ uint32_t stage(int s) const { return base + C::kOffStage + s * C::kStageBytes; }
   __device__ float2* ml() const { return reinterpret_cast<float2*>(ptr + C::kOffMl); }
 };
 
+// Copies issued, counted.  A reader that does not use every entry of a ring cannot
+// tell by parity alone whether a stage's barrier is in the entry's phase or still in
+// the one before: the entry must have been issued, and then it is.
+__device__ __forceinline__ void publish_issued(uint32_t word, uint32_t n) {
+  asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(word), "r"(n) : "memory");
+}
+__device__ __forceinline__ uint32_t issued_of(uint32_t word) {
+  uint32_t n;
+  asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(n) : "r"(word) : "memory");
+  return n;
+}
+template <class C>
+__device__ __noinline__ bool wait_issued_slow(const C& c, uint32_t word, uint32_t least) {
+  const uint64_t t0 = ptx::globaltimer();
+  for (uint32_t n = 1;; ++n) {
+    if ((int32_t)(issued_of(word) - least) >= 0) return true;
+    if ((n & 15) == 0) {
+      if (*c.abort_flag) return false;
+      if ((long long)(ptx::globaltimer() - t0) > tiles::kWaitLimitNs) {
+        *c.abort_flag = 1;
+        if (c.status) atomicOr(c.status, kBatchTimeout);
+        return false;
+      }
+    }
+  }
+}
+// True once at least so many have been issued; the same in all lanes of the warp.
+template <class C>
+__device__ __forceinline__ bool wait_issued(const C& c, uint32_t word, uint32_t least) {
+  bool ok = (int32_t)(issued_of(word) - least) >= 0;
+  if (!ok) ok = wait_issued_slow(c, word, least);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// Those that let go of a listed segment: the copies' warp, the products' two, the
+// queries' thread and eight warps of softmax.
+constexpr uint32_t kReaders = 12;
+
 // ------------------------------------------------------------- copies
 template <int D>
 __device__ void stream_kv(const CUtensorMap* tmk, const CUtensorMap* tmv, const ChunkArgs& a,
-                          const Cta<D>& c, Walk walk) {
+                          const Cta<D>& c) {
   using C = Cfg<D>;
   const ChunkParams& p = a.p;
   const int lane = threadIdx.x & 31;
@@ -252,13 +333,23 @@ __device__ void stream_kv(const CUtensorMap* tmk, const CUtensorMap* tmv, const 
     if (p.status) atomicOr(p.status, kBatchBadSlot);
     return p.num_pages;  // outside the tensor map: read as zeros
   };
-  Segment s, s_next;
-  uint32_t g = 0;
+  Segment s, s_next{};
+  uint32_t g = 0, seg = 0;
   uint32_t zeroed = 0;  // phase of each stage's land barrier
-  bool ok = true, more = walk.next(a, s);
-  int next = more ? page_of(s, s.j0) : 0;
-  while (ok && more) {
-    more = walk.next(a, s_next);
+  const auto read = [&](Segment& to) {  // the next listed segment; false: given up
+    if (!wait<1>(c, c.listed(seg), c.round(seg))) return false;
+    to = *c.segment(seg);
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(c.unlisted(seg));
+    ++seg;
+    return true;
+  };
+  bool ok = read(s);
+  int next = ok && s.j0 < s.j1 ? page_of(s, s.j0) : 0;
+  while (ok && s.j0 < s.j1) {
+    ok = read(s_next);
+    if (!ok) break;
+    const bool more = s_next.j0 < s_next.j1;
     const int n_pages = (s.end + kPage - 1) / kPage;
     for (int j = s.j0; ok && j < s.j1; ++j) {
       const int ids = next;
@@ -279,6 +370,7 @@ __device__ void stream_kv(const CUtensorMap* tmk, const CUtensorMap* tmv, const 
         const uint32_t bar = zero ? c.land(st) : c.full(st);
         const uint32_t dst = c.stage(st);
         const bool leader = ptx::elect_one();
+        if (leader) publish_issued(c.kv_issued(), g + 1);
         if (leader) ptx::mbar_arrive_expect_tx(bar, nb * C::kHead);
         for (int b = 0; b < nb; ++b) {
           const int page = __shfl_sync(0xffffffffu, ids, b);
@@ -322,133 +414,232 @@ __device__ void stream_kv(const CUtensorMap* tmk, const CUtensorMap* tmv, const 
       drain_wait(c.full(k % C::kStages), (k / C::kStages) & 1);
 }
 
+// One thread: lists the run's segments as there is room, and brings each one's
+// queries as soon as its buffer is free.
+template <int D>
+__device__ void list_segments(const CUtensorMap* tmq, const ChunkArgs& a, const Cta<D>& c, Walk walk) {
+  using C = Cfg<D>;
+  uint32_t listed = 0, brought = 0;  // segments
+  uint32_t loads[2] = {0, 0};        // of each query buffer
+  int tile = 0;                      // of two, brought already
+  bool all = false;
+  uint64_t since = ptx::globaltimer();
+  for (uint32_t polls = 0; !all || brought < listed; ++polls) {
+    bool idle = true;
+    if (!all && (listed < C::kListed || ptx::mbar_test_wait(c.unlisted(listed), c.round(listed) ^ 1))) {
+      Segment s{};
+      if (!walk.next(a, s)) {
+        all = true;
+        s.j0 = s.j1 = 0;
+      }
+      *c.segment(listed) = s;
+      ptx::mbar_arrive(c.listed(listed));
+      if (!all) ++listed;
+      idle = false;
+    }
+    if (brought < listed) {
+      const Segment& s = *c.segment(brought);
+      const int buf = s.pair() ? tile : s.buf;
+      const uint32_t n = buf ? loads[1] : loads[0];
+      if (n == 0 || ptx::mbar_test_wait(c.q_empty(buf), (n - 1) & 1)) {
+        const uint32_t bar = c.q_full(buf);
+        publish_issued(c.q_issued(buf), n + 1);
+        ptx::mbar_arrive_expect_tx(bar, a.tile_tokens * a.p.gqa * D * 2);
+        const int tok = s.tok + (s.pair() ? tile * a.tile_tokens : 0);
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h)
+          ptx::tma_load_3d(c.base + buf * C::kQBytes + h * (kTile * 128), tmq, 64 * h, s.head * a.p.gqa, tok, bar);
+        buf ? ++loads[1] : ++loads[0];
+        if (s.pair() && tile == 0) {
+          tile = 1;
+        } else {
+          tile = 0;
+          ptx::mbar_arrive(c.unlisted(brought));
+          ++brought;
+        }
+        idle = false;
+      }
+    }
+    if (!idle) {
+      since = ptx::globaltimer();
+      continue;
+    }
+    __nanosleep(32);
+    if ((polls & 15) == 0) {
+      if (*c.abort_flag) break;
+      // (a segment may take as long as its steps, each of whose waits is limited)
+      if ((long long)(ptx::globaltimer() - since) > kIdleLimitNs) {
+        *c.abort_flag = 1;
+        if (c.status) atomicOr(c.status, kBatchTimeout);
+        break;
+      }
+    }
+  }
+  if (*c.abort_flag)  // the copies in flight land before the CTA may end
+#pragma unroll
+    for (int buf = 0; buf < 2; ++buf)
+      if (loads[buf] > 0) drain_wait(c.q_full(buf), (loads[buf] - 1) & 1);
+}
+
 // ------------------------------------------------------------- products
+// A warp for each half, so that one's waits and the other's products overlap.  S of
+// a half's next task is issued right behind P V of the one before, in one go where
+// its keys are there already.
 template <int D, bool kHalf>
-__device__ void issue_products(const ChunkArgs& a, const Cta<D>& c, Walk walk, uint32_t tmem) {
+__device__ void issue_products(const Cta<D>& c, uint32_t tmem, int t) {
   using C = Cfg<D>;
   constexpr uint32_t kType = kHalf ? 0u : (1u << 7) | (1u << 10);
   constexpr uint32_t kDescQK =
       (ptx::idesc_bf16(128, kTileTokens, 0) & ~((1u << 7) | (1u << 10))) | kType;
   constexpr uint32_t kDescPV = (ptx::idesc_bf16(128, D, 1) & ~((1u << 7) | (1u << 10))) | kType;
-  Segment s;
-  uint32_t g = 0;              // steps before this segment: K is ring entry 2 g, V 2 g + 1
-  uint32_t done[2] = {0, 0};   // steps of each tile before this segment
-  uint32_t loads[2] = {0, 0};  // of each query buffer
-  uint32_t segs = 0;
-  bool ok = true, issued = false;
-  while (ok && walk.next(a, s)) {
-    const int n = s.j1 - s.j0;
-    const bool pair = s.pair();
-    const int n_pages = (s.end + kPage - 1) / kPage;
-    auto qk = [&](int t, int j, bool last_use) {  // S of tile t, step j
-      const uint32_t k = 2 * (g + j);
-      const uint64_t dk = ptx::sdesc_sw128(c.stage(k % C::kStages), 16, 1024);
-      const uint64_t dq = ptx::sdesc_sw128(c.base + (pair ? t : s.buf) * C::kQBytes, 16, 1024);
-      if (ptx::elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
-          ptx::mma_bf16(tmem + t * 128, dq + (off >> 4), dk + (off >> 4), kDescQK, kk > 0);
-        }
-        ptx::mma_commit(c.s_full(t));
-        if (last_use) ptx::mma_commit(c.empty(k % C::kStages));
-      }
-      issued = true;
-    };
-    auto pv = [&](int t, int j, bool first, bool last_use) {  // O of tile t, step j
-      const uint32_t v = 2 * (g + j) + 1;
-      const int pages = min(kStepPages, n_pages - (s.j0 + j) * kStepPages);
-      if (ptx::elect_one()) {
-        const uint64_t dv = ptx::sdesc_sw128(c.stage(v % C::kStages), 2048, 1024);
-        for (int b = 0; b < pages; ++b)  // 16 tokens: 8 columns of P
-          ptx::mma_bf16_ts(tmem + 256 + t * 128, tmem + t * 128 + b * 8, dv + b * (C::kHead >> 4),
-                           kDescPV, !first || b > 0);
-        if (last_use) ptx::mma_commit(c.empty(v % C::kStages));
-        if (j == n - 1) {
-          if (pair) {
-            ptx::mma_commit(c.o_full(t));
-          } else {
-            ptx::mma_commit(c.o_full(0));
-            ptx::mma_commit(c.o_full(1));
-          }
-        }
-      }
-      issued = true;
-    };
-    auto wait_k = [&](int j) {
-      const uint32_t k = 2 * (g + j);
-      return wait<1>(c, c.full(k % C::kStages), (k / C::kStages) & 1);
-    };
-    auto wait_v = [&](int j) {
-      const uint32_t v = 2 * (g + j) + 1;
-      return wait<1>(c, c.full(v % C::kStages), (v / C::kStages) & 1);
-    };
-    auto wait_q = [&](int buf) {
-      const bool there = wait<1>(c, c.q_full(buf), loads[buf]++ & 1);
-      ptx::fence_proxy_async_smem();  // the queries came by cp.async
-      return there;
-    };
-    // the first P V of a segment overwrites O: the last segment's must have been read
-    auto wait_o = [&](int t) { return segs == 0 || wait<1>(c, c.o_empty(t), (segs - 1) & 1); };
-    if (pair) {
-      ok = wait_k(0);
-      for (int t = 0; ok && t < 2; ++t) {
-        ok = wait_q(t);
-        if (!ok) break;
-        ptx::tc_fence_after();
-        qk(t, 0, t == 1);
-      }
-      for (int j = 0; ok && j < n; ++j) {
-        for (int t = 0; ok && t < 2; ++t) {
-          ok = wait<1>(c, c.p_full(t), (done[t] + j) & 1);
-          if (ok && t == 0) ok = wait_v(j);
-          if (ok && j == 0) ok = wait_o(t);
-          if (!ok) break;
-          ptx::tc_fence_after();
-          pv(t, j, j == 0, t == 1);
-          if (j + 1 < n) {
-            if (t == 0) ok = wait_k(j + 1);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            qk(t, j + 1, t == 1);
-          }
-        }
-      }
-      done[0] += n;
-      done[1] += n;
-    } else {
-      ok = wait_q(s.buf);
-      for (int j = 0; ok && j < min(n, 2); ++j) {
-        ok = wait_k(j);
-        if (!ok) break;
-        ptx::tc_fence_after();
-        qk(j, j, true);
-      }
-      for (int j = 0; ok && j < n; ++j) {
-        const int t = j & 1;
-        ok = wait<1>(c, c.p_full(t), (done[t] + (j >> 1)) & 1);
-        if (ok) ok = wait_v(j);
-        if (ok && j < 2) ok = wait_o(t);
-        if (!ok) break;
-        ptx::tc_fence_after();
-        pv(t, j, j < 2, true);
-        if (j + 2 < n) {
-          ok = wait_k(j + 2);
-          if (!ok) break;
-          ptx::tc_fence_after();
-          qk(t, j + 2, true);
-        }
-      }
-      done[0] += (n + 1) / 2;
-      done[1] += n / 2;
+  const uint64_t desc_q = ptx::sdesc_sw128(c.base, 16, 1024);
+  const uint64_t desc_k = ptx::sdesc_sw128(c.stage(0), 16, 1024);
+  const uint64_t desc_v = ptx::sdesc_sw128(c.stage(0), 2048, 1024);
+  const uint32_t s_tmem = tmem + t * 128, o_tmem = tmem + 256 + t * 128;
+  struct Task {
+    uint32_t step;      // of the run: K is ring entry 2 step, V the next one
+    int pages, buf;     // of 16 keys; the query buffer
+    bool first, last;   // of the half's tasks of the segment
+    bool pair, single;  // the block has two tiles; the segment is this task alone
+  };
+  int idx = 0, n = 0, j0 = 0, n_pages = 0, buf = 0;  // of the segment: this half's next step, steps, ...
+  bool pair = false;
+  uint32_t seg = 0, tasks = 0, before = 0;           // listed segments, all tasks and steps before the next one
+  uint32_t base = 0;                                 // steps before this segment
+  uint32_t q_loads[2] = {0, 0};                      // of each query buffer, with this segment's
+  // This half's next task: 1, 0 where there is none, -1: given up.
+  const auto next_task = [&](Task& k) {
+    while (idx >= n) {
+      if (!wait<1>(c, c.listed(seg), c.round(seg))) return -1;
+      const Segment& s = *c.segment(seg);
+      n = s.j1 - s.j0;
+      if (n == 0) return 0;
+      j0 = s.j0;
+      n_pages = (s.end + kPage - 1) / kPage;
+      pair = s.pair();
+      buf = s.buf;
+      __syncwarp();
+      if (ptx::elect_one()) ptx::mbar_arrive(c.unlisted(seg));
+      __syncwarp();
+      ++seg;
+      base = before;
+      before += n;
+      idx = pair ? 0 : (int)(tasks & 1) ^ t;
+      tasks += n << (int)pair;
+      q_loads[0] += pair || buf == 0;
+      q_loads[1] += pair || buf == 1;
     }
-    g += n;
-    ++segs;
+    k.step = base + idx;
+    k.pages = min(kStepPages, n_pages - (j0 + idx) * kStepPages);
+    k.buf = pair ? t : buf;
+    k.pair = pair;
+    k.single = !pair && n == 1;
+    k.first = idx < (pair ? 1 : 2);
+    idx += pair ? 1 : 2;
+    k.last = idx >= n;
+    return 1;
+  };
+  const auto stage_of = [](uint32_t entry) { return (int)(entry % C::kStages); };
+  const auto phase_of = [](uint32_t entry) { return entry / C::kStages & 1; };
+  // one elected lane
+  const auto scores = [&](const Task& k, uint64_t dq, uint64_t dk) {
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
+      ptx::mma_bf16(s_tmem, dq + (off >> 4), dk + (off >> 4), kDescQK, kk > 0);
+    }
+    ptx::mma_commit(c.s_full(t));
+    // a buffer is free when both halves are done with it
+    ptx::mma_commit(c.empty(stage_of(2 * k.step)));
+    if (!k.pair) ptx::mma_commit(c.empty(stage_of(2 * k.step)));
+    if (k.last) {
+      ptx::mma_commit(c.q_empty(k.buf));
+      if (k.pair || k.single) ptx::mma_commit(c.q_empty(k.buf));
+    }
+  };
+  const auto wait_entry = [&](uint32_t entry) {
+    return wait_issued(c, c.kv_issued(), entry + 1) && wait<1>(c, c.full(stage_of(entry)), phase_of(entry));
+  };
+  const auto wait_for_scores = [&](const Task& k) {
+    if (!wait_entry(2 * k.step)) return false;
+    if (!k.first) return true;
+    const uint32_t loads = k.buf ? q_loads[1] : q_loads[0];
+    return wait_issued(c, c.q_issued(k.buf), loads) && wait<1>(c, c.q_full(k.buf), (loads - 1) & 1);
+  };
+  // whether it would not wait
+  const auto can_score = [&](const Task& k) {
+    bool can = (int32_t)(issued_of(c.kv_issued()) - (2 * k.step + 1)) >= 0 &&
+               ptx::mbar_test_wait(c.full(stage_of(2 * k.step)), phase_of(2 * k.step));
+    if (can && k.first) {
+      const uint32_t loads = k.buf ? q_loads[1] : q_loads[0];
+      can = (int32_t)(issued_of(c.q_issued(k.buf)) - loads) >= 0 && ptx::mbar_test_wait(c.q_full(k.buf), (loads - 1) & 1);
+    }
+    return (bool)__all_sync(0xffffffffu, can);
+  };
+  const auto desc_of_q = [&](const Task& k) { return desc_q + (uint32_t)(k.buf * C::kQBytes >> 4); };
+  const auto desc_of = [&](uint64_t desc, uint32_t entry) { return desc + (uint32_t)(stage_of(entry) * C::kStageBytes >> 4); };
+
+  Task now{}, next{};
+  int have = next_task(now);
+  bool ok = have >= 0, issued = false;
+  if (have > 0) {
+    ok = wait_for_scores(now);
+    if (ok) {
+      ptx::tc_fence_after();
+      if (ptx::elect_one()) scores(now, desc_of_q(now), desc_of(desc_k, 2 * now.step));
+      __syncwarp();
+      issued = true;
+    }
+  }
+  uint32_t done = 0, o_read = 0;
+  while (ok && have > 0) {
+    const int more = next_task(next);
+    if (more < 0) {
+      ok = false;
+      break;
+    }
+    const uint64_t dq = desc_of_q(next), dk = desc_of(desc_k, 2 * next.step), dv = desc_of(desc_v, 2 * now.step + 1);
+    const int v_stage = stage_of(2 * now.step + 1);
+    ok = wait_entry(2 * now.step + 1);
+    // the first P V of a segment overwrites O: the last one's must have been read
+    if (ok && now.first) {
+      if (o_read) ok = wait<1>(c, c.o_empty(t), (o_read - 1) & 1);
+      ++o_read;
+    }
+    if (ok) ok = wait<1>(c, c.p_full(t), done++ & 1);
+    if (!ok) break;
+    const bool together = more && can_score(next);
+    ptx::tc_fence_after();
+    if (ptx::elect_one()) {
+      const uint32_t add = now.first ? 0 : 1;
+      if (now.pages == kStepPages) {  // 16 tokens: 8 columns of P
+#pragma unroll
+        for (int b = 0; b < kStepPages; ++b)
+          ptx::mma_bf16_ts(o_tmem, s_tmem + b * 8, dv + b * (C::kHead >> 4), kDescPV, b > 0 ? 1 : add);
+      } else {
+        for (int b = 0; b < now.pages; ++b)
+          ptx::mma_bf16_ts(o_tmem, s_tmem + b * 8, dv + b * (C::kHead >> 4), kDescPV, b > 0 ? 1 : add);
+      }
+      ptx::mma_commit(c.empty(v_stage));
+      if (!now.pair) ptx::mma_commit(c.empty(v_stage));
+      if (now.last) ptx::mma_commit(c.o_full(t));
+      if (together) scores(next, dq, dk);
+    }
+    __syncwarp();
+    if (more && !together) {
+      ok = wait_for_scores(next);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      if (ptx::elect_one()) scores(next, dq, dk);
+      __syncwarp();
+    }
+    now = next;
+    have = more;
   }
   if (!ok && issued) {
-    if (ptx::elect_one()) ptx::mma_commit(c.drain());
+    if (ptx::elect_one()) ptx::mma_commit(c.drain(t));
     __syncwarp();
-    drain_wait(c.drain(), 0);
+    drain_wait(c.drain(t), 0);
   }
 }
 
@@ -456,16 +647,33 @@ __device__ void issue_products(const ChunkArgs& a, const Cta<D>& c, Walk walk, u
 struct Mask {
   uint32_t w[4];
 };
-// The nodes above new token i, and i itself.
-__device__ __forceinline__ Mask nodes_above(const ChunkParams& p, int tok0, int i) {
-  Mask m{};
-  for (int at = i; at >= 0;) {
+// The nodes above each lane's new token i (none below 0), and i itself: the
+// request's parents, four a lane, are handed round as the lanes climb.
+__device__ __forceinline__ Mask nodes_above(const ChunkParams& p, int tok0, int n, int i) {
+  const int lane = threadIdx.x & 31;
+  int up[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (at >> 5 == k) m.w[k] |= 1u << (at & 31);
-    const int up = p.parents[tok0 + at];
-    if ((up < -1 || up >= at) && p.status) atomicOr(p.status, kBatchBadInput);
-    at = up >= at ? -1 : up;
+  for (int k = 0; k < 4; ++k) {
+    const int node = k * 32 + lane;
+    up[k] = node < n ? p.parents[tok0 + node] : -1;
+    if (up[k] < -1 || up[k] >= node) {
+      if (p.status) atomicOr(p.status, kBatchBadInput);
+      up[k] = -1;
+    }
+  }
+  Mask m{};
+  int at = i;
+  while (__any_sync(0xffffffffu, at >= 0)) {
+    int next = -1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int x = __shfl_sync(0xffffffffu, up[k], at & 31);
+      if (at >> 5 == k) {
+        m.w[k] |= 1u << (at & 31);
+        next = x;
+      }
+    }
+    at = next;
   }
   return m;
 }
@@ -491,51 +699,80 @@ __device__ __forceinline__ Mask moved(const Mask& m, int n) {
   return r;
 }
 
+// A row's 128 bytes (8 words of each of 4 chunks, w[chunk][..]) against those of
+// the other three lanes of its quad: lane q ends with chunk q of rows 0..3.
+__device__ __forceinline__ void turn_quads(uint32_t (&w)[4][8]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int bit = 1; bit <= 2; bit <<= 1) {
+    const bool high = lane & bit;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (x & bit) continue;
+      const int y = x | bit;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? w[x][e] : w[y][e], bit);
+        if (high)
+          w[x][e] = got;
+        else
+          w[y][e] = got;
+      }
+    }
+  }
+}
+
 template <int D, bool kHalf>
-__device__ void softmax_rows(const ChunkArgs& a, const Cta<D>& c, Walk walk, uint32_t tmem, int t) {
+__device__ void softmax_rows(const ChunkArgs& a, const Cta<D>& c, uint32_t tmem, int t) {
   using C = Cfg<D>;
   constexpr float kBase = kHalf ? kFp16Base : 0.f;  // m is that much below the largest score
   const ChunkParams& p = a.p;
-  const int tid = threadIdx.x & 127, warp = tid >> 5;
+  const int tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
   const uint32_t lanes = (uint32_t)(warp * 32) << 16;
   const uint32_t s_tmem = tmem + lanes + t * 128;
   const uint32_t o_tmem0 = tmem + lanes + 256, o_tmem = o_tmem0 + t * 128;
-  // the segment's query rows of this tile, into buffer `buf`
-  auto start = [&](const Segment& s, int buf) {
-    const int row = (s.pair() ? t * 128 : 0) + tid;
-    const bool there = row < s.rows;
-    const int i = there ? row / p.gqa : 0, h = there ? row % p.gqa : 0;
-    load_q<D>(p.q + (s.tok + i) * p.q_stride + (s.head * p.gqa + h) * D, there, c.base + buf * C::kQBytes, tid);
-    ptx::cp_async_mbar_arrive_noinc(c.q_full(buf));
-  };
-  auto start_next = [&](const Segment& s) {
-    if (s.pair())
-      start(s, t);
-    else if (t == 0)
-      start(s, s.buf);
-  };
-  Segment s, s_next;
-  bool more = walk.next(a, s), ok = true;
-  if (more) start_next(s);
-  uint32_t done = 0, segs = 0, joins = 0;
-  while (ok && more) {
-    const bool pair = s.pair();
-    more = walk.next(a, s_next);
-    // one tile's rows behind one tile's: the other buffer is free
-    const bool early = more && !pair && !s_next.pair();
-    if (early) start_next(s_next);
-    const int row = (pair ? t * 128 : 0) + tid;
-    const bool act = row - (tid & 31) < s.rows;  // this warp has rows
-    const int i = s.first + row / p.gqa;         // the row's new token
-    Mask above{};
-    const bool tree = p.parents != nullptr;
-    if (tree && row < s.rows && s.j1 * kTileTokens > s.base) above = nodes_above(p, s.tok - s.first, i);
-    // keys before `clear` are seen by this row
-    const int clear = row < s.rows ? (tree ? s.base : s.base + i + 1) : INT32_MAX;
+  const int in_tile = tid / p.gqa, in_group = tid - in_tile * p.gqa;  // the row's token and head
+  const bool tree = p.parents != nullptr;
+  uint32_t task = 0;  // of the whole run
+  uint32_t done = 0, joins = 0;
+  uint32_t o_phase = 0;  // of each half's O, a bit each
+  Mask above{};
+  int above_b = -1, above_tok = 0;  // the block (request, row's token) that `above` was made for
+  bool ok = true;
+  for (uint32_t seg = 0;; ++seg) {
+    ok = wait<0>(c, c.listed(seg), c.round(seg));
+    const Segment& s = *c.segment(seg);
     const int n = s.j1 - s.j0;
+    if (!ok || n == 0) break;
+    const bool pair = s.pair(), alone = pair || n == 1;  // a half has the rows' O to itself
+    const uint32_t f = task & 1;                         // the half of the segment's first task
+    const uint32_t o_now = o_phase;
+    task += s.tasks();
+    o_phase ^= pair || n > 1 ? 3u : 1u << f;
+    const auto let_go = [&]() {
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(c.unlisted(seg));
+    };
+    if (!pair && n == 1 && t != (int)f) {
+      let_go();
+      continue;
+    }
+    const int i0 = pair ? t * a.tile_tokens : 0;      // the tile's first token in the block
+    const int rows = min(s.tokens - i0, a.tile_tokens) * p.gqa;
+    const bool there = tid < rows, act = tid - lane < rows;  // the row, the warp's rows
+    const int i = s.first + i0 + in_tile;               // the row's new token
+    if (tree && act && s.j1 * kTileTokens > s.base &&
+        (above_b != s.b || __any_sync(0xffffffffu, there && above_tok != i))) {
+      above = nodes_above(p, s.tok - s.first, s.len - s.base, there ? i : -1);
+      above_b = s.b;
+      above_tok = i;
+    }
+    // keys before `clear` are seen by this row
+    const int clear = there ? (tree ? s.base : s.base + i + 1) : INT32_MAX;
+    const int j0 = s.j0;
     float m = -INFINITY, l = 0.f;
     bool first = true;
-    for (int j = pair ? 0 : t; j < n; j += pair ? 1 : 2) {
+    for (int j = pair ? 0 : (int)(f ^ t); j < n; j += pair ? 1 : 2) {
       ok = wait<0>(c, c.s_full(t), done++ & 1);
       if (!ok) break;
       ptx::tc_fence_after();
@@ -544,7 +781,7 @@ __device__ void softmax_rows(const ChunkArgs& a, const Cta<D>& c, Walk walk, uin
 #pragma unroll
         for (int k = 0; k < 4; ++k) ptx::tmem_ld32(s_tmem + k * 32, *reinterpret_cast<float(*)[32]>(v + k * 32));
         ptx::tmem_wait_ld();
-        const int key0 = (s.j0 + j) * kTileTokens;
+        const int key0 = (j0 + j) * kTileTokens;
         if (__any_sync(0xffffffffu, clear < key0 + kTileTokens)) {
           const int in = clear - key0;  // seen keys of the step, a tree's aside
           Mask see = first_bits(in);
@@ -567,7 +804,7 @@ __device__ void softmax_rows(const ChunkArgs& a, const Cta<D>& c, Walk walk, uin
         }
         first = false;
         l *= alpha;
-        // the S that was waited for was issued behind the tile's last P V: O holds it
+        // the S that was waited for was issued behind the half's last P V: O holds it
         if (__any_sync(0xffffffffu, alpha != 1.f)) rescale_o<D>(o_tmem, alpha);
         const float nm = m == -INFINITY ? 0.f : -m;
         const uint64_t sc2 = ptx::f2(p.scale_log2, p.scale_log2), nm2 = ptx::f2(nm, nm);
@@ -595,10 +832,8 @@ __device__ void softmax_rows(const ChunkArgs& a, const Cta<D>& c, Walk walk, uin
       ptx::mbar_arrive(c.p_full(t));
     }
     if (!ok) break;
-    // every S of this tile is done: where it had its own query buffer, that is free
-    if (more && pair) start_next(s_next);
-    float a0 = 1.f, a1 = 0.f;  // factors of this tile's and the other's O
-    if (!pair) {
+    float a0 = 1.f, a1 = 0.f;  // factors of this half's and the other's O
+    if (!alone) {
       c.ml()[t * 128 + tid] = make_float2(m, l);
       ptx::mbar_arrive(c.joined());
       ok = wait<0>(c, c.joined(), joins++ & 1);
@@ -609,77 +844,254 @@ __device__ void softmax_rows(const ChunkArgs& a, const Cta<D>& c, Walk walk, uin
       a1 = o.x == -INFINITY ? 0.f : ptx::ex2(o.x - top);
       l = a0 * l + a1 * o.y;
       m = top;
-      if (n == 1) (t ? a0 : a1) = 0.f;
     }
-    ok = wait<0>(c, c.o_full(t), segs & 1);
+    ok = wait<0>(c, c.o_full(t), o_now >> t & 1);
+    if (ok && !alone) ok = wait<0>(c, c.o_full(t ^ 1), o_now >> (t ^ 1) & 1);
     if (!ok) break;
     ptx::tc_fence_after();
-    if (more && !pair && !early) start_next(s_next);
+    const bool whole = s.whole();
+    const float inv = !whole ? 1.f : l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+    a0 *= inv;
+    a1 *= inv;
+    // Both halves' warps have the same rows' lanes: joined, each takes half the columns.
+    const long long at = (long long)(s.tok + i0 + in_tile) * p.hq + s.head * p.gqa + in_group;
+    const long long slot = (2ll * blockIdx.x + (s.j0 == 0 ? 1 : 0)) * a.piece_rows + (pair ? t * kTile : 0) + tid;
+    const int columns = alone ? D : D / 2, c0 = alone ? 0 : t * (D / 2);
     if (act) {
-      const bool there = row < s.rows;
-      const long long at = (long long)(s.tok + row / p.gqa) * p.hq + s.head * p.gqa + row % p.gqa;
-      const long long slot = (2ll * blockIdx.x + (s.j0 == 0 ? 1 : 0)) * a.piece_rows + row;
-      const bool whole = s.whole();
-      const float inv = !whole ? 1.f : l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-      a0 *= inv;
-      a1 *= inv;
-      // both tiles' warps have the same rows' lanes: with one tile's rows each takes half the columns
-      constexpr int kColumns = D / 32;
-      const int k0 = pair ? 0 : t * (kColumns / 2), k1 = pair ? kColumns : k0 + kColumns / 2;
-      const uint32_t other = o_tmem0 + (t ^ 1) * 128;
-      for (int k = k0; k < k1; ++k) {
-        float o[32];
-        if (pair || n > 1 || t == 0) {
-          ptx::tmem_ld32(o_tmem + k * 32, o);
-          ptx::tmem_wait_ld();
+      float o[D];
+      if (alone) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] *= a0;
-        } else {
+        for (int k = 0; k < D / 32; ++k) ptx::tmem_ld32(o_tmem + k * 32, *reinterpret_cast<float(*)[32]>(o + k * 32));
+      } else {
+        const uint32_t other = o_tmem0 + (t ^ 1) * 128;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0.f;
-        }
-        if (!pair && (n > 1 || t == 1)) {
-          float o2[32];
-          ptx::tmem_ld32(other + k * 32, o2);
-          ptx::tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = fmaf(o2[e], a1, o[e]);
-        }
-        if (there && whole) {
-          uint16_t* dst = p.out + at * D + k * 32;
-#pragma unroll
-          for (int e = 0; e < 32; e += 16)
-            ptx::st_global_v8(dst + e, pack2<kHalf>(o[e], o[e + 1]), pack2<kHalf>(o[e + 2], o[e + 3]),
-                              pack2<kHalf>(o[e + 4], o[e + 5]), pack2<kHalf>(o[e + 6], o[e + 7]),
-                              pack2<kHalf>(o[e + 8], o[e + 9]), pack2<kHalf>(o[e + 10], o[e + 11]),
-                              pack2<kHalf>(o[e + 12], o[e + 13]), pack2<kHalf>(o[e + 14], o[e + 15]));
-        } else if (there) {
-          float* dst = a.piece_o + slot * D + k * 32;
-#pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            ptx::st_global_v8(dst + e, __float_as_uint(o[e]), __float_as_uint(o[e + 1]),
-                              __float_as_uint(o[e + 2]), __float_as_uint(o[e + 3]), __float_as_uint(o[e + 4]),
-                              __float_as_uint(o[e + 5]), __float_as_uint(o[e + 6]), __float_as_uint(o[e + 7]));
+        for (int k = 0; k < D / 64; ++k) {
+          ptx::tmem_ld32(o_tmem + c0 + k * 32, *reinterpret_cast<float(*)[32]>(o + k * 32));
+          ptx::tmem_ld32(other + c0 + k * 32, *reinterpret_cast<float(*)[32]>(o + D / 2 + k * 32));
         }
       }
-      if (there && (pair || t == 0)) {
+      ptx::tmem_wait_ld();
+      ptx::tc_fence_before();
+      if (alone) {
+        ptx::mbar_arrive_n(c.o_empty(t), 2);
+#pragma unroll
+        for (int k = 0; k < D; ++k) o[k] *= a0;
+      } else {
+        ptx::mbar_arrive(c.o_empty(0));
+        ptx::mbar_arrive(c.o_empty(1));
+#pragma unroll
+        for (int k = 0; k < D / 2; ++k) o[k] = fmaf(o[D / 2 + k], a1, o[k] * a0);
+      }
+      if (whole) {
+        const int row_at = there ? (int)at : -1;  // (below 2^30)
+#pragma unroll
+        for (int g = 0; g < D / 64; ++g) {  // 64 columns: a line of 128 bytes
+          if (g * 64 < columns) {
+            uint32_t w[4][8];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) w[e >> 3][e & 7] = pack2<kHalf>(o[g * 64 + 2 * e], o[g * 64 + 2 * e + 1]);
+            if (D == 64 && !alone) {
+              // 32 columns: two chunks a row, stored as they are
+              if (there) {
+                uint16_t* dst = p.out + at * D + c0;
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                  ptx::st_global_v8(dst + x * 16, w[x][0], w[x][1], w[x][2], w[x][3], w[x][4], w[x][5], w[x][6], w[x][7]);
+              }
+            } else {
+              turn_quads(w);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const int of = __shfl_sync(0xffffffffu, row_at, (lane & ~3) + x);
+                if (of >= 0)
+                  ptx::st_global_v8(p.out + (long long)of * D + c0 + g * 64 + (lane & 3) * 16, w[x][0], w[x][1], w[x][2],
+                                    w[x][3], w[x][4], w[x][5], w[x][6], w[x][7]);
+              }
+            }
+          }
+        }
+      } else if (there) {
+        float* dst = a.piece_o + slot * D + c0;
+#pragma unroll
+        for (int e = 0; e < D; e += 8)
+          if (e < columns)
+            ptx::st_global_v8(dst + e, __float_as_uint(o[e]), __float_as_uint(o[e + 1]), __float_as_uint(o[e + 2]),
+                              __float_as_uint(o[e + 3]), __float_as_uint(o[e + 4]), __float_as_uint(o[e + 5]),
+                              __float_as_uint(o[e + 6]), __float_as_uint(o[e + 7]));
+      }
+      if (there && (alone || t == 0)) {
         if (!whole)
           a.piece_ml[slot] = make_float2(m, l);
         else if (p.lse)
           p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       }
-    }
-    ptx::tc_fence_before();
-    if (pair) {
-      ptx::mbar_arrive_n(c.o_empty(t), 2);
     } else {
-      ptx::mbar_arrive(c.o_empty(0));
-      ptx::mbar_arrive(c.o_empty(1));
+      if (alone) {
+        ptx::mbar_arrive_n(c.o_empty(t), 2);
+      } else {
+        ptx::mbar_arrive(c.o_empty(0));
+        ptx::mbar_arrive(c.o_empty(1));
+      }
     }
-    ++segs;
-    s = s_next;
+    let_go();
   }
-  ptx::cp_async_wait_all();
+}
+
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_tile_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                      const __grid_constant__ CUtensorMap tmv, const ChunkArgs a) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const ChunkParams& p = a.p;
+  Cta<D> c;
+  c.base = ptx::smem_u32(smem);
+  c.ptr = smem;
+  c.status = p.status;
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::kOffWords);
+  c.abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffWords + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Walk& s_walk = *reinterpret_cast<Walk*>(smem + C::kOffWalk);
+  long long* s_sums = reinterpret_cast<long long*>(smem + C::kOffMl);  // (before it holds anything else)
+  long long& s_in = s_sums[kThreads / 32];
+  if (c.base & 1023) {  // the swizzled layouts need it
+    if (threadIdx.x == 0) {
+      if (p.status) atomicOr(p.status, kBatchTimeout);
+      a.cuts[blockIdx.x].pieces = a.cuts[blockIdx.x].broken = 0;
+    }
+    return;
+  }
+  // the merge may set itself up where there is room
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      ptx::mbar_init(c.full(s), 1);
+      ptx::mbar_init(c.empty(s), 2);
+      ptx::mbar_init(c.land(s), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      ptx::mbar_init(c.q_full(t), 1);
+      ptx::mbar_init(c.q_empty(t), 2);
+      ptx::mbar_init(c.drain(t), 1);
+      ptx::mbar_init(c.s_full(t), 1);
+      ptx::mbar_init(c.p_full(t), 128);
+      ptx::mbar_init(c.o_full(t), 1);
+      ptx::mbar_init(c.o_empty(t), 256);
+    }
+    for (int i = 0; i < C::kListed; ++i) {
+      ptx::mbar_init(c.listed(i), 1);
+      ptx::mbar_init(c.unlisted(i), kReaders);
+    }
+    ptx::mbar_init(c.joined(), 256);
+    *c.abort_flag = 0;
+    publish_issued(c.kv_issued(), 0);
+    publish_issued(c.q_issued(0), 0);
+    publish_issued(c.q_issued(1), 0);
+    s_walk.left = s_walk.lead = 0;  // (no steps: nothing else of it is read)
+    ptx::fence_mbar_init();
+  }
+  if (warp == 9) {
+    ptx::tmem_alloc(c.base + C::kOffWords, kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  // Where the run starts: each thread sums up some requests, and the one whose
+  // requests hold the run's first step looks for it.
+  const int per = (p.n_req + kThreads - 1) / kThreads;
+  const int b0 = min((int)threadIdx.x * per, p.n_req), b1 = min(b0 + per, p.n_req);
+  int bad = 0;
+  long long mine = 0, total;
+  for (int b = b0; b < b1; ++b) mine += cost_of_request(a, checked(p, raw_of(p, b), bad));
+  const bool broken = __syncthreads_or(bad & kBadOffsets);
+  if (broken) mine = 0;
+  if (blockIdx.x == 0 && bad && p.status) atomicOr(p.status, bad & ~kBadOffsets);
+  const long long before = scan_block(mine, s_sums, total) - mine;
+  const long long run = max(quotient(total + a.grid - 1, a.grid), 1ll);
+  const long long x0 = run * blockIdx.x, x1 = min(x0 + run, total);
+  if (x0 < x1 && x0 >= before && x0 < before + mine) {
+    long long at = before;
+    for (int b = b0; b < b1; ++b) {
+      const Chunk r = checked(p, raw_of(p, b), bad);
+      const long long cost = cost_of_request(a, r);
+      if (x0 < at + cost) {
+        s_walk.b = b;
+        s_walk.r = r;
+        s_walk.left = (int)(x1 - x0);
+        s_in = x0 - at;
+        break;
+      }
+      at += cost;
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (warp == 0) {
+    Walk w = s_walk;
+    __syncwarp();
+    int pieces = 0;
+    if (w.left > 0) {
+      const int blocks = blocks_of(a, w.r);
+      const long long head_cost = cost_before(a, w.r, blocks);
+      w.head = (int)quotient(s_in, head_cost);
+      const long long in = s_in - w.head * head_cost;
+      // the last block that starts at or before `in`: 32 places at a time
+      int lo = 0, hi = blocks;  // it lies in [lo, hi)
+      while (hi - lo > 1) {
+        const int each = (hi - lo + 31) / 32, k = lo + lane * each;
+        const bool at_or_before = k < hi && cost_before(a, w.r, k) <= in;
+        const int n = __popc(__ballot_sync(0xffffffffu, at_or_before));  // lane 0's is
+        lo += (n - 1) * each;
+        hi = min(hi, lo + each);
+      }
+      const long long start = cost_before(a, w.r, lo);
+      const int behind = (int)(in - start);
+      w.block = lo;
+      w.j = max(behind - kSegmentCost, 0);
+      w.lead = max(kSegmentCost - behind, 0);
+      w.buf = 2;
+      w.look_ahead(p);
+      const int np = (end_of(a, w.r, lo) + kTileTokens - 1) / kTileTokens;
+      if (w.j > 0 && w.j + w.left >= np) {  // (of a segment's first step the run is behind .. - j)
+        const int first = (int)quotient(x0 - w.j, run), t = a.block_tokens;
+        if (lane == 0) {
+          Cut cut{};
+          cut.pieces = (int)blockIdx.x - first + 1;
+          cut.first = first;
+          cut.tok = w.r.tok0 + lo * t;
+          cut.tokens = min(w.r.n - lo * t, t);
+          cut.head = w.head;
+          cut.broken = broken;
+          a.cuts[blockIdx.x] = cut;
+        }
+        pieces = 1;
+      }
+    }
+    if (lane == 0) {
+      if (!pieces) a.cuts[blockIdx.x].pieces = 0, a.cuts[blockIdx.x].broken = broken;
+      s_walk = w;
+    }
+  }
+  __syncthreads();
+  if (warp < 8) {
+    ptx::setmaxnreg_inc<kSoftmaxRegs>();
+    softmax_rows<D, kHalf>(a, c, tmem, warp >> 2);
+  } else {
+    ptx::setmaxnreg_dec<kIssueRegs>();
+    if (warp == 8)
+      stream_kv<D>(&tmk, &tmv, a, c);
+    else if (warp == 10)
+      lane == 0 ? list_segments<D>(&tmq, a, c, s_walk) : void();
+    else
+      issue_products<D, kHalf>(c, tmem, warp == 9 ? 0 : 1);
+    __syncwarp();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kTmemCols);
+  }
 }
 
 // ------------------------------------------------------------- rows that see nothing
@@ -692,169 +1104,25 @@ __device__ __forceinline__ void fill_tokens(const ChunkParams& p, int from, int 
     for (long long i = (long long)from * p.hq + thread; i < (long long)to * p.hq; i += threads) p.lse[i] = -INFINITY;
 }
 __device__ void fill_empty(const ChunkParams& p, bool broken, int thread) {
-  constexpr int kFill = 64;
-  const int all = gridDim.x * kFill, mine = blockIdx.x * kFill + thread;
+  const int blocks = gridDim.x * gridDim.y, block = blockIdx.y * gridDim.x + blockIdx.x;
+  const int all = blocks * blockDim.x, mine = block * blockDim.x + thread;
   if (broken || p.n_req == 0) return fill_tokens(p, 0, p.n_tokens, mine, all);
   if (p.cu) {
     fill_tokens(p, 0, p.cu[0], mine, all);
     fill_tokens(p, p.cu[p.n_req], p.n_tokens, mine, all);
   }
-  for (int b = blockIdx.x; b < p.n_req; b += gridDim.x) {
+  for (int b = block; b < p.n_req; b += blocks) {
     const Raw raw = raw_of(p, b);
     int bad = 0;
     const Chunk r = checked(p, raw, bad);
     const int n = raw.last - raw.first;
-    fill_tokens(p, raw.first, raw.first + (r.n < n ? n : min(max(r.n - r.len, 0), n)), thread, kFill);
-  }
-}
-
-template <int D, bool kHalf>
-__global__ void __launch_bounds__(kThreads, 1)
-    chunk_tile_kernel(const __grid_constant__ CUtensorMap tmk,
-                      const __grid_constant__ CUtensorMap tmv, const ChunkArgs a) {
-  using C = Cfg<D>;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  const ChunkParams& p = a.p;
-  Cta<D> c;
-  c.base = ptx::smem_u32(smem);
-  c.ptr = smem;
-  c.status = p.status;
-  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::kOffBar + C::kBars * 8);
-  c.abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffBar + C::kBars * 8 + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Walk& s_walk = *reinterpret_cast<Walk*>(smem + C::kOffWalk);
-  long long* s_sums = reinterpret_cast<long long*>(smem + C::kOffMl);  // (before it holds anything else)
-  long long& s_in = s_sums[kThreads / 32];
-  if (c.base & 1023) {  // the swizzled layouts need it
-    if (threadIdx.x == 0) {
-      if (p.status) atomicOr(p.status, kBatchTimeout);
-      a.cuts[blockIdx.x].pieces = 0;
-    }
-    return;
-  }
-  // the merge may set itself up where there is room
-  asm volatile("griddepcontrol.launch_dependents;");
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
-      ptx::mbar_init(c.full(s), 1);
-      ptx::mbar_init(c.empty(s), 1);
-      ptx::mbar_init(c.land(s), 1);
-    }
-    for (int t = 0; t < 2; ++t) {
-      ptx::mbar_init(c.q_full(t), 128);
-      ptx::mbar_init(c.s_full(t), 1);
-      ptx::mbar_init(c.p_full(t), 128);
-      ptx::mbar_init(c.o_full(t), 1);
-      ptx::mbar_init(c.o_empty(t), 256);
-    }
-    ptx::mbar_init(c.joined(), 256);
-    ptx::mbar_init(c.drain(), 1);
-    *c.abort_flag = 0;
-    s_walk.left = 0;
-    ptx::fence_mbar_init();
-  }
-  if (warp == 9) {
-    ptx::tmem_alloc(c.base + C::kOffBar + C::kBars * 8, kTmemCols);
-    ptx::tmem_relinquish();
-  }
-  // Where the run starts: each thread sums up some requests, and the one whose
-  // requests hold the run's first step looks for it.
-  const int per = (p.n_req + kThreads - 1) / kThreads;
-  const int b0 = min((int)threadIdx.x * per, p.n_req), b1 = min(b0 + per, p.n_req);
-  int bad = 0;
-  long long mine = 0, total;
-  for (int b = b0; b < b1; ++b) mine += steps_of_request(a, checked(p, raw_of(p, b), bad));
-  const bool broken = __syncthreads_or(bad & kBadOffsets);
-  if (broken) mine = 0;
-  if (blockIdx.x == 0 && bad && p.status) atomicOr(p.status, bad & ~kBadOffsets);
-  const long long before = scan_block(mine, s_sums, total) - mine;
-  const long long run = max(quotient(total + a.grid - 1, a.grid), 1ll);
-  const long long x0 = run * blockIdx.x, x1 = min(x0 + run, total);
-  if (x0 < x1 && x0 >= before && x0 < before + mine) {
-    long long at = before;
-    for (int b = b0; b < b1; ++b) {
-      const Chunk r = checked(p, raw_of(p, b), bad);
-      const long long steps = steps_of_request(a, r);
-      if (x0 < at + steps) {
-        s_walk.b = b;
-        s_walk.r = r;
-        s_walk.left = (int)(x1 - x0);
-        s_in = x0 - at;
-        break;
-      }
-      at += steps;
-    }
-  }
-  ptx::tc_fence_before();
-  __syncthreads();
-  ptx::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  if (warp == 0) {
-    Walk w = s_walk;
-    __syncwarp();
-    int pieces = 0;
-    if (w.left > 0) {
-      const long long head_steps = steps_before(a, w.r, blocks_of(a, w.r));
-      w.head = (int)quotient(s_in, head_steps);
-      const long long in = s_in - w.head * head_steps;
-      // the last block that starts at or before step `in`: 32 places at a time
-      int lo = 0, hi = blocks_of(a, w.r);  // it lies in [lo, hi)
-      while (hi - lo > 1) {
-        const int each = (hi - lo + 31) / 32, k = lo + lane * each;
-        const bool at_or_before = k < hi && steps_before(a, w.r, k) <= in;
-        const int n = __popc(__ballot_sync(0xffffffffu, at_or_before));  // lane 0's is
-        lo += (n - 1) * each;
-        hi = min(hi, lo + each);
-      }
-      w.block = lo;
-      w.j = (int)(in - steps_before(a, w.r, lo));
-      w.buf = -1;
-      w.look_ahead(p);
-      const int np = steps_of_block(a, w.r, lo);
-      if (w.j > 0 && w.j + w.left >= np) {
-        const int first = (int)quotient(x0 - w.j, run), t = a.block_tokens;
-        if (lane == 0) {
-          Cut cut{};
-          cut.pieces = (int)blockIdx.x - first + 1;
-          cut.first = first;
-          cut.tok = w.r.tok0 + lo * t;
-          cut.rows = min(w.r.n - lo * t, t) * p.gqa;
-          cut.head = w.head;
-          a.cuts[blockIdx.x] = cut;
-        }
-        pieces = 1;
-      }
-    }
-    if (lane == 0) {
-      if (!pieces) a.cuts[blockIdx.x].pieces = 0;
-      s_walk = w;
-    }
-  }
-  __syncthreads();
-  const Walk walk = s_walk;
-  if (warp < 8) {
-    ptx::setmaxnreg_inc<kSoftmaxRegs>();
-    softmax_rows<D, kHalf>(a, c, walk, tmem, warp >> 2);
-  } else {
-    ptx::setmaxnreg_dec<kIssueRegs>();
-    if (warp == 8)
-      stream_kv<D>(&tmk, &tmv, a, c, walk);
-    else if (warp == 9)
-      issue_products<D, kHalf>(a, c, walk, tmem);
-    else
-      fill_empty(p, broken, threadIdx.x - 320);
-    __syncwarp();
-  }
-  ptx::tc_fence_before();
-  __syncthreads();
-  if (warp == 9) {
-    ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, kTmemCols);
+    fill_tokens(p, raw.first, raw.first + (r.n < n ? n : min(max(r.n - r.len, 0), n)), thread, blockDim.x);
   }
 }
 
 // ------------------------------------------------------------- merge
-// A warp a row of a segment that was cut; blockIdx.x is the run where it ends.
+// A warp a row of a segment that was cut; blockIdx.x is the run where it ends.  And
+// the rows that see nothing.
 constexpr int kMergeWarps = 8;
 
 template <int D, bool kHalf>
@@ -863,9 +1131,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
   const ChunkParams& p = a.p;
   const int lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  fill_empty(p, a.cuts[0].broken, threadIdx.x);
   const Cut cut = a.cuts[blockIdx.x];
   const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
-  if (cut.pieces == 0 || row >= cut.rows) return;
+  const int in_tile = (row & (kTile - 1)) / p.gqa, tok = (row / kTile) * a.tile_tokens + in_tile;
+  if (cut.pieces == 0 || in_tile >= a.tile_tokens || tok >= cut.tokens) return;
   auto slot = [&](int k) { return (2ll * (cut.first + k) + (k == 0 ? 1 : 0)) * a.piece_rows + row; };
   float m = -INFINITY;
   for (int k = lane; k < cut.pieces; k += 32) m = fmaxf(m, a.piece_ml[slot(k)].x);
@@ -899,7 +1169,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
 #pragma unroll
   for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-  const long long at = (long long)(cut.tok + row / p.gqa) * p.hq + cut.head * p.gqa + row % p.gqa;
+  const long long at = (long long)(cut.tok + tok) * p.hq + cut.head * p.gqa + (row & (kTile - 1)) % p.gqa;
   uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + at * D + lane * E);
 #pragma unroll
   for (int e = 0; e < E; e += 2) dst[e / 2] = pack2<kHalf>(acc[e] * inv, acc[e + 1] * inv);
@@ -909,10 +1179,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
 // Sizes of a run, and where its workspace lies.
 size_t lay_out(const ChunkParams& p, uint8_t* work, ChunkArgs* a) {
   a->p = p;
-  a->block_tokens = kBlockRows / p.gqa;
+  a->tile_tokens = kTile / p.gqa;
+  a->block_tokens = 2 * a->tile_tokens;
+  a->block_shift = -1;
+  for (int e = 0; e <= 8; ++e)
+    if (a->block_tokens == 1 << e) a->block_shift = e;
   const long long blocks = ((long long)p.n_tokens / a->block_tokens + std::min(p.n_req, p.n_tokens)) * p.hkv;
   a->grid = (int)std::max(1ll, std::min<long long>(p.num_sms, blocks * (p.width ? p.width / kStepPages + 1 : p.num_sms)));
-  a->piece_rows = (int)std::min<long long>(kBlockRows, (long long)p.n_tokens * p.gqa);
+  a->piece_rows = p.n_tokens > a->tile_tokens ? 2 * kTile : p.n_tokens * p.gqa;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     uint8_t* from = work ? work + at : nullptr;
@@ -930,8 +1204,11 @@ size_t lay_out(const ChunkParams& p, uint8_t* work, ChunkArgs* a) {
 template <int D, bool kHalf>
 cudaError_t run(const ChunkArgs& a, cudaStream_t s) {
   const ChunkParams& p = a.p;
-  CUtensorMap mk, mv;
-  cudaError_t e = make_page_map(&mk, p.k_pages, D, p.hkv, p.num_pages, false);
+  CUtensorMap mq, mk, mv;
+  cudaError_t e = make_query_map(&mq, p.q, D, p.hq, p.n_tokens, std::max<long long>(p.q_stride, (long long)p.hq * D),
+                                 p.gqa, a.tile_tokens);
+  if (e != cudaSuccess) return e;
+  e = make_page_map(&mk, p.k_pages, D, p.hkv, p.num_pages, false);
   if (e != cudaSuccess) return e;
   e = make_page_map(&mv, p.v_pages, D, p.hkv, p.num_pages, true);
   if (e != cudaSuccess) return e;
@@ -943,7 +1220,7 @@ cudaError_t run(const ChunkArgs& a, cudaStream_t s) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Cfg<D>::kSmem;
   cfg.stream = s;
-  e = cudaLaunchKernelEx(&cfg, chunk_tile_kernel<D, kHalf>, mk, mv, a);
+  e = cudaLaunchKernelEx(&cfg, chunk_tile_kernel<D, kHalf>, mq, mk, mv, a);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -83,6 +83,9 @@ constexpr int64_t kMergeEarlyRows = 16384;
 // Tensor map of a page pool (see its definition).
 cudaError_t make_page_map(CUtensorMap* m, const void* base, int d, int hkv, int num_pages,
                           bool whole_page_head);
+// Tensor map of queries (see its definition).
+cudaError_t make_query_map(CUtensorMap* m, const void* q, int d, int hq, long long tokens,
+                           long long stride, int heads, int box_tokens);
 // Launch the persistent grouped partial-attention kernel (TMA + tcgen05 /
 // CUDA cores), one CTA per schedule entry.  kv_evict: the plan's K/V mostly
 // streams once (HostPlan::kv_evict); its copies then carry L2 policies.

@@ -40,6 +40,11 @@ __device__ __forceinline__ bool wait(const Cta& c, uint32_t bar, uint32_t parity
   if (!ok) ok = wait_slow<kRole>(bar, parity, c.abort_flag, c.status);
   return __all_sync(0xffffffffu, ok);
 }
+// The same for a role of one thread.
+template <int kRole, class Cta>
+__device__ __forceinline__ bool wait_one(const Cta& c, uint32_t bar, uint32_t parity) {
+  return ptx::mbar_try_wait(bar, parity) || wait_slow<kRole>(bar, parity, c.abort_flag, c.status);
+}
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = ptx::globaltimer();
   while (!ptx::mbar_try_wait(bar, parity))

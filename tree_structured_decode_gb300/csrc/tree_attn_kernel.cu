@@ -1345,6 +1345,23 @@ cudaError_t make_page_map(CUtensorMap* m, const void* base, int d, int hkv, int 
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Queries [tokens][hq][d], tokens `stride` elements apart, as a 3-D tensor (d,
+// head, token) whose box is 64 columns of `heads` heads of `box_tokens` tokens:
+// rows (token, head) of 128 bytes, 128-byte swizzle.
+cudaError_t make_query_map(CUtensorMap* m, const void* q, int d, int hq, long long tokens,
+                           long long stride, int heads, int box_tokens) {
+  auto fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)hq, (cuuint64_t)tokens};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)box_tokens};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box,
+                        estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 namespace {
 
 template <int D, bool kEvict>
