@@ -56,8 +56,6 @@ namespace {
 using tiles::drain_wait;
 using tiles::pack2;
 using tiles::rescale_o;
-using tiles::wait;
-using tiles::wait_one;
 
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kThreads = 384;
@@ -66,6 +64,7 @@ static_assert(256 * kSoftmaxRegs + 128 * kIssueRegs <= kThreads * 168, "register
 constexpr float kRescaleLog2 = 8.f;  // O is rescaled when a row's maximum grows by more than 2^8
 constexpr uint32_t kTmemCols = 512;  // S of both tiles (128 columns each), O of both (128 each)
 constexpr int kTile = 128;           // query rows of a tile, at most
+constexpr int kTurnTries = 1 << 24;  // a second or so
 constexpr long long kIdleLimitNs = 20000000000ll;  // without a segment to list or queries to bring
 constexpr int kSegmentCost = 2;      // what a segment costs beside its steps, in steps
 constexpr int kStepPages = kTileTokens / kPage;
@@ -150,9 +149,10 @@ __device__ __forceinline__ long long shifted_sum(long long n, long long c, int s
 __device__ __forceinline__ int blind_blocks(const ChunkArgs& a, const Chunk& r) {
   return r.len < r.n ? (r.n - r.len) / a.block_tokens : 0;
 }
+// (Out of line, and so is what calls it: code that runs once is fetched once.)
 // What the first k blocks cost, one kv head: their steps, and kSegmentCost for each
 // that has some.
-__device__ __forceinline__ long long cost_before(const ChunkArgs& a, const Chunk& r, int k) {
+__device__ __noinline__ long long cost_before(const ChunkArgs& a, const Chunk& r, int k) {
   const int blocks = blocks_of(a, r), base = r.len - r.n, t = a.block_tokens;
   const int k0 = min(blind_blocks(a, r), k);
   long long sum = (long long)kSegmentCost * (k - k0);
@@ -210,24 +210,64 @@ struct Walk {
     // one tile's queries: not into the buffer of the ones before
     buf = s.tokens > a.tile_tokens ? 2 : buf == 0;
     s.buf = buf;
+    lead = kSegmentCost;
+    if (left > lead) advance(a);
+    return true;
+  }
+  // To the next segment, which there has to be.
+  __device__ __forceinline__ void advance(const ChunkArgs& a) {
     j = 0;
     lead = kSegmentCost;
-    if (left > lead && (++block) * t >= r.n) {
-      if (++head == a.p.hkv) {
-        head = 0;
-        int bad = 0;
-        do {  // the steps left are some request's
-          ++b;
-          r = checked(a.p, ahead, bad);
-          look_ahead(a.p);
-        } while ((r.n == 0 || r.len == 0) && b + 1 < a.p.n_req);
-      }
-      block = blind_blocks(a, r);
+    if ((++block) * a.block_tokens < r.n) return;
+    if (++head == a.p.hkv) {
+      head = 0;
+      int bad = 0;
+      do {
+        ++b;
+        r = checked(a.p, ahead, bad);
+        look_ahead(a.p);
+      } while ((r.n == 0 || r.len == 0) && b + 1 < a.p.n_req);
     }
-    return true;
+    block = blind_blocks(a, r);
   }
 };
 
+// A place in the line of costs: the request, and how far behind its start.
+struct Place {
+  long long in;
+  int b;
+  Chunk r;
+};
+// Its segment (a warp looks for it): how far behind that one's start, and its cost.
+struct Spot {
+  int head, block, behind, cost;
+};
+__device__ __noinline__ Spot spot_of(const ChunkArgs& a, const Place& at) {
+  const int lane = threadIdx.x & 31, blocks = blocks_of(a, at.r);
+  const long long head_cost = cost_before(a, at.r, blocks);
+  Spot s;
+  s.head = (int)quotient(at.in, head_cost);
+  const long long in = at.in - s.head * head_cost;
+  if (blocks == 1) {
+    s.block = 0;
+    s.behind = (int)in;
+    s.cost = (int)head_cost;
+    return s;
+  }
+  // the last block that starts at or before `in`: 32 places at a time
+  int lo = 0, hi = blocks;  // it lies in [lo, hi)
+  while (hi - lo > 1) {
+    const int each = (hi - lo + 31) / 32, k = lo + lane * each;
+    const bool at_or_before = k < hi && cost_before(a, at.r, k) <= in;
+    const int n = __popc(__ballot_sync(0xffffffffu, at_or_before));  // lane 0's is
+    lo += (n - 1) * each;
+    hi = min(hi, lo + each);
+  }
+  s.block = lo;
+  s.behind = (int)(in - cost_before(a, at.r, lo));
+  s.cost = (end_of(a, at.r, lo) + kTileTokens - 1) / kTileTokens + kSegmentCost;
+  return s;
+}
 template <int D>
 struct Cfg {
   static constexpr int kHalves = D / 64;
@@ -243,20 +283,22 @@ struct Cfg {
   // the TMEM address, the abort flag, copies issued: ring entries, of each query buffer
   static constexpr int kOffWords = kOffBar + kBars * 8;
   static constexpr int kOffList = (kOffWords + 20 + 15) / 16 * 16;
-  static constexpr int kOffWalk = kOffList + kListed * sizeof(Segment);
-  static constexpr int kSmem = kOffWalk + sizeof(Walk);
+  static constexpr int kOffPlace = kOffList + kListed * sizeof(Segment);
+  static constexpr int kSmem = kOffPlace + sizeof(Place);
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 
+extern __shared__ __align__(1024) uint8_t chunk_smem[];
+
+// Places in shared memory.  (No member: what the roles hold in registers decides how
+// fast they are.)
 template <int D>
 struct Cta {
   using C = Cfg<D>;
-  uint32_t base;
-  uint8_t* ptr;
-  volatile int* abort_flag;
-  int32_t* status;
+  static __device__ uint32_t base() { return ptx::smem_u32(chunk_smem); }
+  static __device__ volatile int* abort_flag() { return reinterpret_cast<volatile int*>(chunk_smem + C::kOffWords + 4); }
 
-  __device__ uint32_t bar(int i) const { return base + C::kOffBar + 8 * i; }
+  __device__ uint32_t bar(int i) const { return base() + C::kOffBar + 8 * i; }
   __device__ uint32_t full(int s) const { return bar(s); }
   __device__ uint32_t empty(int s) const { return bar(C::kStages + s); }
   __device__ uint32_t land(int s) const { return bar(2 * C::kStages + s); }
@@ -271,14 +313,22 @@ struct Cta {
   __device__ uint32_t listed(uint32_t i) const { return bar(3 * C::kStages + 15 + i % C::kListed); }
   __device__ uint32_t unlisted(uint32_t i) const { return bar(3 * C::kStages + 15 + C::kListed + i % C::kListed); }
   __device__ Segment* segment(uint32_t i) const {
-    return reinterpret_cast<Segment*>(ptr + C::kOffList) + i % C::kListed;
+    return reinterpret_cast<Segment*>(chunk_smem + C::kOffList) + i % C::kListed;
   }
   static __device__ uint32_t round(uint32_t i) { return i / C::kListed & 1; }
-  __device__ uint32_t kv_issued() const { return base + C::kOffWords + 8; }
-  __device__ uint32_t q_issued(int buf) const { return base + C::kOffWords + 12 + 4 * buf; }
-  __device__ uint32_t stage(int s) const { return base + C::kOffStage + s * C::kStageBytes; }
-  __device__ float2* ml() const { return reinterpret_cast<float2*>(ptr + C::kOffMl); }
+  __device__ uint32_t kv_issued() const { return base() + C::kOffWords + 8; }
+  __device__ uint32_t q_issued(int buf) const { return base() + C::kOffWords + 12 + 4 * buf; }
+  __device__ uint32_t stage(int s) const { return base() + C::kOffStage + s * C::kStageBytes; }
+  __device__ float2* ml() const { return reinterpret_cast<float2*>(chunk_smem + C::kOffMl); }
 };
+
+// tiles::wait with this kernel's abort flag and status word.
+template <int kRole, int D>
+__device__ __forceinline__ bool wait(const Cta<D>& c, int32_t* status, uint32_t bar, uint32_t parity) {
+  bool ok = ptx::mbar_try_wait(bar, parity);
+  if (!ok) ok = tiles::wait_slow<kRole>(bar, parity, c.abort_flag(), status);
+  return __all_sync(0xffffffffu, ok);
+}
 
 // Copies issued, counted.  A reader that does not use every entry of a ring cannot
 // tell by parity alone whether a stage's barrier is in the entry's phase or still in
@@ -291,26 +341,25 @@ __device__ __forceinline__ uint32_t issued_of(uint32_t word) {
   asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(n) : "r"(word) : "memory");
   return n;
 }
-template <class C>
-__device__ __noinline__ bool wait_issued_slow(const C& c, uint32_t word, uint32_t least) {
+__device__ __noinline__ bool wait_issued_slow(uint32_t word, uint32_t least, volatile int* abort_flag, int32_t* status) {
   const uint64_t t0 = ptx::globaltimer();
   for (uint32_t n = 1;; ++n) {
     if ((int32_t)(issued_of(word) - least) >= 0) return true;
     if ((n & 15) == 0) {
-      if (*c.abort_flag) return false;
+      if (*abort_flag) return false;
       if ((long long)(ptx::globaltimer() - t0) > tiles::kWaitLimitNs) {
-        *c.abort_flag = 1;
-        if (c.status) atomicOr(c.status, kBatchTimeout);
+        *abort_flag = 1;
+        if (status) atomicOr(status, kBatchTimeout);
         return false;
       }
     }
   }
 }
 // True once at least so many have been issued; the same in all lanes of the warp.
-template <class C>
-__device__ __forceinline__ bool wait_issued(const C& c, uint32_t word, uint32_t least) {
+template <int D>
+__device__ __forceinline__ bool wait_issued(const Cta<D>& c, int32_t* status, uint32_t word, uint32_t least) {
   bool ok = (int32_t)(issued_of(word) - least) >= 0;
-  if (!ok) ok = wait_issued_slow(c, word, least);
+  if (!ok) ok = wait_issued_slow(word, least, c.abort_flag(), status);
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -337,7 +386,7 @@ __device__ void stream_kv(const CUtensorMap* tmk, const CUtensorMap* tmv, const 
   uint32_t g = 0, seg = 0;
   uint32_t zeroed = 0;  // phase of each stage's land barrier
   const auto read = [&](Segment& to) {  // the next listed segment; false: given up
-    if (!wait<1>(c, c.listed(seg), c.round(seg))) return false;
+    if (!wait<1>(c, p.status, c.listed(seg), c.round(seg))) return false;
     to = *c.segment(seg);
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(c.unlisted(seg));
@@ -362,7 +411,7 @@ __device__ void stream_kv(const CUtensorMap* tmk, const CUtensorMap* tmv, const 
 #pragma unroll
       for (int v = 0; v < 2; ++v, ++g) {
         const int st = g % C::kStages;
-        if (g >= (uint32_t)C::kStages && !wait<1>(c, c.empty(st), (g / C::kStages + 1) & 1)) {
+        if (g >= (uint32_t)C::kStages && !wait<1>(c, p.status, c.empty(st), (g / C::kStages + 1) & 1)) {
           ok = false;
           break;
         }
@@ -391,8 +440,8 @@ __device__ void stream_kv(const CUtensorMap* tmk, const CUtensorMap* tmv, const 
           // 0 * NaN is not 0
           const uint32_t par = (zeroed >> st) & 1;
           zeroed ^= 1u << st;
-          if (wait<1>(c, bar, par)) {
-            uint8_t* head = c.ptr + C::kOffStage + st * C::kStageBytes + (nb - 1) * C::kHead;
+          if (wait<1>(c, p.status, bar, par)) {
+            uint8_t* head = chunk_smem + C::kOffStage + st * C::kStageBytes + (nb - 1) * C::kHead;
             for (int i = lane; i < (kPage - last) * 8 * C::kHalves; i += 32) {
               const int r = last + i / (8 * C::kHalves), h = (i >> 3) % C::kHalves, ch = i & 7;
               *reinterpret_cast<uint4*>(head + h * 2048 + r * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
@@ -414,11 +463,41 @@ __device__ void stream_kv(const CUtensorMap* tmk, const CUtensorMap* tmv, const 
       drain_wait(c.full(k % C::kStages), (k / C::kStages) & 1);
 }
 
-// One thread: lists the run's segments as there is room, and brings each one's
-// queries as soon as its buffer is free.
+// A warp finds where the run [x0, x1) starts, and says what the merge has to know.
+__device__ __forceinline__ Walk start_of_run(const ChunkArgs& a, const Place& place, long long x0, long long x1,
+                                             long long run, bool broken) {
+  Walk w{};  // (no steps: left and lead are 0)
+  Cut cut{};
+  cut.broken = broken;
+  if (x0 < x1) {
+    const Spot spot = spot_of(a, place);
+    w.b = place.b;
+    w.r = place.r;
+    w.head = spot.head;
+    w.block = spot.block;
+    w.left = (int)(x1 - x0);
+    w.j = max(spot.behind - kSegmentCost, 0);
+    w.lead = max(kSegmentCost - spot.behind, 0);
+    w.buf = 2;
+    w.look_ahead(a.p);
+    if (w.j > 0 && w.j + w.left >= spot.cost - kSegmentCost) {  // a piece that began before, and ends here
+      cut.first = (int)quotient(x0 - w.j, run);                  // (x0 - j: its first step)
+      cut.pieces = (int)blockIdx.x - cut.first + 1;
+      cut.tok = w.r.tok0 + w.block * a.block_tokens;
+      cut.tokens = min(w.r.n - w.block * a.block_tokens, a.block_tokens);
+      cut.head = w.head;
+    }
+  }
+  if ((threadIdx.x & 31) == 0) a.cuts[blockIdx.x] = cut;
+  return w;
+}
+
+// One thread of a warp: lists the run's segments as there is room, and brings each
+// one's queries as soon as its buffer is free.
 template <int D>
 __device__ void list_segments(const CUtensorMap* tmq, const ChunkArgs& a, const Cta<D>& c, Walk walk) {
   using C = Cfg<D>;
+  if (threadIdx.x & 31) return;
   uint32_t listed = 0, brought = 0;  // segments
   uint32_t loads[2] = {0, 0};        // of each query buffer
   int tile = 0;                      // of two, brought already
@@ -448,7 +527,7 @@ __device__ void list_segments(const CUtensorMap* tmq, const ChunkArgs& a, const 
         const int tok = s.tok + (s.pair() ? tile * a.tile_tokens : 0);
 #pragma unroll
         for (int h = 0; h < C::kHalves; ++h)
-          ptx::tma_load_3d(c.base + buf * C::kQBytes + h * (kTile * 128), tmq, 64 * h, s.head * a.p.gqa, tok, bar);
+          ptx::tma_load_3d(c.base() + buf * C::kQBytes + h * (kTile * 128), tmq, 64 * h, s.head * a.p.gqa, tok, bar);
         buf ? ++loads[1] : ++loads[0];
         if (s.pair() && tile == 0) {
           tile = 1;
@@ -466,16 +545,16 @@ __device__ void list_segments(const CUtensorMap* tmq, const ChunkArgs& a, const 
     }
     __nanosleep(32);
     if ((polls & 15) == 0) {
-      if (*c.abort_flag) break;
+      if (*c.abort_flag()) break;
       // (a segment may take as long as its steps, each of whose waits is limited)
       if ((long long)(ptx::globaltimer() - since) > kIdleLimitNs) {
-        *c.abort_flag = 1;
-        if (c.status) atomicOr(c.status, kBatchTimeout);
+        *c.abort_flag() = 1;
+        if (a.p.status) atomicOr(a.p.status, kBatchTimeout);
         break;
       }
     }
   }
-  if (*c.abort_flag)  // the copies in flight land before the CTA may end
+  if (*c.abort_flag())  // the copies in flight land before the CTA may end
 #pragma unroll
     for (int buf = 0; buf < 2; ++buf)
       if (loads[buf] > 0) drain_wait(c.q_full(buf), (loads[buf] - 1) & 1);
@@ -486,13 +565,13 @@ __device__ void list_segments(const CUtensorMap* tmq, const ChunkArgs& a, const 
 // a half's next task is issued right behind P V of the one before, in one go where
 // its keys are there already.
 template <int D, bool kHalf>
-__device__ void issue_products(const Cta<D>& c, uint32_t tmem, int t) {
+__device__ void issue_products(const ChunkParams& p, const Cta<D>& c, uint32_t tmem, int t) {
   using C = Cfg<D>;
   constexpr uint32_t kType = kHalf ? 0u : (1u << 7) | (1u << 10);
   constexpr uint32_t kDescQK =
       (ptx::idesc_bf16(128, kTileTokens, 0) & ~((1u << 7) | (1u << 10))) | kType;
   constexpr uint32_t kDescPV = (ptx::idesc_bf16(128, D, 1) & ~((1u << 7) | (1u << 10))) | kType;
-  const uint64_t desc_q = ptx::sdesc_sw128(c.base, 16, 1024);
+  const uint64_t desc_q = ptx::sdesc_sw128(c.base(), 16, 1024);
   const uint64_t desc_k = ptx::sdesc_sw128(c.stage(0), 16, 1024);
   const uint64_t desc_v = ptx::sdesc_sw128(c.stage(0), 2048, 1024);
   const uint32_t s_tmem = tmem + t * 128, o_tmem = tmem + 256 + t * 128;
@@ -510,7 +589,7 @@ __device__ void issue_products(const Cta<D>& c, uint32_t tmem, int t) {
   // This half's next task: 1, 0 where there is none, -1: given up.
   const auto next_task = [&](Task& k) {
     while (idx >= n) {
-      if (!wait<1>(c, c.listed(seg), c.round(seg))) return -1;
+      if (!wait<1>(c, p.status, c.listed(seg), c.round(seg))) return -1;
       const Segment& s = *c.segment(seg);
       n = s.j1 - s.j0;
       if (n == 0) return 0;
@@ -558,13 +637,13 @@ __device__ void issue_products(const Cta<D>& c, uint32_t tmem, int t) {
     }
   };
   const auto wait_entry = [&](uint32_t entry) {
-    return wait_issued(c, c.kv_issued(), entry + 1) && wait<1>(c, c.full(stage_of(entry)), phase_of(entry));
+    return wait_issued(c, p.status, c.kv_issued(), entry + 1) && wait<1>(c, p.status, c.full(stage_of(entry)), phase_of(entry));
   };
   const auto wait_for_scores = [&](const Task& k) {
     if (!wait_entry(2 * k.step)) return false;
     if (!k.first) return true;
     const uint32_t loads = k.buf ? q_loads[1] : q_loads[0];
-    return wait_issued(c, c.q_issued(k.buf), loads) && wait<1>(c, c.q_full(k.buf), (loads - 1) & 1);
+    return wait_issued(c, p.status, c.q_issued(k.buf), loads) && wait<1>(c, p.status, c.q_full(k.buf), (loads - 1) & 1);
   };
   // whether it would not wait
   const auto can_score = [&](const Task& k) {
@@ -603,10 +682,10 @@ __device__ void issue_products(const Cta<D>& c, uint32_t tmem, int t) {
     ok = wait_entry(2 * now.step + 1);
     // the first P V of a segment overwrites O: the last one's must have been read
     if (ok && now.first) {
-      if (o_read) ok = wait<1>(c, c.o_empty(t), (o_read - 1) & 1);
+      if (o_read) ok = wait<1>(c, p.status, c.o_empty(t), (o_read - 1) & 1);
       ++o_read;
     }
-    if (ok) ok = wait<1>(c, c.p_full(t), done++ & 1);
+    if (ok) ok = wait<1>(c, p.status, c.p_full(t), done++ & 1);
     if (!ok) break;
     const bool together = more && can_score(next);
     ptx::tc_fence_after();
@@ -699,30 +778,7 @@ __device__ __forceinline__ Mask moved(const Mask& m, int n) {
   return r;
 }
 
-// A row's 128 bytes (8 words of each of 4 chunks, w[chunk][..]) against those of
-// the other three lanes of its quad: lane q ends with chunk q of rows 0..3.
-__device__ __forceinline__ void turn_quads(uint32_t (&w)[4][8]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int bit = 1; bit <= 2; bit <<= 1) {
-    const bool high = lane & bit;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      if (x & bit) continue;
-      const int y = x | bit;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? w[x][e] : w[y][e], bit);
-        if (high)
-          w[x][e] = got;
-        else
-          w[y][e] = got;
-      }
-    }
-  }
-}
-
-template <int D, bool kHalf>
+template <int D, bool kHalf, bool kTree>
 __device__ void softmax_rows(const ChunkArgs& a, const Cta<D>& c, uint32_t tmem, int t) {
   using C = Cfg<D>;
   constexpr float kBase = kHalf ? kFp16Base : 0.f;  // m is that much below the largest score
@@ -732,7 +788,6 @@ __device__ void softmax_rows(const ChunkArgs& a, const Cta<D>& c, uint32_t tmem,
   const uint32_t s_tmem = tmem + lanes + t * 128;
   const uint32_t o_tmem0 = tmem + lanes + 256, o_tmem = o_tmem0 + t * 128;
   const int in_tile = tid / p.gqa, in_group = tid - in_tile * p.gqa;  // the row's token and head
-  const bool tree = p.parents != nullptr;
   uint32_t task = 0;  // of the whole run
   uint32_t done = 0, joins = 0;
   uint32_t o_phase = 0;  // of each half's O, a bit each
@@ -740,7 +795,7 @@ __device__ void softmax_rows(const ChunkArgs& a, const Cta<D>& c, uint32_t tmem,
   int above_b = -1, above_tok = 0;  // the block (request, row's token) that `above` was made for
   bool ok = true;
   for (uint32_t seg = 0;; ++seg) {
-    ok = wait<0>(c, c.listed(seg), c.round(seg));
+    ok = wait<0>(c, p.status, c.listed(seg), c.round(seg));
     const Segment& s = *c.segment(seg);
     const int n = s.j1 - s.j0;
     if (!ok || n == 0) break;
@@ -761,19 +816,19 @@ __device__ void softmax_rows(const ChunkArgs& a, const Cta<D>& c, uint32_t tmem,
     const int rows = min(s.tokens - i0, a.tile_tokens) * p.gqa;
     const bool there = tid < rows, act = tid - lane < rows;  // the row, the warp's rows
     const int i = s.first + i0 + in_tile;               // the row's new token
-    if (tree && act && s.j1 * kTileTokens > s.base &&
+    if (kTree && act && s.j1 * kTileTokens > s.base &&
         (above_b != s.b || __any_sync(0xffffffffu, there && above_tok != i))) {
       above = nodes_above(p, s.tok - s.first, s.len - s.base, there ? i : -1);
       above_b = s.b;
       above_tok = i;
     }
     // keys before `clear` are seen by this row
-    const int clear = there ? (tree ? s.base : s.base + i + 1) : INT32_MAX;
+    const int clear = there ? (kTree ? s.base : s.base + i + 1) : INT32_MAX;
     const int j0 = s.j0;
     float m = -INFINITY, l = 0.f;
     bool first = true;
     for (int j = pair ? 0 : (int)(f ^ t); j < n; j += pair ? 1 : 2) {
-      ok = wait<0>(c, c.s_full(t), done++ & 1);
+      ok = wait<0>(c, p.status, c.s_full(t), done++ & 1);
       if (!ok) break;
       ptx::tc_fence_after();
       if (act) {
@@ -785,7 +840,7 @@ __device__ void softmax_rows(const ChunkArgs& a, const Cta<D>& c, uint32_t tmem,
         if (__any_sync(0xffffffffu, clear < key0 + kTileTokens)) {
           const int in = clear - key0;  // seen keys of the step, a tree's aside
           Mask see = first_bits(in);
-          if (tree && in < kTileTokens && in > -kTileTokens) {
+          if (kTree && in < kTileTokens && in > -kTileTokens) {
             const Mask nodes = moved(above, in);
 #pragma unroll
             for (int k = 0; k < 4; ++k) see.w[k] |= nodes.w[k];
@@ -803,6 +858,16 @@ __device__ void softmax_rows(const ChunkArgs& a, const Cta<D>& c, uint32_t tmem,
           m = mx - kBase;
         }
         first = false;
+        // The halves take turns with their exponentials: side by side on the same
+        // schedulers both take as long as one behind the other, and the tensor cores
+        // then wait for both (16384 tokens of 64 heads: 3.24 ms, in turns 3.04).
+        const uint32_t turn = 2 * done - 3 + t;  // the task before this one (done counts it already)
+        if (done + t > 1) {
+          const uint32_t bar = c.p_full(t ^ 1), parity = turn >> 1 & 1;
+          bool there = ptx::mbar_test_wait(bar, parity);  // (in line: a call would spill the scores)
+          for (int tries = 0; !there && tries < kTurnTries; ++tries) there = ptx::mbar_test_wait(bar, parity);
+          // (where it never comes, the waits behind this one give up)
+        }
         l *= alpha;
         // the S that was waited for was issued behind the half's last P V: O holds it
         if (__any_sync(0xffffffffu, alpha != 1.f)) rescale_o<D>(o_tmem, alpha);
@@ -836,7 +901,7 @@ __device__ void softmax_rows(const ChunkArgs& a, const Cta<D>& c, uint32_t tmem,
     if (!alone) {
       c.ml()[t * 128 + tid] = make_float2(m, l);
       ptx::mbar_arrive(c.joined());
-      ok = wait<0>(c, c.joined(), joins++ & 1);
+      ok = wait<0>(c, p.status, c.joined(), joins++ & 1);
       if (!ok) break;
       const float2 o = c.ml()[(t ^ 1) * 128 + tid];
       const float top = fmaxf(m, o.x);
@@ -845,8 +910,8 @@ __device__ void softmax_rows(const ChunkArgs& a, const Cta<D>& c, uint32_t tmem,
       l = a0 * l + a1 * o.y;
       m = top;
     }
-    ok = wait<0>(c, c.o_full(t), o_now >> t & 1);
-    if (ok && !alone) ok = wait<0>(c, c.o_full(t ^ 1), o_now >> (t ^ 1) & 1);
+    ok = wait<0>(c, p.status, c.o_full(t), o_now >> t & 1);
+    if (ok && !alone) ok = wait<0>(c, p.status, c.o_full(t ^ 1), o_now >> (t ^ 1) & 1);
     if (!ok) break;
     ptx::tc_fence_after();
     const bool whole = s.whole();
@@ -857,67 +922,48 @@ __device__ void softmax_rows(const ChunkArgs& a, const Cta<D>& c, uint32_t tmem,
     const long long at = (long long)(s.tok + i0 + in_tile) * p.hq + s.head * p.gqa + in_group;
     const long long slot = (2ll * blockIdx.x + (s.j0 == 0 ? 1 : 0)) * a.piece_rows + (pair ? t * kTile : 0) + tid;
     const int columns = alone ? D : D / 2, c0 = alone ? 0 : t * (D / 2);
-    if (act) {
-      float o[D];
-      if (alone) {
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) ptx::tmem_ld32(o_tmem + k * 32, *reinterpret_cast<float(*)[32]>(o + k * 32));
-      } else {
-        const uint32_t other = o_tmem0 + (t ^ 1) * 128;
-#pragma unroll
-        for (int k = 0; k < D / 64; ++k) {
-          ptx::tmem_ld32(o_tmem + c0 + k * 32, *reinterpret_cast<float(*)[32]>(o + k * 32));
-          ptx::tmem_ld32(other + c0 + k * 32, *reinterpret_cast<float(*)[32]>(o + D / 2 + k * 32));
-        }
-      }
-      ptx::tmem_wait_ld();
+    const uint32_t o_other = o_tmem0 + (t ^ 1) * 128;
+    const auto o_is_read = [&]() {
       ptx::tc_fence_before();
       if (alone) {
         ptx::mbar_arrive_n(c.o_empty(t), 2);
-#pragma unroll
-        for (int k = 0; k < D; ++k) o[k] *= a0;
       } else {
         ptx::mbar_arrive(c.o_empty(0));
         ptx::mbar_arrive(c.o_empty(1));
-#pragma unroll
-        for (int k = 0; k < D / 2; ++k) o[k] = fmaf(o[D / 2 + k], a1, o[k] * a0);
       }
-      if (whole) {
-        const int row_at = there ? (int)at : -1;  // (below 2^30)
+    };
+    if (act) {
+      for (int k = c0; k < c0 + columns; k += 32) {
+        float o[32];
+        ptx::tmem_ld32(o_tmem + k, o);
+        if (alone) {
+          ptx::tmem_wait_ld();
 #pragma unroll
-        for (int g = 0; g < D / 64; ++g) {  // 64 columns: a line of 128 bytes
-          if (g * 64 < columns) {
-            uint32_t w[4][8];
+          for (int e = 0; e < 32; ++e) o[e] *= a0;
+        } else {
+          float o2[32];
+          ptx::tmem_ld32(o_other + k, o2);
+          ptx::tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) w[e >> 3][e & 7] = pack2<kHalf>(o[g * 64 + 2 * e], o[g * 64 + 2 * e + 1]);
-            if (D == 64 && !alone) {
-              // 32 columns: two chunks a row, stored as they are
-              if (there) {
-                uint16_t* dst = p.out + at * D + c0;
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-                  ptx::st_global_v8(dst + x * 16, w[x][0], w[x][1], w[x][2], w[x][3], w[x][4], w[x][5], w[x][6], w[x][7]);
-              }
-            } else {
-              turn_quads(w);
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const int of = __shfl_sync(0xffffffffu, row_at, (lane & ~3) + x);
-                if (of >= 0)
-                  ptx::st_global_v8(p.out + (long long)of * D + c0 + g * 64 + (lane & 3) * 16, w[x][0], w[x][1], w[x][2],
-                                    w[x][3], w[x][4], w[x][5], w[x][6], w[x][7]);
-              }
-            }
-          }
+          for (int e = 0; e < 32; ++e) o[e] = fmaf(o2[e], a1, o[e] * a0);
         }
-      } else if (there) {
-        float* dst = a.piece_o + slot * D + c0;
+        if (k + 32 == c0 + columns) o_is_read();
+        if (there && whole) {
+          uint16_t* dst = p.out + at * D + k;
 #pragma unroll
-        for (int e = 0; e < D; e += 8)
-          if (e < columns)
+          for (int e = 0; e < 32; e += 16)
+            ptx::st_global_v8(dst + e, pack2<kHalf>(o[e], o[e + 1]), pack2<kHalf>(o[e + 2], o[e + 3]),
+                              pack2<kHalf>(o[e + 4], o[e + 5]), pack2<kHalf>(o[e + 6], o[e + 7]),
+                              pack2<kHalf>(o[e + 8], o[e + 9]), pack2<kHalf>(o[e + 10], o[e + 11]),
+                              pack2<kHalf>(o[e + 12], o[e + 13]), pack2<kHalf>(o[e + 14], o[e + 15]));
+        } else if (there) {
+          float* dst = a.piece_o + slot * D + k;
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
             ptx::st_global_v8(dst + e, __float_as_uint(o[e]), __float_as_uint(o[e + 1]), __float_as_uint(o[e + 2]),
                               __float_as_uint(o[e + 3]), __float_as_uint(o[e + 4]), __float_as_uint(o[e + 5]),
                               __float_as_uint(o[e + 6]), __float_as_uint(o[e + 7]));
+        }
       }
       if (there && (alone || t == 0)) {
         if (!whole)
@@ -926,35 +972,25 @@ __device__ void softmax_rows(const ChunkArgs& a, const Cta<D>& c, uint32_t tmem,
           p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       }
     } else {
-      if (alone) {
-        ptx::mbar_arrive_n(c.o_empty(t), 2);
-      } else {
-        ptx::mbar_arrive(c.o_empty(0));
-        ptx::mbar_arrive(c.o_empty(1));
-      }
+      o_is_read();
     }
     let_go();
   }
 }
 
-template <int D, bool kHalf>
+template <int D, bool kHalf, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_tile_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv, const ChunkArgs a) {
   using C = Cfg<D>;
-  extern __shared__ __align__(1024) uint8_t smem[];
   const ChunkParams& p = a.p;
-  Cta<D> c;
-  c.base = ptx::smem_u32(smem);
-  c.ptr = smem;
-  c.status = p.status;
+  const Cta<D> c{};
+  uint8_t* const smem = chunk_smem;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::kOffWords);
-  c.abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffWords + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Walk& s_walk = *reinterpret_cast<Walk*>(smem + C::kOffWalk);
+  Place& s_place = *reinterpret_cast<Place*>(smem + C::kOffPlace);
   long long* s_sums = reinterpret_cast<long long*>(smem + C::kOffMl);  // (before it holds anything else)
-  long long& s_in = s_sums[kThreads / 32];
-  if (c.base & 1023) {  // the swizzled layouts need it
+  if (c.base() & 1023) {  // the swizzled layouts need it
     if (threadIdx.x == 0) {
       if (p.status) atomicOr(p.status, kBatchTimeout);
       a.cuts[blockIdx.x].pieces = a.cuts[blockIdx.x].broken = 0;
@@ -983,40 +1019,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(c.unlisted(i), kReaders);
     }
     ptx::mbar_init(c.joined(), 256);
-    *c.abort_flag = 0;
+    *c.abort_flag() = 0;
     publish_issued(c.kv_issued(), 0);
     publish_issued(c.q_issued(0), 0);
     publish_issued(c.q_issued(1), 0);
-    s_walk.left = s_walk.lead = 0;  // (no steps: nothing else of it is read)
     ptx::fence_mbar_init();
   }
   if (warp == 9) {
-    ptx::tmem_alloc(c.base + C::kOffWords, kTmemCols);
+    ptx::tmem_alloc(c.base() + C::kOffWords, kTmemCols);
     ptx::tmem_relinquish();
   }
-  // Where the run starts: each thread sums up some requests, and the one whose
-  // requests hold the run's first step looks for it.
+  // Each thread sums up some requests, and the one whose requests hold the run's
+  // start says which.
   const int per = (p.n_req + kThreads - 1) / kThreads;
   const int b0 = min((int)threadIdx.x * per, p.n_req), b1 = min(b0 + per, p.n_req);
   int bad = 0;
   long long mine = 0, total;
-  for (int b = b0; b < b1; ++b) mine += cost_of_request(a, checked(p, raw_of(p, b), bad));
-  const bool broken = __syncthreads_or(bad & kBadOffsets);
-  if (broken) mine = 0;
+  Chunk only{};  // where a thread has one request
+  for (int b = b0; b < b1; ++b) {
+    only = checked(p, raw_of(p, b), bad);
+    mine += cost_of_request(a, only);
+  }
+  // offsets out of order leave no request any tokens; told with the sum, which stays below
+  constexpr long long kBroken = 1ll << 48;
+  const long long before = scan_block(mine + (bad & kBadOffsets ? kBroken : 0ll), s_sums, total) - mine;
+  const bool broken = total >= kBroken;
+  if (broken) total = 0;
   if (blockIdx.x == 0 && bad && p.status) atomicOr(p.status, bad & ~kBadOffsets);
-  const long long before = scan_block(mine, s_sums, total) - mine;
   const long long run = max(quotient(total + a.grid - 1, a.grid), 1ll);
-  const long long x0 = run * blockIdx.x, x1 = min(x0 + run, total);
+  const long long x0 = min(run * blockIdx.x, total), x1 = min(x0 + run, total);
   if (x0 < x1 && x0 >= before && x0 < before + mine) {
     long long at = before;
     for (int b = b0; b < b1; ++b) {
-      const Chunk r = checked(p, raw_of(p, b), bad);
-      const long long cost = cost_of_request(a, r);
+      const Chunk r = per == 1 ? only : checked(p, raw_of(p, b), bad);
+      const long long cost = per == 1 ? mine : cost_of_request(a, r);
       if (x0 < at + cost) {
-        s_walk.b = b;
-        s_walk.r = r;
-        s_walk.left = (int)(x1 - x0);
-        s_in = x0 - at;
+        s_place = Place{x0 - at, b, r};
         break;
       }
       at += cost;
@@ -1026,64 +1064,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (warp == 0) {
-    Walk w = s_walk;
-    __syncwarp();
-    int pieces = 0;
-    if (w.left > 0) {
-      const int blocks = blocks_of(a, w.r);
-      const long long head_cost = cost_before(a, w.r, blocks);
-      w.head = (int)quotient(s_in, head_cost);
-      const long long in = s_in - w.head * head_cost;
-      // the last block that starts at or before `in`: 32 places at a time
-      int lo = 0, hi = blocks;  // it lies in [lo, hi)
-      while (hi - lo > 1) {
-        const int each = (hi - lo + 31) / 32, k = lo + lane * each;
-        const bool at_or_before = k < hi && cost_before(a, w.r, k) <= in;
-        const int n = __popc(__ballot_sync(0xffffffffu, at_or_before));  // lane 0's is
-        lo += (n - 1) * each;
-        hi = min(hi, lo + each);
-      }
-      const long long start = cost_before(a, w.r, lo);
-      const int behind = (int)(in - start);
-      w.block = lo;
-      w.j = max(behind - kSegmentCost, 0);
-      w.lead = max(kSegmentCost - behind, 0);
-      w.buf = 2;
-      w.look_ahead(p);
-      const int np = (end_of(a, w.r, lo) + kTileTokens - 1) / kTileTokens;
-      if (w.j > 0 && w.j + w.left >= np) {  // (of a segment's first step the run is behind .. - j)
-        const int first = (int)quotient(x0 - w.j, run), t = a.block_tokens;
-        if (lane == 0) {
-          Cut cut{};
-          cut.pieces = (int)blockIdx.x - first + 1;
-          cut.first = first;
-          cut.tok = w.r.tok0 + lo * t;
-          cut.tokens = min(w.r.n - lo * t, t);
-          cut.head = w.head;
-          cut.broken = broken;
-          a.cuts[blockIdx.x] = cut;
-        }
-        pieces = 1;
-      }
-    }
-    if (lane == 0) {
-      if (!pieces) a.cuts[blockIdx.x].pieces = 0, a.cuts[blockIdx.x].broken = broken;
-      s_walk = w;
-    }
-  }
-  __syncthreads();
   if (warp < 8) {
     ptx::setmaxnreg_inc<kSoftmaxRegs>();
-    softmax_rows<D, kHalf>(a, c, tmem, warp >> 2);
+    softmax_rows<D, kHalf, kTree>(a, c, tmem, warp >> 2);
   } else {
     ptx::setmaxnreg_dec<kIssueRegs>();
     if (warp == 8)
       stream_kv<D>(&tmk, &tmv, a, c);
     else if (warp == 10)
-      lane == 0 ? list_segments<D>(&tmq, a, c, s_walk) : void();
+      list_segments<D>(&tmq, a, c, start_of_run(a, s_place, x0, x1, run, broken));
     else
-      issue_products<D, kHalf>(c, tmem, warp == 9 ? 0 : 1);
+      issue_products<D, kHalf>(p, c, tmem, warp == 9 ? 0 : 1);
     __syncwarp();
   }
   ptx::tc_fence_before();
@@ -1121,9 +1112,12 @@ __device__ void fill_empty(const ChunkParams& p, bool broken, int thread) {
 }
 
 // ------------------------------------------------------------- merge
-// A warp a row of a segment that was cut; blockIdx.x is the run where it ends.  And
-// the rows that see nothing.
-constexpr int kMergeWarps = 8;
+// A warp four rows of a segment that was cut; blockIdx.x is the run where it ends.
+// And the rows that see nothing.  Bound by the loads that depend on one another
+// (the cut, its pieces' sums, the pieces) and, where many segments are cut, by
+// reading the pieces: 152 of two pieces of 256 rows at d = 128, 80 MB in 10 us (18
+// with one row a warp).
+constexpr int kMergeWarps = 8, kMergeRows = 4;
 
 template <int D, bool kHalf>
 __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const ChunkArgs a) {
@@ -1131,49 +1125,71 @@ __global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const Chu
   const ChunkParams& p = a.p;
   const int lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  fill_empty(p, a.cuts[0].broken, threadIdx.x);
   const Cut cut = a.cuts[blockIdx.x];
-  const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
-  const int in_tile = (row & (kTile - 1)) / p.gqa, tok = (row / kTile) * a.tile_tokens + in_tile;
-  if (cut.pieces == 0 || in_tile >= a.tile_tokens || tok >= cut.tokens) return;
-  auto slot = [&](int k) { return (2ll * (cut.first + k) + (k == 0 ? 1 : 0)) * a.piece_rows + row; };
+  fill_empty(p, a.cuts[0].broken, threadIdx.x);
+  const int row0 = (blockIdx.y * kMergeWarps + (threadIdx.x >> 5)) * kMergeRows;
+  if (cut.pieces == 0 || row0 >= a.piece_rows) return;
+  const auto there = [&](int row) {
+    const int in_tile = (row & (kTile - 1)) / p.gqa;
+    return row < a.piece_rows && in_tile < a.tile_tokens && row / kTile * a.tile_tokens + in_tile < cut.tokens;
+  };
+  const auto slot = [&](int k, int row) { return (2ll * (cut.first + k) + (k == 0 ? 1 : 0)) * a.piece_rows + row; };
+  // lane i has row i & 3 of piece i >> 2, eight pieces at a time
+  const int mine = row0 + (lane & 3);
+  const bool have = there(mine);
+  const auto ml_of = [&](int k) {
+    return have && k < cut.pieces ? a.piece_ml[slot(k, mine)] : make_float2(-INFINITY, 0.f);
+  };
   float m = -INFINITY;
-  for (int k = lane; k < cut.pieces; k += 32) m = fmaxf(m, a.piece_ml[slot(k)].x);
+  for (int k0 = 0; k0 < cut.pieces; k0 += 8) m = fmaxf(m, ml_of(k0 + (lane >> 2)).x);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float l = 0.f, acc[E] = {};
-  for (int k0 = 0; k0 < cut.pieces; k0 += 32) {
-    const int count = min(cut.pieces - k0, 32);
-    float w = 0.f;
-    if (lane < count) {
-      const float2 ml = a.piece_ml[slot(k0 + lane)];
-      w = ml.x == -INFINITY ? 0.f : ptx::ex2(ml.x - m);
-      l = fmaf(w, ml.y, l);
-    }
-#pragma unroll 4
+  for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float l = 0.f, acc[kMergeRows][E] = {};
+  for (int k0 = 0; k0 < cut.pieces; k0 += 8) {
+    const float2 ml = ml_of(k0 + (lane >> 2));
+    const float w = ml.x == -INFINITY ? 0.f : ptx::ex2(ml.x - m);
+    l = fmaf(w, ml.y, l);
+    const int count = min(cut.pieces - k0, 8);
+#pragma unroll 2
     for (int k = 0; k < count; ++k) {
-      const float wk = __shfl_sync(0xffffffffu, w, k);
-      const float* src = a.piece_o + slot(k0 + k) * D + lane * E;
-      float v[E];
-      if constexpr (E == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(src);
-        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(src);
-        v[0] = x.x, v[1] = x.y;
+      float v[kMergeRows][E];
+#pragma unroll
+      for (int r = 0; r < kMergeRows; ++r) {
+        const float* src = a.piece_o + slot(k0 + k, row0 + r) * D + lane * E;
+        if (row0 + r >= a.piece_rows) {  // (rows there in no segment are not read into a result)
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[r][e] = 0.f;
+        } else if constexpr (E == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(src);
+          v[r][0] = x.x, v[r][1] = x.y, v[r][2] = x.z, v[r][3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(src);
+          v[r][0] = x.x, v[r][1] = x.y;
+        }
       }
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(wk, v[e], acc[e]);
+      for (int r = 0; r < kMergeRows; ++r) {
+        const float wk = __shfl_sync(0xffffffffu, w, k * 4 + r);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[r][e] = fmaf(wk, v[r][e], acc[r][e]);
+      }
     }
   }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-  const long long at = (long long)(cut.tok + tok) * p.hq + cut.head * p.gqa + (row & (kTile - 1)) % p.gqa;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + at * D + lane * E);
 #pragma unroll
-  for (int e = 0; e < E; e += 2) dst[e / 2] = pack2<kHalf>(acc[e] * inv, acc[e + 1] * inv);
-  if (lane == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  for (int r = 0; r < kMergeRows; ++r) {
+    const int row = row0 + r;
+    const float inv_r = __shfl_sync(0xffffffffu, inv, r);
+    if (!there(row)) continue;
+    const int in_tile = (row & (kTile - 1)) / p.gqa, tok = row / kTile * a.tile_tokens + in_tile;
+    const long long at = (long long)(cut.tok + tok) * p.hq + cut.head * p.gqa + (row & (kTile - 1)) % p.gqa;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + at * D + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) dst[e / 2] = pack2<kHalf>(acc[r][e] * inv_r, acc[r][e + 1] * inv_r);
+    if (lane == r && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  }
 }
 
 // Sizes of a run, and where its workspace lies.
@@ -1204,6 +1220,7 @@ size_t lay_out(const ChunkParams& p, uint8_t* work, ChunkArgs* a) {
 template <int D, bool kHalf>
 cudaError_t run(const ChunkArgs& a, cudaStream_t s) {
   const ChunkParams& p = a.p;
+  const auto kernel = p.parents ? chunk_tile_kernel<D, kHalf, true> : chunk_tile_kernel<D, kHalf, false>;
   CUtensorMap mq, mk, mv;
   cudaError_t e = make_query_map(&mq, p.q, D, p.hq, p.n_tokens, std::max<long long>(p.q_stride, (long long)p.hq * D),
                                  p.gqa, a.tile_tokens);
@@ -1212,7 +1229,7 @@ cudaError_t run(const ChunkArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = make_page_map(&mv, p.v_pages, D, p.hkv, p.num_pages, true);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(chunk_tile_kernel<D, kHalf>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1220,12 +1237,12 @@ cudaError_t run(const ChunkArgs& a, cudaStream_t s) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Cfg<D>::kSmem;
   cfg.stream = s;
-  e = cudaLaunchKernelEx(&cfg, chunk_tile_kernel<D, kHalf>, mq, mk, mv, a);
+  e = cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, a);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(a.grid, (a.piece_rows + kMergeWarps - 1) / kMergeWarps);
+  cfg.gridDim = dim3(a.grid, (a.piece_rows + kMergeWarps * kMergeRows - 1) / (kMergeWarps * kMergeRows));
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.dynamicSmemBytes = 0;
   cfg.attrs = attr;
