@@ -244,16 +244,30 @@ struct Spot {
 };
 __device__ __noinline__ Spot spot_of(const ChunkArgs& a, const Place& at) {
   const int lane = threadIdx.x & 31, blocks = blocks_of(a, at.r);
-  const long long head_cost = cost_before(a, at.r, blocks);
+  const auto cost_of = [&](int k) {
+    const int end = k < blocks ? end_of(a, at.r, k) : 0;
+    return end > 0 ? (end + kTileTokens - 1) / kTileTokens + kSegmentCost : 0;
+  };
   Spot s;
-  s.head = (int)quotient(at.in, head_cost);
-  const long long in = at.in - s.head * head_cost;
-  if (blocks == 1) {
-    s.block = 0;
-    s.behind = (int)in;
-    s.cost = (int)head_cost;
+  if (blocks <= 32) {  // a block a lane
+    const int cost = cost_of(lane);
+    int behind = cost;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, behind, o);
+      if (lane >= o) behind += x;
+    }
+    const int head_cost = __shfl_sync(0xffffffffu, behind, 31);
+    s.head = (int)quotient(at.in, head_cost);
+    const int in = (int)(at.in - (long long)s.head * head_cost);
+    s.block = __popc(__ballot_sync(0xffffffffu, behind <= in));  // those that end before it
+    s.cost = __shfl_sync(0xffffffffu, cost, s.block);
+    s.behind = in - __shfl_sync(0xffffffffu, behind - cost, s.block);
     return s;
   }
+  const long long head_cost = cost_before(a, at.r, blocks);
+  s.head = (int)quotient(at.in, head_cost);
+  const long long in = at.in - s.head * head_cost;
   // the last block that starts at or before `in`: 32 places at a time
   int lo = 0, hi = blocks;  // it lies in [lo, hi)
   while (hi - lo > 1) {
@@ -265,9 +279,10 @@ __device__ __noinline__ Spot spot_of(const ChunkArgs& a, const Place& at) {
   }
   s.block = lo;
   s.behind = (int)(in - cost_before(a, at.r, lo));
-  s.cost = (end_of(a, at.r, lo) + kTileTokens - 1) / kTileTokens + kSegmentCost;
+  s.cost = cost_of(lo);
   return s;
 }
+
 template <int D>
 struct Cfg {
   static constexpr int kHalves = D / 64;
@@ -778,6 +793,12 @@ __device__ __forceinline__ Mask moved(const Mask& m, int n) {
   return r;
 }
 
+template <int kColumns>
+__device__ __forceinline__ void load_columns(uint32_t tmem, float (&o)[kColumns]) {
+#pragma unroll
+  for (int k = 0; k < kColumns; k += 32) ptx::tmem_ld32(tmem + k, *reinterpret_cast<float(*)[32]>(o + k));
+}
+
 template <int D, bool kHalf, bool kTree>
 __device__ void softmax_rows(const ChunkArgs& a, const Cta<D>& c, uint32_t tmem, int t) {
   using C = Cfg<D>;
@@ -833,8 +854,7 @@ __device__ void softmax_rows(const ChunkArgs& a, const Cta<D>& c, uint32_t tmem,
       ptx::tc_fence_after();
       if (act) {
         float v[128];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) ptx::tmem_ld32(s_tmem + k * 32, *reinterpret_cast<float(*)[32]>(v + k * 32));
+        load_columns(s_tmem, v);
         ptx::tmem_wait_ld();
         const int key0 = (j0 + j) * kTileTokens;
         if (__any_sync(0xffffffffu, clear < key0 + kTileTokens)) {
@@ -933,25 +953,26 @@ __device__ void softmax_rows(const ChunkArgs& a, const Cta<D>& c, uint32_t tmem,
       }
     };
     if (act) {
-      for (int k = c0; k < c0 + columns; k += 32) {
-        float o[32];
-        ptx::tmem_ld32(o_tmem + k, o);
+      constexpr int kChunk = D / 2;
+      for (int k = c0; k < c0 + columns; k += kChunk) {
+        float o[kChunk];
+        load_columns(o_tmem + k, o);
         if (alone) {
           ptx::tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] *= a0;
+          for (int e = 0; e < kChunk; ++e) o[e] *= a0;
         } else {
-          float o2[32];
-          ptx::tmem_ld32(o_other + k, o2);
+          float o2[kChunk];
+          load_columns(o_other + k, o2);
           ptx::tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = fmaf(o2[e], a1, o[e] * a0);
+          for (int e = 0; e < kChunk; ++e) o[e] = fmaf(o2[e], a1, o[e] * a0);
         }
-        if (k + 32 == c0 + columns) o_is_read();
+        if (k + kChunk == c0 + columns) o_is_read();
         if (there && whole) {
           uint16_t* dst = p.out + at * D + k;
 #pragma unroll
-          for (int e = 0; e < 32; e += 16)
+          for (int e = 0; e < kChunk; e += 16)
             ptx::st_global_v8(dst + e, pack2<kHalf>(o[e], o[e + 1]), pack2<kHalf>(o[e + 2], o[e + 3]),
                               pack2<kHalf>(o[e + 4], o[e + 5]), pack2<kHalf>(o[e + 6], o[e + 7]),
                               pack2<kHalf>(o[e + 8], o[e + 9]), pack2<kHalf>(o[e + 10], o[e + 11]),
@@ -959,7 +980,7 @@ __device__ void softmax_rows(const ChunkArgs& a, const Cta<D>& c, uint32_t tmem,
         } else if (there) {
           float* dst = a.piece_o + slot * D + k;
 #pragma unroll
-          for (int e = 0; e < 32; e += 8)
+          for (int e = 0; e < kChunk; e += 8)
             ptx::st_global_v8(dst + e, __float_as_uint(o[e]), __float_as_uint(o[e + 1]), __float_as_uint(o[e + 2]),
                               __float_as_uint(o[e + 3]), __float_as_uint(o[e + 4]), __float_as_uint(o[e + 5]),
                               __float_as_uint(o[e + 6]), __float_as_uint(o[e + 7]));
