@@ -340,9 +340,7 @@ struct Cta {
 // tiles::wait with this kernel's abort flag and status word.
 template <int kRole, int D>
 __device__ __forceinline__ bool wait(const Cta<D>& c, int32_t* status, uint32_t bar, uint32_t parity) {
-  bool ok = ptx::mbar_try_wait(bar, parity);
-  if (!ok) ok = tiles::wait_slow<kRole>(bar, parity, c.abort_flag(), status);
-  return __all_sync(0xffffffffu, ok);
+  return tiles::wait<kRole>(bar, parity, c.abort_flag(), status);
 }
 
 // Copies issued, counted.  A reader that does not use every entry of a ring cannot
@@ -1085,6 +1083,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  Walk walk{};
+  if (warp == 10) walk = start_of_run(a, s_place, x0, x1, run, broken);  // (its calls need the registers of the launch)
   if (warp < 8) {
     ptx::setmaxnreg_inc<kSoftmaxRegs>();
     softmax_rows<D, kHalf, kTree>(a, c, tmem, warp >> 2);
@@ -1093,7 +1093,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8)
       stream_kv<D>(&tmk, &tmv, a, c);
     else if (warp == 10)
-      list_segments<D>(&tmq, a, c, start_of_run(a, s_place, x0, x1, run, broken));
+      list_segments<D>(&tmq, a, c, walk);
     else
       issue_products<D, kHalf>(p, c, tmem, warp == 9 ? 0 : 1);
     __syncwarp();

@@ -38,15 +38,19 @@
 #include "kernels.h"
 #include "prefix_attn.h"
 #include "ptx.cuh"
+#include "tiles.cuh"
 
 namespace ta {
 namespace {
+
+using tiles::drain_wait;
+using tiles::pack2;
+using tiles::rescale_o;
 
 constexpr int kThreads = 384;
 constexpr int kSoftmaxRegs = 224, kIssueRegs = 56;
 static_assert(256 * kSoftmaxRegs + 128 * kIssueRegs <= kThreads * 168, "register split too large");
 constexpr float kRescaleLog2 = 8.f;  // O is rescaled when a row's maximum grows by more than 2^8
-constexpr long long kWaitLimitNs = 2000000000ll, kDrainLimitNs = 200000000ll;
 constexpr uint32_t kTmemCols = 512;  // S of both tiles (128 columns each), O of both (128 each)
 constexpr int kStepPages = kTileTokens / kPage;
 
@@ -85,36 +89,10 @@ struct Cta {
   __device__ uint32_t stage(int s) const { return base + C::kOffStage + s * C::kStageBytes; }
 };
 
-// Out of line, once per register split: a call must match its caller's.
-template <int kRole>
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                       int32_t* status) {
-  if (*abort_flag) return false;
-  const uint64_t t0 = ptx::globaltimer();
-  for (uint32_t n = 1;; ++n) {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
-    if ((n & 15) == 0) {
-      if (*abort_flag) return false;
-      if ((long long)(ptx::globaltimer() - t0) > kWaitLimitNs) {
-        *abort_flag = 1;
-        if (status) atomicOr(status, kBatchTimeout);
-        return false;
-      }
-    }
-  }
-}
-// True once the phase is complete; false when the CTA has given up.  The same
-// in all lanes of the warp.
+// tiles::wait with this CTA's abort flag and status word.
 template <int kRole, int D>
 __device__ __forceinline__ bool wait(const Cta<D>& c, uint32_t bar, uint32_t parity) {
-  bool ok = ptx::mbar_try_wait(bar, parity);
-  if (!ok) ok = wait_slow<kRole>(bar, parity, c.abort_flag, c.status);
-  return __all_sync(0xffffffffu, ok);
-}
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = ptx::globaltimer();
-  while (!ptx::mbar_try_wait(bar, parity))
-    if ((long long)(ptx::globaltimer() - t0) > kDrainLimitNs) return;
+  return tiles::wait<kRole>(bar, parity, c.abort_flag, c.status);
 }
 
 // The CTA's run, segment by segment: kv head, row block, steps [j0, j1) of n.
@@ -332,26 +310,6 @@ __device__ __forceinline__ void load_q(const uint16_t* src, bool there, uint32_t
                     reinterpret_cast<const uint16_t*>(s) + ch * 8, h ? 16u : 0u);
   }
   ptx::cp_async_commit();
-}
-
-template <bool kHalf>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  if constexpr (kHalf) return ptx::pack_f16(lo, hi);
-  return ptx::pack_bf16(lo, hi);
-}
-
-template <int D>
-__device__ __noinline__ void rescale_o(uint32_t o, float alpha) {
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c) {
-    float v[32];
-    ptx::tmem_ld32(o + c * 32, v);
-    ptx::tmem_wait_ld();
-#pragma unroll
-    for (int e = 0; e < 32; ++e) v[e] *= alpha;
-    ptx::tmem_st32(o + c * 32, v);
-  }
-  ptx::tmem_wait_st();
 }
 
 template <int D, bool kHalf>

@@ -1,5 +1,5 @@
-// What the kernels of 128-row attention tiles on tcgen05 share: bounded waits,
-// the query tile's layout, the accumulator's rescaling.
+// What the kernels of 128-row attention tiles on tcgen05 share: bounded waits, the
+// weights' rounding, the accumulator's rescaling.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -32,45 +32,18 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
     }
   }
 }
-// True once the phase is complete; false when the CTA (its abort_flag) has given
-// up.  The same in all lanes of the warp.
-template <int kRole, class Cta>
-__device__ __forceinline__ bool wait(const Cta& c, uint32_t bar, uint32_t parity) {
+// True once the phase is complete; false when the CTA has given up.  The same in
+// all lanes of the warp.
+template <int kRole>
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
   bool ok = ptx::mbar_try_wait(bar, parity);
-  if (!ok) ok = wait_slow<kRole>(bar, parity, c.abort_flag, c.status);
+  if (!ok) ok = wait_slow<kRole>(bar, parity, abort_flag, status);
   return __all_sync(0xffffffffu, ok);
-}
-// The same for a role of one thread.
-template <int kRole, class Cta>
-__device__ __forceinline__ bool wait_one(const Cta& c, uint32_t bar, uint32_t parity) {
-  return ptx::mbar_try_wait(bar, parity) || wait_slow<kRole>(bar, parity, c.abort_flag, c.status);
 }
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = ptx::globaltimer();
   while (!ptx::mbar_try_wait(bar, parity))
     if ((long long)(ptx::globaltimer() - t0) > kDrainLimitNs) return;
-}
-
-__device__ __forceinline__ uint32_t sw128(int row, int chunk) {
-  return row * 128 + ((chunk ^ (row & 7)) << 4);
-}
-
-// Copies a tile's query rows (zeros past the last) into the swizzled buffer: a
-// warp its own 32 rows, whole rows per instruction.
-template <int D>
-__device__ __forceinline__ void load_q(const uint16_t* src, bool there, uint32_t q, int tid) {
-  constexpr int kChunks = D / 8, kPer = 32 / kChunks;
-  const int lane = tid & 31, ch = lane % kChunks;
-  const unsigned long long at = reinterpret_cast<unsigned long long>(src);
-#pragma unroll
-  for (int k = 0; k < 32 / kPer; ++k) {
-    const int r = k * kPer + lane / kChunks;
-    const unsigned long long s = __shfl_sync(0xffffffffu, at, r);
-    const int h = __shfl_sync(0xffffffffu, (int)there, r);
-    ptx::cp_async16(q + (ch >> 3) * (128 * 128) + sw128((tid & ~31) + r, ch & 7),
-                    reinterpret_cast<const uint16_t*>(s) + ch * 8, h ? 16u : 0u);
-  }
-  ptx::cp_async_commit();
 }
 
 template <bool kHalf>
