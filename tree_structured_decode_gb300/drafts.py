@@ -112,6 +112,24 @@ def accept_drafts(drafted, parents, cu_new, sampled, status=None, stream=None):
     return path, kept, following, back
 
 
+def _layers(k_pages, v_pages, index):
+    """(layers, pages, kv heads, d, elements from one layer's pool to the next) of a pool or of all layers' pools, checked."""
+    if k_pages.dim() != 5:
+        pages, hkv, _, d = _pools(k_pages, v_pages, index)
+        return 1, pages, hkv, d, 0
+    shape = k_pages.shape
+    if v_pages.shape != shape or v_pages.stride() != k_pages.stride():
+        raise ValueError(f"v_pages must be as k_pages, {tuple(shape)}")
+    layers = _int32("the number of layers", shape[0])
+    if layers == 0:
+        return 0, 0, 0, 0, 0
+    pages, hkv, _, d = _pools(k_pages[0], v_pages[0], index)
+    between = k_pages.stride(0)
+    if layers > 1 and between < pages * hkv * 16 * d:
+        raise ValueError("the layers' pools must lie one behind another")
+    return layers, pages, hkv, d, between if layers > 1 else 0
+
+
 def keep_drafts(path, cu_new, block_table, lens, k_pages, v_pages, status=None, stream=None):
     """``tree_attn_keep_drafts``: move the kept nodes' keys and values together, in place.
 
@@ -120,18 +138,9 @@ def keep_drafts(path, cu_new, block_table, lens, k_pages, v_pages, status=None, 
     import torch
 
     index, kind = _index("k_pages", k_pages), torch.int32
-    if k_pages.dim() == 5:
-        if v_pages.shape != k_pages.shape or v_pages.stride() != k_pages.stride():
-            raise ValueError(f"v_pages must be as k_pages, {tuple(k_pages.shape)}")
-        layers = _int32("the number of layers", k_pages.shape[0])
-        k0, v0, between = (k_pages[0], v_pages[0], k_pages.stride(0)) if layers else (k_pages, v_pages, 0)
-        if not layers:
-            return
-    else:
-        layers, k0, v0, between = 1, k_pages, v_pages, 0
-    pages, hkv, _, d = _pools(k0, v0, index)
-    if layers > 1 and between < k0.numel():
-        raise ValueError("the layers' pools must lie one behind another")
+    layers, pages, hkv, d, between = _layers(k_pages, v_pages, index)
+    if layers == 0:
+        return
     b = _int32("lens' length", lens.numel())
     t = _int32("path's length", path.numel())
     table, stride, width = _table(block_table, b, index, kind)
@@ -141,8 +150,8 @@ def keep_drafts(path, cu_new, block_table, lens, k_pages, v_pages, status=None, 
     context, handle = _launch_on(index, stream)
     with context:
         check(load_library().tree_attn_keep_drafts(
-            path_at, cu_at, lens_at, table, stride, width, b, t, k0.data_ptr(), v0.data_ptr(), between if layers > 1 else 0,
-            layers, pages, hkv, d, status_at, handle), "tree_attn_keep_drafts")
+            path_at, cu_at, lens_at, table, stride, width, b, t, k_pages.data_ptr(), v_pages.data_ptr(), between, layers, pages, hkv,
+            d, status_at, handle), "tree_attn_keep_drafts")
 
 
 def token_logprobs(logits, tokens=None, temperature=1.0, top=0, stream=None):
