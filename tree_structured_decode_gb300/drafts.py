@@ -103,9 +103,11 @@ def accept_drafts(drafted, parents, cu_new, sampled, status=None, stream=None):
     status_at = None if status is None else _vector("status", status, 1, index, kind)
     context, handle = _launch_on(index, stream)
     with context:
-        path = torch.empty(t, dtype=kind, device=drafted.device)
-        each = torch.empty((3, b), dtype=kind, device=drafted.device)
-        kept, following, back = each.unbind(0)
+        device = drafted.device
+        path = torch.empty(t, dtype=kind, device=device)
+        kept = torch.empty(b, dtype=kind, device=device)
+        following = torch.empty(b, dtype=kind, device=device)
+        back = torch.empty(b, dtype=kind, device=device)
         check(load_library().tree_attn_accept_drafts(
             at[0], at[1], cu_at, at[2], b, t, path.data_ptr(), kept.data_ptr(), following.data_ptr(), back.data_ptr(),
             status_at, handle), "tree_attn_accept_drafts")
