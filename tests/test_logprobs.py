@@ -135,6 +135,24 @@ def test_ties_go_to_the_lowest_index():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("copies,top", [(1, 8), (1, 64), (300, 8), (300, 64)])
+def test_rows_that_rise(copies, top, dtype):
+    """The largest come last, in pieces of many sizes: what lies above the largest so far is few, many, all."""
+    vocab = 40000
+    i = torch.arange(vocab)
+    noise = torch.randn((4, vocab), generator=torch.Generator().manual_seed(top))
+    x = torch.stack([i * 1e-3, (i // 3000) * 1.5 + noise[0], torch.where(i % 2048 < 40, i * 2e-3, noise[1]),
+                     torch.where((i > 9000) & (i < 17000), 8 + noise[2], noise[2]), torch.where(i > vocab - 1500, 9 + noise[3], noise[3])])
+    x = x.to(TYPES[dtype])
+    given = [[0, vocab - 1]] * len(x)
+    got = run(x.repeat(copies, 1), given * copies, 1.3, top)
+    check(x, given, 1.3, top, [g[:len(x)] for g in got])
+    for g in got:  # (other rows at other alignments of the grid, the same sums)
+        assert torch.equal(g.reshape(copies, -1), g[:len(x)].reshape(1, -1).expand(copies, -1))
+
+
+@pytest.mark.gpu
 def test_largest_values():
     big = torch.finfo(torch.float32).max
     x = torch.zeros((3, 5000))

@@ -9,11 +9,13 @@
 // no term is negative, so nothing cancels.  Sums are in 32 bits, a thread's of its
 // own 1/128 or less of a row, then a tree.
 //
-// The likeliest k: a list in shared memory takes every logit above a threshold,
-// which rises to the list's k-th whenever the list has grown long (all compared
-// with all).  Where a round's logits would overflow it (the first round's always
-// do), the k-th largest of the threads' largest is a threshold that lets at most
-// k times a thread's part through.  Order is by (logit, index), one 64-bit key.
+// The likeliest k: a thread whose round's largest logit is above a threshold notes
+// the round's logits in shared memory.  When many are noted, those of the k threads
+// with the largest (no others can hold one) join a list of the k best so far, by
+// all-with-all comparison, whose last is the next threshold.  The first threshold
+// is taken from the lanes' largest.  Order is by (logit, index), one 64-bit key.
+// (Logits put in the list one by one, where they are found: 70 us instead of 57 at
+// 1664 rows of 50257 bf16, k = 8.)
 //
 // A row belongs to a CTA, or to a cluster of up to eight where rows are few; their
 // sums and lists meet in the first one's shared memory.
@@ -108,15 +110,23 @@ __device__ __forceinline__ Sums joined_warp(Sums x, float c) {
   return x;
 }
 
-// A list of at most kRoom keys.
+// The likeliest so far, and what has come above them since.
 template <int kThreads, int kGroup>
 struct List {
-  // what is kept of it, and the logits of the threads that a threshold lets through
-  static constexpr int kRoom = kMaxTop + kMaxTop * kGroup;
+  static constexpr int kRoom = kMaxTop + kMaxTop * kGroup;  // what is kept, and the logits of k threads
+  // threads noted before the list is made anew (8: 60 us at 1664 rows, k = 8, and 91 at
+  // 1216, k = 64; 32: 57 and 80; 64 takes 1 and 4 % more)
+  static constexpr int kLook = 32;
+  struct __align__(16) Noted {
+    float x[kLook + kThreads][kGroup];  // (a round adds one a thread)
+    u64 most[kLook + kThreads];         // the largest of them
+    int index[kLook + kThreads];        // of the first of them
+    int n;
+  } noted;
   u64 key[kRoom];
-  u64 best[kThreads > kMaxCluster * kMaxTop ? kThreads : kMaxCluster * kMaxTop];
-  u64 threshold;  // keys up to it are left out
-  int n, before;
+  u64 best[kMaxCluster * kMaxTop];
+  u64 threshold;  // keys up to it are left out; 0: fewer than k are known
+  int n;
 };
 
 // The k largest of from[0..n) to to[0..k), in order (0 where there are fewer).
@@ -132,10 +142,55 @@ __device__ __forceinline__ void select_largest(const u64* from, int n, u64* to, 
   }
 }
 
+// The noted threads' logits join the list.
+template <int kThreads, int kVec, int kGroup>
+__device__ __forceinline__ void add_noted(List<kThreads, kGroup>& s, int k) {
+  const int tid = threadIdx.x, n = s.noted.n;
+  const auto index = [&](int from, int e) {
+    return s.noted.index[from] + (e / kVec) * (kThreads * kVec) + e % kVec;
+  };
+  for (int i = tid; i < n; i += kThreads) {
+    float most = s.noted.x[i][0];
+    int first = 0;
+#pragma unroll
+    for (int e = 1; e < kGroup; ++e)
+      if (s.noted.x[i][e] > most) most = s.noted.x[i][e], first = e;
+    s.noted.most[i] = key_at(most, index(i, first));
+  }
+  __syncthreads();
+  if (n > k) {  // the k-th of the threads' largest is reached by k logits, and by k threads only
+    for (int i = tid; i < n; i += kThreads) {
+      const u64 mine = s.noted.most[i];
+      int above = 0;
+      for (int j = 0; j < n; ++j) above += s.noted.most[j] > mine;
+      if (above == k - 1 && mine - 1 > s.threshold) s.threshold = mine - 1;
+    }
+    __syncthreads();
+  }
+  const u64 low = s.threshold;
+  for (int i = tid; i < n * kGroup; i += kThreads) {
+    const int from = i / kGroup, e = i % kGroup;
+    if (s.noted.most[from] <= low) continue;
+    const float x = s.noted.x[from][e];
+    const u64 key = key_at(x, index(from, e));
+    if (x > -INFINITY && key > low) s.key[atomicAdd(&s.n, 1)] = key;
+  }
+  __syncthreads();
+  const int have = s.n;
+  if (have > k) {
+    select_largest<kThreads>(s.key, have, s.best, k);
+    __syncthreads();
+    for (int i = tid; i < k; i += kThreads) s.key[i] = s.best[i];
+    if (tid == 0) s.n = k, s.threshold = s.best[k - 1];
+  }
+  if (tid == 0) s.noted.n = 0;
+  __syncthreads();
+}
+
 template <class T, int kThreads, bool kTop>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) scores_kernel(const ScoreParams p) {
   constexpr int kVec = Type<T>::kVec, kVectors = Type<T>::kVectors, kGroup = kVectors * kVec;
-  constexpr int kWarps = kThreads / 32;
+  constexpr int kWarps = kThreads / 32, kRound = kVectors * kThreads;
   using Keys = List<kThreads, kGroup>;
   __shared__ Keys s_list;
   __shared__ Sums s_sums[kWarps], s_rank[kMaxCluster];
@@ -192,14 +247,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) scores_kernel(const
   const float given_x = given_i >= 0 ? (float)row[given_i] : 0.f;
 
   if (kTop) {
-    if (tid == 0) s_list.n = 0, s_list.threshold = 0, s_list.before = INT32_MAX;
+    if (tid == 0) s_list.n = 0, s_list.threshold = 0, s_list.noted.n = 0;
     __syncthreads();
   }
   Sums sum{kLowest, 0.f, 0.f};
   const uint64_t c2 = ptx::f2(c, c);
   uint4 ahead[kVectors];
   load(v0, ahead);
-  for (int at = v0; at < v1; at += kVectors * kThreads) {
+  for (int at = v0; at < v1; at += kRound) {
     float x[kGroup];
 #pragma unroll
     for (int u = 0; u < kVectors; ++u) {
@@ -207,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) scores_kernel(const
 #pragma unroll
       for (int e = 0; e < 4; ++e) Type<T>::split(w[e], x + u * kVec + e * (kVec / 4));
     }
-    if (at + kVectors * kThreads < v1) load(at + kVectors * kThreads, ahead);
+    if (at + kRound < v1) load(at + kRound, ahead);
     float most = x[0];
 #pragma unroll
     for (int e = 1; e + 1 < kGroup; e += 2) most = ptx::max3(most, x[e], x[e + 1]);
@@ -237,10 +292,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) scores_kernel(const
       sum.h -= a + b;
     }
     if (kTop && k > 0) {
-      const auto index = [&](int e) { return (at + (e / kVec) * kThreads + tid) * kVec - shift + e % kVec; };
       u64 low = s_list.threshold;
-      int room = 2 * k + 32;  // a longer list is worth a pass
-      if (!low) {  // none yet: of each warp's lanes the m-th largest, of these the least, has k logits at or above it
+      const bool open = !low;
+      if (open) {  // of each warp's lanes the m-th largest, of these the least, has k threads' largest at or above it
         uint32_t left = key_of(most), mth = 0;
         for (int m = (k + kWarps - 1) / kWarps; m > 0; --m) {
           mth = __reduce_max_sync(0xffffffffu, left);
@@ -254,64 +308,20 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) scores_kernel(const
         if (of_key(mth) > -INFINITY) {
           low = ((u64)mth << 32) - 1;
           if (tid == 0) s_list.threshold = low;  // (read again behind a barrier)
-          room = k;
         }
       }
-      const auto push = [&]() {  // true where the list has become long
-        const float least = low ? of_key((uint32_t)((low + 1) >> 32)) : kLowest;
-        bool longer = false;
-        if (most >= least) {
-          uint32_t hits = 0;
+      // (what equals the k-th of earlier rounds comes behind it)
+      const float least = low ? of_key((uint32_t)((low + 1) >> 32)) : kLowest;
+      bool many = open;
+      if (open ? most >= least : most > least) {
+        const int to = atomicAdd(&s_list.noted.n, 1);
+        s_list.noted.index[to] = (at + tid) * kVec - shift;
 #pragma unroll
-          for (int e = 0; e < kGroup; ++e) hits |= (uint32_t)(x[e] >= least) << e;
-#pragma unroll
-          for (int e = 0; e < kGroup; ++e)
-            if (hits >> e & 1) {
-              const u64 key = key_at(x[e], index(e));
-              if (key > low) {
-                const int to = atomicAdd(&s_list.n, 1);
-                if (to < Keys::kRoom) s_list.key[to] = key;
-                longer |= to >= room;
-              }
-            }
-        }
-        return longer;
-      };
-      const int before = s_list.n;  // with what others have pushed in this round: the least of all is before it
-      if (__syncthreads_or(push())) {
-        const bool over = s_list.n > Keys::kRoom;
-        if (over) atomicMin(&s_list.before, before);
-        __syncthreads();
-        const int n = over ? s_list.before : s_list.n;
-        if (n > k) {
-          select_largest<kThreads>(s_list.key, n, s_list.best, k);
-          __syncthreads();
-          for (int i = tid; i < k; i += kThreads) s_list.key[i] = s_list.best[i];
-          if (tid == 0) s_list.n = k, s_list.threshold = s_list.best[k - 1];
-        } else {
-          __syncthreads();
-          if (tid == 0) s_list.n = n;
-        }
-        __syncthreads();
-        if (over) {  // this round's go again, with a threshold that they fit behind
-          u64 mine = 0;
-#pragma unroll
-          for (int e = 0; e < kGroup; ++e) {
-            const u64 key = x[e] > -INFINITY ? key_at(x[e], index(e)) : 0;
-            mine = key > mine ? key : mine;
-          }
-          s_list.best[tid] = mine;
-          __syncthreads();
-          int above = 0;
-          for (int j = 0; j < kThreads; ++j) above += s_list.best[j] > mine;
-          if (above == k - 1 && mine && mine - 1 > s_list.threshold) s_list.threshold = mine - 1;
-          if (tid == 0) s_list.before = INT32_MAX;
-          __syncthreads();
-          low = s_list.threshold;
-          push();
-          __syncthreads();
-        }
+        for (int e = 0; e < kGroup; e += 4)
+          *reinterpret_cast<float4*>(s_list.noted.x[to] + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        many |= to + 1 >= Keys::kLook;
       }
+      if (__syncthreads_or(many || at + kRound >= v1)) add_noted<kThreads, kVec, kGroup>(s_list, k);
     }
   }
 
@@ -406,11 +416,11 @@ cudaError_t pick(const ScoreParams& p, cudaStream_t s) {
   // a row whose temperature is not above 0 needs its largest logit's place
   const bool top = p.top > 0 || p.temperature || !(p.temperature_all > 0.f);
   const long long bytes = (long long)p.vocab * sizeof(T);
-  // Half the threads where rows are short, or so many that eight of their CTAs share
-  // an SM: 2048 rows of 128000 fp32 logits take 153 us (160 with 256 threads), 1664
-  // of 50257 bf16 with 8 alternatives 70 (72), but with 64 130 (118), whose first
-  // list comes from twice the logits then; 272 rows of 28510, all at once, 9.9 (7.4).
-  if (bytes <= 8192 || (p.rows >= 8 * p.num_sms && p.top <= 32)) return run<T, 128>(p, top, 1, s);
+  // Half the threads where rows are short, or too many for all their CTAs of 256 to be
+  // on the SMs at once: 900 rows of 50257 bf16 with 8 alternatives take 32 us (with 256
+  // threads 37), 1664 58 (61), with 64 110 (108), 2048 rows of 128000 fp32 151 (158),
+  // with 8 186 (174); 272 rows of 28510, all at once either way, 18 (13).
+  if (bytes <= 8192 || p.rows > 4 * p.num_sms) return run<T, 128>(p, top, 1, s);
   // Few rows are split until every SM has two parts or the parts are short.
   int ranks = 1;
   while (ranks < kMaxCluster && (long long)p.rows * ranks * 2 <= 2 * p.num_sms && bytes / ranks > 16384) ranks *= 2;
