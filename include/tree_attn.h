@@ -419,7 +419,8 @@ tree_attn_status tree_attn_append_slots(const void* k_new, const void* v_new, in
  * Made for the few queries that a request has in a decode step.  A chunk of a
  * prompt is accepted, and its prefix is as fast; its own keys are read once
  * for every 16 query rows of a kv head, and the workspace holds its output
- * twice in 32 bits.
+ * twice in 32 bits.  For prompts and larger trees of drafts there is
+ * tree_attn_chunk_run().
  * A row that sees no key, and every token at or past cu_new[n_requests], gets
  * out = 0 and lse = -inf.  Slots past a request's end may hold anything; those
  * of its tokens that a query does not see (later drafts) must be finite.  A

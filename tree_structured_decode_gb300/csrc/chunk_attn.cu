@@ -35,6 +35,15 @@
 // in the order of issue, so S of its next task may be issued right behind the P V
 // that still reads P from the same columns.
 //
+// Measured (d = 128, 64 q heads on 8): a prompt of 16384 tokens in 3.05 ms, 1440
+// TFLOP/s, 0.74 of the measured bf16 peak and 0.84 of what it sustains.  A pair of
+// tasks takes about 2900 cycles where its products take 2048: S, softmax and P V of
+// one half follow one another, and two halves cover each other only in part (P
+// handed over in two parts: 3200 us; two threads a row: 3560).  26 drafts behind
+// 500 to 4000 tokens (64 requests, 32 heads on 8, 458 MB) in 110 us: 4.1 TB/s in
+// all, about 6 while K and V stream; the rest is the start, runs that do not end
+// together, and the merge.
+//
 // Every wait has a limit.  One that runs out sets the status word's timeout bit
 // and the CTA's abort flag; every role then stops issuing, waits (with a limit)
 // for its copies or products in flight, and the CTA frees its TMEM and returns.
@@ -66,7 +75,9 @@ constexpr uint32_t kTmemCols = 512;  // S of both tiles (128 columns each), O of
 constexpr int kTile = 128;           // query rows of a tile, at most
 constexpr int kTurnTries = 1 << 24;  // a second or so
 constexpr long long kIdleLimitNs = 20000000000ll;  // without a segment to list or queries to bring
-constexpr int kSegmentCost = 2;      // what a segment costs beside its steps, in steps
+// What a segment costs beside its steps, in steps (24 packed prompts took 166 us
+// with 2, 176 with 1, 172 with 3).
+constexpr int kSegmentCost = 2;
 constexpr int kStepPages = kTileTokens / kPage;
 
 struct Cut {  // a segment that lies in several runs, told by the run where it ends
@@ -1006,7 +1017,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Cta<D> c{};
   uint8_t* const smem = chunk_smem;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::kOffWords);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   Place& s_place = *reinterpret_cast<Place*>(smem + C::kOffPlace);
   long long* s_sums = reinterpret_cast<long long*>(smem + C::kOffMl);  // (before it holds anything else)
   if (c.base() & 1023) {  // the swizzled layouts need it

@@ -118,13 +118,15 @@ struct List {
   // 1216, k = 64; 32: 57 and 80; 64 takes 1 and 4 % more)
   static constexpr int kLook = 32;
   struct __align__(16) Noted {
-    float x[kLook + kThreads][kGroup];  // (a round adds one a thread)
+    union {
+      float x[kLook + kThreads][kGroup];  // (a round adds one a thread)
+      u64 best[kMaxCluster * kMaxTop];    // selected ones, when the logits have been looked at
+    };
     u64 most[kLook + kThreads];         // the largest of them
     int index[kLook + kThreads];        // of the first of them
     int n;
   } noted;
   u64 key[kRoom];
-  u64 best[kMaxCluster * kMaxTop];
   u64 threshold;  // keys up to it are left out; 0: fewer than k are known
   int n;
 };
@@ -178,10 +180,10 @@ __device__ __forceinline__ void add_noted(List<kThreads, kGroup>& s, int k) {
   __syncthreads();
   const int have = s.n;
   if (have > k) {
-    select_largest<kThreads>(s.key, have, s.best, k);
+    select_largest<kThreads>(s.key, have, s.noted.best, k);
     __syncthreads();
-    for (int i = tid; i < k; i += kThreads) s.key[i] = s.best[i];
-    if (tid == 0) s.n = k, s.threshold = s.best[k - 1];
+    for (int i = tid; i < k; i += kThreads) s.key[i] = s.noted.best[i];
+    if (tid == 0) s.n = k, s.threshold = s.noted.best[k - 1];
   }
   if (tid == 0) s.noted.n = 0;
   __syncthreads();
@@ -336,12 +338,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) scores_kernel(const
   }
   if (kTop) {
     __syncthreads();
-    select_largest<kThreads>(s_list.key, s_list.n, s_list.best, k);
+    select_largest<kThreads>(s_list.key, s_list.n, s_list.noted.best, k);
     __syncthreads();
     if (ranks > 1) {  // (the first one's keys are its own list's until all have been ranked)
       u64* to = cluster.map_shared_rank(s_list.key, 0);
       cluster.sync();
-      for (int i = tid; i < k; i += kThreads) to[rank * k + i] = s_list.best[i];
+      for (int i = tid; i < k; i += kThreads) to[rank * k + i] = s_list.noted.best[i];
     }
   }
   if (ranks > 1)
@@ -350,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) scores_kernel(const
     __syncthreads();
   if (rank) return;
   if (kTop && ranks > 1) {
-    select_largest<kThreads>(s_list.key, ranks * k, s_list.best, k);
+    select_largest<kThreads>(s_list.key, ranks * k, s_list.noted.best, k);
   }
   Sums all = s_rank[0];
   for (int i = 1; i < ranks; ++i) all = joined(all, s_rank[i], c);
@@ -373,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) scores_kernel(const
   }
   __syncthreads();
   if (infinite) all = Sums{INFINITY, (float)infinite, 0.f};
-  const int first = kTop ? (int)~(uint32_t)s_list.best[0] : 0;
+  const int first = kTop ? (int)~(uint32_t)s_list.noted.best[0] : 0;
   const float log_s = greedy ? 0.f : log2f(all.s) * kLn2;
   const auto logprob = [&](float x, int i) {
     if (broken) return NAN;
@@ -387,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) scores_kernel(const
   }
   if (kTop)
     for (int e = tid; e < p.top; e += kThreads) {
-      const u64 key = s_list.best[e];
+      const u64 key = s_list.noted.best[e];
       const long long to = (long long)r * p.top + e;
       p.top_tokens[to] = broken || !key ? -1 : (int)~(uint32_t)key;
       p.top_logprobs[to] = broken ? NAN : key ? logprob(of_key((uint32_t)(key >> 32)), (int)~(uint32_t)key) : -INFINITY;
@@ -419,7 +421,8 @@ cudaError_t pick(const ScoreParams& p, cudaStream_t s) {
   // Half the threads where rows are short, or too many for all their CTAs of 256 to be
   // on the SMs at once: 900 rows of 50257 bf16 with 8 alternatives take 32 us (with 256
   // threads 37), 1664 58 (61), with 64 110 (108), 2048 rows of 128000 fp32 151 (158),
-  // with 8 186 (174); 272 rows of 28510, all at once either way, 18 (13).
+  // with 8 172 (174); 272 rows of 28510, all at once either way, 18 (13).  (64 threads:
+  // 1664 rows 56, but 900 46 and with 64 alternatives 161.)
   if (bytes <= 8192 || p.rows > 4 * p.num_sms) return run<T, 128>(p, top, 1, s);
   // Few rows are split until every SM has two parts or the parts are short.
   int ranks = 1;
