@@ -504,7 +504,7 @@ tree_attn_status tree_attn_sample(const void* logits, int64_t stride, int32_t dt
  * its pages already: a prompt or a chunk of one, or a tree of drafted tokens.
  *   q, q_stride, k_pages, v_pages, num_pages, block_table, table_stride,
  *   table_width, dtype, softmax_scale, out, lse
- *                  as in tree_attn_prefix_run().
+ *                  as in tree_attn_prefix_run(); out 32-byte aligned.
  *   lens           tokens of each request, this step's among them.
  *   cu_new[n_requests+1]   request b's n new tokens are [cu_new[b],
  *                  cu_new[b+1]), its last n; NULL: one each, n_tokens ==

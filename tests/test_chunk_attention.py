@@ -373,6 +373,10 @@ def test_refusals(kw, name):
     assert _abi.load_library().tree_attn_last_error()
 
 
+def test_outputs_off_32_bytes_are_refused():
+    assert _abi.STATUS_NAMES[_run(out=272)] == "TA_ERR_ALIGNMENT"  # (rows are written 32 bytes at a time)
+
+
 def test_workspace_of_nothing():
     f, n = _abi.load_library().tree_attn_chunk_workspace, ctypes.c_size_t(0)
     assert f(0, 0, 8, 2, 128, ctypes.byref(n)) == _abi.TA_OK and n.value == 0

@@ -83,9 +83,9 @@ tree_attn_status tree_attn_chunk_run(const void* q, int64_t q_stride, const void
       return fail(TA_ERR_INVALID_ARG, "q, out, the pools, lens and block_table must be non-NULL");
     if (n_tokens > 1 && q_stride < (int64_t)n_q_heads * head_dim)
       return fail(TA_ERR_INVALID_ARG, "q_stride must be at least n_q_heads * head_dim");
-    if (off(q, 16) || off(k_pages, 16) || off(v_pages, 16) || off(out, 16) || q_stride % 8)
+    if (off(q, 16) || off(k_pages, 16) || off(v_pages, 16) || off(out, 32) || q_stride % 8)
       return fail(TA_ERR_ALIGNMENT,
-                  "q, out and the pools must be 16-byte aligned, q_stride a multiple of 8 elements");
+                  "q and the pools must be 16-byte aligned, out 32-byte, q_stride a multiple of 8 elements");
     if (off(block_table, 4) || off(lens, 4) || off(cu_new, 4) || off(parents, 4) || off(lse, 4) ||
         off(status, 4))
       return fail(TA_ERR_ALIGNMENT, "int32 and fp32 buffers must be 4-byte aligned");
