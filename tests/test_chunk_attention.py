@@ -377,6 +377,11 @@ def test_outputs_off_32_bytes_are_refused():
     assert _abi.STATUS_NAMES[_run(out=272)] == "TA_ERR_ALIGNMENT"  # (rows are written 32 bytes at a time)
 
 
+def test_tables_of_nearly_2_31_tokens_are_refused():
+    # the last step's keys, 128 and its pages' more, must be countable in 32 bits
+    assert _abi.STATUS_NAMES[_run(width=(1 << 27) - 16, stride=1 << 27)] == "TA_ERR_UNSUPPORTED"
+
+
 def test_workspace_of_nothing():
     f, n = _abi.load_library().tree_attn_chunk_workspace, ctypes.c_size_t(0)
     assert f(0, 0, 8, 2, 128, ctypes.byref(n)) == _abi.TA_OK and n.value == 0

@@ -68,8 +68,9 @@ tree_attn_status tree_attn_chunk_run(const void* q, int64_t q_stride, const void
       return fail(TA_ERR_UNSUPPORTED, "queries and pages must be bf16 or fp16");
     if (table_width < 0 || (n_requests > 1 && table_stride < table_width))
       return fail(TA_ERR_INVALID_ARG, "table_width is negative or table_stride below it");
-    if ((int64_t)table_width * ta::kPage > INT32_MAX || (uint32_t)num_pages > ta::kMaxPages)
-      return fail(TA_ERR_UNSUPPORTED, "rows of 2^31 tokens or more, or num_pages out of range");
+    // (the keys of a request's last step and its pages, a step more at most, are counted in 32 bits)
+    if ((int64_t)table_width * ta::kPage > INT32_MAX - 256 || (uint32_t)num_pages > ta::kMaxPages)
+      return fail(TA_ERR_UNSUPPORTED, "rows of 2^31 - 256 tokens or more, or num_pages out of range");
     if (!cu_new && n_tokens != n_requests)
       return fail(TA_ERR_INVALID_ARG, "without cu_new there is one query a request: n_tokens must be n_requests");
     // an SM's share of the steps is counted in 32 bits
