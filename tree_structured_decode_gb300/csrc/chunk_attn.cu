@@ -39,10 +39,11 @@
 // TFLOP/s, 0.74 of the measured bf16 peak and 0.84 of what it sustains.  A pair of
 // tasks takes about 2900 cycles where its products take 2048: S, softmax and P V of
 // one half follow one another, and two halves cover each other only in part (P
-// handed over in two parts: 3200 us; two threads a row: 3560).  26 drafts behind
-// 500 to 4000 tokens (64 requests, 32 heads on 8, 458 MB) in 110 us: 4.1 TB/s in
-// all, about 6 while K and V stream; the rest is the start, runs that do not end
-// together, and the merge.
+// handed over in two parts: 3200 us; two threads a row: 3560).  What takes the
+// softmax a few registers more spills its scores (finished rows by TMA through shared
+// memory: 4500).  26 drafts behind 500 to 4000 tokens (64 requests, 32 heads on 8,
+// 458 MB) in 107 us: 4.3 TB/s in all, about 6 while K and V stream; the rest is the
+// start, runs that do not end together, and the merge.
 //
 // Every wait has a limit.  One that runs out sets the status word's timeout bit
 // and the CTA's abort flag; every role then stops issuing, waits (with a limit)
@@ -299,7 +300,9 @@ struct Cfg {
   static constexpr int kHalves = D / 64;
   static constexpr int kQBytes = 128 * D * 2;               // one tile of queries
   static constexpr int kStageBytes = kTileTokens * D * 2;   // K or V of a step
-  static constexpr int kStages = D == 128 ? 5 : 10;         // K and V take turns
+  // K and V take turns.  (A fifth stage, 10 at d = 64: 110 us against 106 for 64 trees of
+  // drafts, 157 against 159 for 24 packed prompts, else the same.)
+  static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kHead = kPage * D * 2;               // a page-head
   static constexpr int kOffStage = 2 * kQBytes;
   static constexpr int kOffMl = kOffStage + kStages * kStageBytes;  // {m, l} of both tiles' rows
