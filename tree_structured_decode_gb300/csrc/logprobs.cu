@@ -424,12 +424,13 @@ cudaError_t pick(const ScoreParams& p, cudaStream_t s) {
   // with 8 172 (174); 272 rows of 28510, all at once either way, 18 (13).  (64 threads:
   // 1664 rows 56, but 900 46 and with 64 alternatives 161.)
   if (bytes <= 8192 || p.rows > 4 * p.num_sms) return run<T, 128>(p, top, 1, s);
-  // Few rows are split until every SM has two parts or the parts are short: one row of
-  // 32000 fp32 takes 6.3 us in eight (whole 11.1), 100 of 50257 bf16 13.4 in two (whole
-  // 14.7, in four 11.8), 150 of 128000 fp32 22.6 in two (in four 28.5), 250 of 50257 bf16
-  // 16.7 whole (in two 17.3).
+  // Few rows are split while that leaves at most three parts an SM and the parts are
+  // long: one row of 32000 fp32 takes 6.3 us in eight (whole 11.1), 100 of 50257 bf16
+  // 11.9 in four (in two 13.3, whole 14.7), 225 of 128000 fp32 27.8 in two (whole 35.8);
+  // with more parts, 150 of 128000 fp32 28.5 in four (in two 22.6), 250 of 50257 bf16
+  // 17.3 in two (whole 16.7).
   int ranks = 1;
-  while (ranks < kMaxCluster && (long long)p.rows * ranks * 2 <= 2 * p.num_sms && bytes / ranks > 16384) ranks *= 2;
+  while (ranks < kMaxCluster && (long long)p.rows * ranks * 2 <= 3 * p.num_sms && bytes / ranks > 16384) ranks *= 2;
   return run<T, 256>(p, top, ranks, s);
 }
 
