@@ -256,6 +256,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) scores_kernel(const
   const uint64_t c2 = ptx::f2(c, c);
   uint4 ahead[kVectors];
   load(v0, ahead);
+  // (shared memory of another CTA may be written once that CTA has started: waited
+  // for where the row's sums go to the first one, so that it costs no time here)
+  if (ranks > 1) ptx::cluster_arrive();
   for (int at = v0; at < v1; at += kRound) {
     float x[kGroup];
 #pragma unroll
@@ -331,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) scores_kernel(const
   sum = joined_warp(sum, c);
   if (lane == 0) s_sums[warp] = sum;
   __syncthreads();
+  if (ranks > 1) ptx::cluster_wait();
   if (warp == 0) {
     Sums x = lane < kWarps ? s_sums[lane] : Sums{kLowest, 0.f, 0.f};
     x = joined_warp(x, c);
