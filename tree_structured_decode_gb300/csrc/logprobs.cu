@@ -127,7 +127,9 @@ struct List {
     int n;
   } noted;
   u64 key[kRoom];
-  u64 threshold;  // keys up to it are left out; 0: fewer than k are known
+  // Keys up to it are left out: one less than a key that k are known to reach, so that
+  // the logit of (threshold + 1) is that key's, whatever its index.  0: fewer are known.
+  u64 threshold;
   int n;
 };
 
@@ -183,7 +185,8 @@ __device__ __forceinline__ void add_noted(List<kThreads, kGroup>& s, int k) {
     select_largest<kThreads>(s.key, have, s.noted.best, k);
     __syncthreads();
     for (int i = tid; i < k; i += kThreads) s.key[i] = s.noted.best[i];
-    if (tid == 0) s.n = k, s.threshold = s.noted.best[k - 1];
+    // (the k-th itself does not come again)
+    if (tid == 0) s.n = k, s.threshold = s.noted.best[k - 1] - 1;
   }
   if (tid == 0) s.noted.n = 0;
   __syncthreads();
