@@ -603,7 +603,8 @@ tree_attn_status tree_attn_keep_drafts(const int32_t* path, const int32_t* cu_ne
  *   - A row with a NaN, or with nothing above -inf, gives NaN, and tokens -1.
  *     +inf shares the row among its like.
  *   - temperature not above 0: the largest logit (the first of equal ones) has
- *     probability 1.
+ *     probability 1.  +inf: all logits above -inf have the same.
+ *   - l_j - max is taken in 32 bits: what falls below their range is -inf.
  * Errors: TA_ERR_INVALID_ARG, TA_ERR_ALIGNMENT, TA_ERR_UNSUPPORTED (vocab above
  * TREE_ATTN_MAX_VOCAB, top above TREE_ATTN_TOP_MAX), TA_ERR_CUDA. */
 #define TREE_ATTN_TOP_MAX 64

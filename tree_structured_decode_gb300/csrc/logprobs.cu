@@ -208,8 +208,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) scores_kernel(const
   const float heat = p.temperature ? p.temperature[r] : p.temperature_all;
   const bool greedy = !(heat > 0.f);
   const float inv = greedy ? 1.f : 1.f / heat;
-  // (finite, and not 0: -inf stays below everything)
-  const float c = fminf(fmaxf(inv * kLog2e, 1.17549435e-38f), kLargest);
+  // (finite, and not 0: -inf stays below everything; the least there is, so that a
+  // temperature of +inf weighs all other logits alike)
+  const float c = fminf(fmaxf(inv * kLog2e, 1.40129846e-45f), kLargest);
   const int k = kTop ? (greedy ? max(p.top, 1) : p.top) : 0;
 
   // the row as 16-byte vectors; `shift` elements of the first lie before it
@@ -387,7 +388,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) scores_kernel(const
   const auto logprob = [&](float x, int i) {
     if (broken) return NAN;
     if (greedy) return i == first ? 0.f : -INFINITY;
-    return (x == all.m ? 0.f : (x - all.m) * inv) - log_s;
+    const float y = x - all.m;
+    return (x == all.m ? 0.f : y > -INFINITY ? y * inv : -INFINITY) - log_s;  // (inv may be 0)
   };
   if (tid == 0 && p.entropy) p.entropy[r] = broken ? NAN : greedy ? 0.f : fmaf(all.h / all.s, kLn2, log_s);
   for (int g = tid; g < p.n_given; g += kThreads) {
