@@ -559,7 +559,8 @@ tree_attn_status tree_attn_chunk_workspace(int32_t n_requests, int32_t n_tokens,
  * A request of more than TREE_ATTN_NODES_MAX nodes keeps none; with offsets that
  * fall or leave the tokens no request has nodes; both, and a parent that is not
  * below its node (which counts as -1), set the status word.
- * Errors: TA_ERR_INVALID_ARG, TA_ERR_ALIGNMENT, TA_ERR_UNSUPPORTED, TA_ERR_CUDA. */
+ * Errors: TA_ERR_INVALID_ARG, TA_ERR_ALIGNMENT, TA_ERR_UNSUPPORTED (2^30 nodes or
+ * more in all), TA_ERR_CUDA. */
 tree_attn_status tree_attn_accept_drafts(const int32_t* drafted, const int32_t* parents,
                                          const int32_t* cu_new, const int32_t* sampled,
                                          int32_t n_requests, int32_t n_tokens, int32_t* path,
@@ -576,7 +577,7 @@ tree_attn_status tree_attn_accept_drafts(const int32_t* drafted, const int32_t* 
  * Only the positions that a kept node moves to are written.  A path that does not
  * rise, and positions or pages out of range, end the request's moves there and
  * set the status word.  Errors: TA_ERR_INVALID_ARG, TA_ERR_ALIGNMENT,
- * TA_ERR_UNSUPPORTED, TA_ERR_CUDA. */
+ * TA_ERR_UNSUPPORTED (as above), TA_ERR_CUDA. */
 tree_attn_status tree_attn_keep_drafts(const int32_t* path, const int32_t* cu_new,
                                        const int32_t* lens, const int32_t* block_table,
                                        int64_t table_stride, int32_t table_width,
@@ -606,7 +607,8 @@ tree_attn_status tree_attn_keep_drafts(const int32_t* path, const int32_t* cu_ne
  *     probability 1.  +inf: all logits above -inf have the same.
  *   - l_j - max is taken in 32 bits: what falls below their range is -inf.
  * Errors: TA_ERR_INVALID_ARG, TA_ERR_ALIGNMENT, TA_ERR_UNSUPPORTED (vocab above
- * TREE_ATTN_MAX_VOCAB, top above TREE_ATTN_TOP_MAX), TA_ERR_CUDA. */
+ * TREE_ATTN_MAX_VOCAB, top above TREE_ATTN_TOP_MAX, 2^28 rows or 2^30 given
+ * tokens a row or more), TA_ERR_CUDA. */
 #define TREE_ATTN_TOP_MAX 64
 tree_attn_status tree_attn_token_logprobs(const void* logits, int64_t stride, int32_t dtype,
                                           int32_t n_rows, int32_t vocab, const int32_t* given,

@@ -25,6 +25,9 @@ tree_attn_status too_many_requests() {
   return fail(TA_ERR_UNSUPPORTED, "more than " + std::to_string(TREE_ATTN_MAX_REQUESTS) + " requests");
 }
 
+// (the kernels step through what they count in 32 bits)
+bool uncountable(int32_t n) { return n > INT32_MAX / 2; }
+
 // The sizes that decide the workspace of a chunk run.
 tree_attn_status chunk_sizes(int32_t n_requests, int32_t n_tokens, int32_t n_q_heads,
                              int32_t n_kv_heads, int32_t head_dim, ta::ChunkParams* p) {
@@ -138,6 +141,7 @@ tree_attn_status tree_attn_accept_drafts(const int32_t* drafted, const int32_t* 
   return guarded([&]() -> tree_attn_status {
     if (n_requests < 0 || n_tokens < 0) return fail(TA_ERR_INVALID_ARG, "a count is negative");
     if (n_requests > TREE_ATTN_MAX_REQUESTS) return too_many_requests();
+    if (uncountable(n_tokens)) return fail(TA_ERR_UNSUPPORTED, "2^30 nodes or more");
     if (!cu_new && n_tokens != n_requests)
       return fail(TA_ERR_INVALID_ARG, "without cu_new there is one node a request: n_tokens must be n_requests");
     if ((n_requests > 0 && (!n_kept || !next_tokens)) ||
@@ -176,6 +180,7 @@ tree_attn_status tree_attn_keep_drafts(const int32_t* path, const int32_t* cu_ne
     if (n_kv_heads > 4096 || (uint32_t)num_pages > ta::kMaxPages || n_layers > 65535)
       return fail(TA_ERR_UNSUPPORTED, "more than 4096 kv heads, 65535 layers or 2^27 pages");
     if (n_requests > TREE_ATTN_MAX_REQUESTS) return too_many_requests();
+    if (uncountable(n_tokens)) return fail(TA_ERR_UNSUPPORTED, "2^30 nodes or more");
     if ((int64_t)table_width * ta::kPage > INT32_MAX)
       return fail(TA_ERR_UNSUPPORTED, "rows of 2^31 tokens or more");
     if (!cu_new && n_tokens != n_requests)
@@ -230,6 +235,7 @@ tree_attn_status tree_attn_token_logprobs(const void* logits, int64_t stride, in
     if (top > TREE_ATTN_TOP_MAX)
       return fail(TA_ERR_UNSUPPORTED, "top is above " + std::to_string(TREE_ATTN_TOP_MAX));
     if (n_rows > INT32_MAX / 8) return fail(TA_ERR_UNSUPPORTED, "2^28 rows or more");
+    if (uncountable(n_given)) return fail(TA_ERR_UNSUPPORTED, "2^30 given tokens a row or more");
     if (n_rows == 0) return TA_OK;
     if (!logits || (n_given > 0 && (!given || !given_logprobs)) || (top > 0 && (!top_tokens || !top_logprobs)))
       return fail(TA_ERR_INVALID_ARG, "logits, and what is asked for, must be non-NULL");
