@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kKeepThreads) keep_drafts_kernel(const KeepPar
   const int b = blockIdx.x, tid = threadIdx.x;
   const Nodes r = nodes_of(p.cu, b, p.n_tokens);
   const int len = p.lens[b];
-  const int base = len - r.n;
+  const long long base = (long long)len - r.n;  // (any 32 bits may stand in lens)
   if (tid == 0 && !r.ok && p.status) atomicOr(p.status, kBatchBadInput);
   const int chunks = p.d / 8, pieces = p.hkv * chunks;
   uint16_t* const k = p.k_pages + (long long)blockIdx.y * p.layer_stride;
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kKeepThreads) keep_drafts_kernel(const KeepPar
         const int from = i < r.n ? p.path[r.tok0 + i] : -1;
         const int prev = i < r.n && i > 0 ? p.path[r.tok0 + i - 1] : -1;
         const bool ends = from == -1;
-        const long long at = (long long)base + from, to = (long long)base + i;
+        const long long at = base + from, to = base + i;
         bool fine = from >= 0 && from > prev && from < r.n && base >= 0 && len <= (long long)p.width * kPage;
         long long source = 0, target = 0;
         if (fine && from != i) {
