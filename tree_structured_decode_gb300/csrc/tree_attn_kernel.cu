@@ -824,6 +824,12 @@ __device__ __forceinline__ void write_row_cols(const AttnParams& p, const UnitDe
   if (gt.pbase < 0) {
     float* dst = p.out + ((size_t)gt.tok * p.hq + h) * D;
     if (with_lse && p.lse) p.lse[(size_t)gt.tok * p.hq + h] = lse2 * kLn2;
+    if (reinterpret_cast<uintptr_t>(p.out) & 16) {  // rows are whole sectors, half a sector off
+#pragma unroll
+      for (int c = 0; c < N; c += 4)
+        *reinterpret_cast<float4*>(dst + c0 + c) = make_float4(o[c] * inv, o[c + 1] * inv, o[c + 2] * inv, o[c + 3] * inv);
+      return;
+    }
     // 32-byte stores: one per sector
 #pragma unroll
     for (int c = 0; c < N; c += 8)
