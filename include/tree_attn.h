@@ -495,6 +495,10 @@ tree_attn_status tree_attn_sample(const void* logits, int64_t stride, int32_t dt
  *   tree_attn_accept_drafts()   the path that agrees with them
  *   tree_attn_keep_drafts()     its keys and values moved together
  *   tree_attn_extend_tables()   the other nodes taken back
+ * The positions that tree_attn_extend_tables() gives count a request's tokens
+ * one behind another.  A node's place in the text is lens[b] - n plus the number
+ * of nodes above it: where keys are rotated by their position, that is the one to
+ * use, and a node that is kept then moves with the right one.
  * ------------------------------------------------------------------------ */
 
 /* Most nodes of a request's tree in a step. */
